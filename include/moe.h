@@ -341,6 +341,111 @@ MOE_API moe_status moe_quantize_weights_mxfp8(const moe_config* cfg, const moe_w
 MOE_API moe_status moe_quantize_weights_mxfp4(const moe_config* cfg, const moe_weights* w,
                                               const moe_weights_mx4* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Building blocks: the layer's data movements and products as calls of their
+ * own, for callers whose experts are not the layer's bias-free SwiGLU, who
+ * exchange rows between ranks between dispatch and experts, or who project in
+ * front of or behind the layer.  A layer of such experts is
+ *   moe_schedule, moe_permute_forward,
+ *   moe_linear_forward (grouped, bias, activation), moe_linear_forward,
+ *   moe_unpermute_forward (router weights, residual)
+ * and backward the same calls' gradients in reverse.
+ * ------------------------------------------------------------------------ */
+typedef enum moe_dtype {
+    MOE_DT_BF16 = 0,
+    MOE_DT_FP16 = 1,
+    MOE_DT_FP32 = 2      /* permute and unpermute only */
+} moe_dtype;
+
+/* Rows to experts ([AREX] first decision; [ALPHA] 一: dispatch).
+ *   x [T, H], xs [S, H] of `dtype` (xs written): xs[row_of_slot[t*k+j]] = x[t].
+ *   Of cfg only T, H, E and k matter, of sched only row_of_slot; rows are those
+ *   of the whole batch (macrobatch m's are [m*M*k, (m+1)*M*k)).
+ *   workspace: the layer's, or any 256 zeroed bytes (256-byte aligned): only the
+ *   device error word, its first 4 bytes, is used.  A row outside [0, S) is
+ *   skipped and sets MOE_DEVERR_BAD_ROW; rows that no slot names are left as
+ *   they were. */
+MOE_API moe_status moe_permute_forward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
+                                       const void* x, void* xs, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Its gradient: dx[t] = sum_{j=0..k-1} dxs[row_of_slot[t*k+j]], summed in fp32
+ * in that order, rounded once.  dxs [S, H], dx [T, H] (written). */
+MOE_API moe_status moe_permute_backward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
+                                        const void* dxs, void* dx, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Expert rows back to tokens ([ALPHA] 二: the router-weighted reduction).
+ *   y[t] = sum_{j=0..k-1} topk_w[t,j] * o[row_of_slot[t*k+j]] + residual[t],
+ *   summed in fp32 in that order, rounded once.  o [S, H], residual [T, H] (may
+ *   be NULL; may be y itself), y [T, H] (written).  Reads sched's row_of_slot and
+ *   topk_w; workspace as in moe_permute_forward. */
+MOE_API moe_status moe_unpermute_forward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
+                                         const void* o, const void* residual, void* y, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* Its gradients (the residual's is dy itself):
+ *   d_o [S, H] of `dtype` (written): d_o[row(t,j)] = topk_w[t,j] * dy[t];
+ *   dw [T, k] fp32 (written): <o[row(t,j)], dy[t]>;
+ *   d_logits [T, E] fp32 (written; may be NULL): through the softmax over the
+ *   chosen logits, zero for experts a token did not choose.
+ * d_o must not overlap o.  Reads sched's row_of_slot, topk_w and (for d_logits)
+ * topk_idx; workspace as in moe_permute_forward. */
+MOE_API moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
+                                          const void* o, const void* dy, void* d_o, float* dw, float* d_logits,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_GELU = 2,        /* z Phi(z), by erf                                      */
+    MOE_ACT_GELU_TANH = 3,   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))         */
+    MOE_ACT_SILU = 4         /* z sigmoid(z)                                          */
+} moe_act;
+
+typedef struct moe_linear_config {
+    int32_t M;             /* rows, 1..2^24                                            */
+    int32_t N;             /* outputs, a multiple of 8, 8..65536                       */
+    int32_t K;             /* inputs, a multiple of 8, 8..65536                        */
+    int32_t E;             /* 0: one dense product; 1..1024: a product per expert      */
+    int32_t dtype;         /* MOE_DT_BF16 or MOE_DT_FP16: every tensor's type          */
+    int32_t act;           /* moe_act                                                  */
+    int32_t flags;         /* 0                                                        */
+} moe_linear_config;
+
+/* Host-only: bytes of workspace moe_linear_forward and moe_linear_backward
+ * need.  One workspace serves both and any number of calls on one stream;
+ * calls that overlap need one each.  Zero its first 256 bytes once (the sticky
+ * device error word of moe_check_device_error). */
+MOE_API moe_status moe_linear_workspace_size(const moe_linear_config* cfg, size_t* bytes);
+
+/* y = act(z) + residual, z = x w^T + bias.
+ *   x [M, K], w [N, K] (E > 0: [E, N, K]), bias [N] (or [E, N]; may be NULL),
+ *   residual [M, N] (may be NULL; may be y itself), y [M, N] (written),
+ *   z [M, N] (written for the backward; may be NULL), all of cfg->dtype.
+ *   offsets: NULL if E is 0, else device int32 [E+1] ascending (one macrobatch's
+ *   moe_sched.offsets): rows offsets[e] .. offsets[e+1] take expert e's weights.
+ *   Rows in no group are neither read nor written.  A group that is not inside
+ *   [0, M] or not ascending is skipped and sets MOE_DEVERR_BAD_OFFSETS.
+ *   fp32 accumulation; the sum, bias, activation and residual in fp32, y and z
+ *   rounded once each.  Apart from residual = y, outputs overlap no input. */
+MOE_API moe_status moe_linear_forward(const moe_linear_config* cfg, const int32_t* offsets, const void* x,
+                                      const void* w, const void* bias, const void* residual, void* y, void* z,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients asked for (dx, dw, db: NULL = not wanted, but not all three;
+ * the residual's is dy itself):
+ *   dz = dy * act'(z);  dx [M, K] = dz w;  dw (w's shape) = dz^T x over each
+ *   group's rows;  db (bias's shape) = the sum of dz over them.
+ *   z: as moe_linear_forward wrote it (not read if act is MOE_ACT_NONE); x is
+ *   read for dw, w for dx (else they may be NULL).
+ *   dz is rounded to cfg->dtype once as the products' operand (db sums it
+ *   unrounded); outputs are overwritten.  A group without rows gets dw = 0 and
+ *   db = 0; rows of dx in no group are left as they were. */
+MOE_API moe_status moe_linear_backward(const moe_linear_config* cfg, const int32_t* offsets, const void* x,
+                                       const void* w, const void* z, const void* dy, void* dx, void* dw, void* db,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads and clears the sticky device error word that kernels set when a
  * caller-built schedule holds an out-of-range expert, slot or row (those
  * entries are skipped, never dereferenced), or when more routed experts take

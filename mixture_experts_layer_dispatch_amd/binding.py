@@ -34,6 +34,8 @@ EXPORTED = [
     "moe_check_device_error", "moe_quantize_weights_mxfp8", "moe_profile_enable", "moe_profile_collect", "moe_profile_query",
     "moe_profile_names", "moe_profile_reset", "moe_workspace_region", "moe_schedule_noalloc",
     "moe_router_forward", "moe_router_backward", "moe_quantize_weights_mxfp4",
+    "moe_permute_forward", "moe_permute_backward", "moe_unpermute_forward", "moe_unpermute_backward",
+    "moe_linear_workspace_size", "moe_linear_forward", "moe_linear_backward",
 ]
 
 FLAG_RECOMPUTE = 1
@@ -51,6 +53,10 @@ class moe_config(ctypes.Structure):
                 ("macrobatch", ctypes.c_int32), ("minibatch", ctypes.c_int32),
                 ("capacity_rows", ctypes.c_int64), ("precision", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("acc_experts", ctypes.c_int32)]
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "E", "dtype", "act", "flags")]
 
 
 class moe_sched(ctypes.Structure):
@@ -132,6 +138,14 @@ def lib() -> ctypes.CDLL:
         L.moe_profile_reset.argtypes = []
         L.moe_workspace_region.argtypes = [cfgp, ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t),
                                            ctypes.POINTER(ctypes.c_size_t)]
+        sp, sz, lcp = ctypes.POINTER(moe_sched), ctypes.c_size_t, ctypes.POINTER(moe_linear_config)
+        L.moe_permute_forward.argtypes = [cfgp, sp, ctypes.c_int, vp, vp, vp, sz, vp]
+        L.moe_permute_backward.argtypes = [cfgp, sp, ctypes.c_int, vp, vp, vp, sz, vp]
+        L.moe_unpermute_forward.argtypes = [cfgp, sp, ctypes.c_int, vp, vp, vp, vp, sz, vp]
+        L.moe_unpermute_backward.argtypes = [cfgp, sp, ctypes.c_int, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_workspace_size.argtypes = [lcp, ctypes.POINTER(sz)]
+        L.moe_linear_forward.argtypes = [lcp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_backward.argtypes = [lcp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         for name in EXPORTED:
             if name != "moe_status_string":
                 getattr(L, name).restype = ctypes.c_int
@@ -536,6 +550,208 @@ def moe_quantize_weights_mxfp8(cfg: Config, weights: dict, out: dict, stream=Non
     _check(lib().moe_quantize_weights_mxfp8(ctypes.byref(cfg.c()), ctypes.byref(wst),
                                             ctypes.byref(mx), _stream(stream)),
            "moe_quantize_weights_mxfp8")
+
+
+# ------------------------------------------------------------------ building blocks
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+@dataclass(frozen=True)
+class LinearConfig:
+    """moe_linear_config: M rows, N outputs, K inputs; E = 0 for one dense
+    product, else a product per expert over the groups of `offsets`."""
+    M: int
+    N: int
+    K: int
+    E: int = 0
+    dtype: torch.dtype = torch.bfloat16
+    act: str = "none"
+
+    def c(self) -> moe_linear_config:
+        if self.act not in ACTS:
+            raise ValueError(f"act: {self.act!r}, expected one of {', '.join(ACTS)}")
+        if self.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype: {self.dtype}, expected torch.bfloat16 or torch.float16")
+        return moe_linear_config(self.M, self.N, self.K, self.E, DTYPES[self.dtype], ACTS[self.act], 0)
+
+
+def linear_workspace_size(lc: LinearConfig) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().moe_linear_workspace_size(ctypes.byref(lc.c()), ctypes.byref(v)), "moe_linear_workspace_size")
+    return v.value
+
+
+def alloc_linear_workspace(lc: LinearConfig, device="cuda") -> torch.Tensor:
+    """Workspace of moe_linear_forward / moe_linear_backward, its device error word cleared."""
+    ws = torch.empty(linear_workspace_size(lc), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def alloc_error_word(device="cuda") -> torch.Tensor:
+    """256 zeroed bytes: all of a workspace that the permute / unpermute calls use."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _check_tensors(specs):
+    """_validate for the building blocks: tensors (name, tensor, shape, dtype;
+    a None tensor is an optional one that was not given), which have to be
+    on the current device, where the call's work is enqueued."""
+    for name, t, shape, dtype in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    here = None
+    for name, t, _, _ in specs:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be on the GPU, found on {t.device}")
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.get_device() != here:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
+
+
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name}: missing")
+
+
+def _rows_checks(cfg: Config, sched: dict, ws, first: str, data, names):
+    """Checks what every permute / unpermute call takes; returns the tensors' dtype code."""
+    if not isinstance(data, torch.Tensor) or data.dtype not in DTYPES:
+        raise ValueError(f"{first}: expected a bf16, fp16 or fp32 tensor")
+    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
+    if 0 <= n < 256:
+        raise ValueError(f"workspace: {n} bytes, at least 256 are needed")
+    i32 = torch.int32
+    want = {"row_of_slot": ((cfg.S,), i32), "topk_w": ((cfg.T, cfg.k), torch.float32), "topk_idx": ((cfg.T, cfg.k), i32)}
+    for name in names:
+        if sched.get(name) is None:
+            raise ValueError(f"sched[{name!r}]: missing")
+    _required(workspace=ws)
+    return DTYPES[data.dtype], [("workspace", ws, (n,), torch.uint8)] + [
+        (f"sched[{name!r}]", sched[name], *want[name]) for name in names]
+
+
+def _some_sched(sched: dict, names) -> moe_sched:
+    st = moe_sched()
+    for name in names:
+        setattr(st, name, sched[name].data_ptr())
+    return st
+
+
+def moe_permute_forward(cfg: Config, sched: dict, x: torch.Tensor, xs: torch.Tensor, ws: torch.Tensor, stream=None):
+    """xs[row_of_slot[t, j]] = x[t]: token rows [T, H] to their experts' rows [S, H] (bf16, fp16 or fp32)."""
+    _required(x=x, xs=xs)
+    names = ("row_of_slot",)
+    dt, specs = _rows_checks(cfg, sched, ws, "x", x, names)
+    _check_tensors(specs + [("x", x, (cfg.T, cfg.H), x.dtype), ("xs", xs, (cfg.S, cfg.H), x.dtype)])
+    _check(lib().moe_permute_forward(cfg.c(), _some_sched(sched, names), dt, x.data_ptr(), xs.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), _stream(stream)), "moe_permute_forward")
+
+
+def moe_permute_backward(cfg: Config, sched: dict, dxs: torch.Tensor, dx: torch.Tensor, ws: torch.Tensor, stream=None):
+    """dx[t] = sum_j dxs[row_of_slot[t, j]]."""
+    _required(dxs=dxs, dx=dx)
+    names = ("row_of_slot",)
+    dt, specs = _rows_checks(cfg, sched, ws, "dxs", dxs, names)
+    _check_tensors(specs + [("dxs", dxs, (cfg.S, cfg.H), dxs.dtype), ("dx", dx, (cfg.T, cfg.H), dxs.dtype)])
+    _check(lib().moe_permute_backward(cfg.c(), _some_sched(sched, names), dt, dxs.data_ptr(), dx.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), _stream(stream)), "moe_permute_backward")
+
+
+def moe_unpermute_forward(cfg: Config, sched: dict, o: torch.Tensor, y: torch.Tensor, ws: torch.Tensor, residual=None,
+                          stream=None):
+    """y[t] = sum_j topk_w[t, j] o[row_of_slot[t, j]] (+ residual[t], which may be y itself)."""
+    _required(o=o, y=y)
+    names = ("row_of_slot", "topk_w")
+    dt, specs = _rows_checks(cfg, sched, ws, "o", o, names)
+    _check_tensors(specs + [("o", o, (cfg.S, cfg.H), o.dtype), ("y", y, (cfg.T, cfg.H), o.dtype),
+                            ("residual", residual, (cfg.T, cfg.H), o.dtype)])
+    _check(lib().moe_unpermute_forward(cfg.c(), _some_sched(sched, names), dt, o.data_ptr(), _ptr(residual),
+                                       y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+           "moe_unpermute_forward")
+
+
+def moe_unpermute_backward(cfg: Config, sched: dict, o: torch.Tensor, dy: torch.Tensor, do: torch.Tensor,
+                           dw: torch.Tensor, ws: torch.Tensor, d_logits=None, stream=None):
+    """do[row(t, j)] = topk_w[t, j] dy[t]; dw[t, j] = <o[row(t, j)], dy[t]>; d_logits [T, E] through the
+    softmax over the chosen logits.  The residual's gradient is dy itself."""
+    _required(o=o, dy=dy, do=do, dw=dw)
+    names = ("row_of_slot", "topk_w") if d_logits is None else ("row_of_slot", "topk_w", "topk_idx")
+    dt, specs = _rows_checks(cfg, sched, ws, "o", o, names)
+    f32_ = torch.float32
+    _check_tensors(specs + [("o", o, (cfg.S, cfg.H), o.dtype), ("dy", dy, (cfg.T, cfg.H), o.dtype),
+                            ("do", do, (cfg.S, cfg.H), o.dtype), ("dw", dw, (cfg.T, cfg.k), f32_),
+                            ("d_logits", d_logits, (cfg.T, cfg.E), f32_)])
+    _check(lib().moe_unpermute_backward(cfg.c(), _some_sched(sched, names), dt, o.data_ptr(), dy.data_ptr(),
+                                        do.data_ptr(), dw.data_ptr(), _ptr(d_logits), ws.data_ptr(), ws.numel(),
+                                        _stream(stream)), "moe_unpermute_backward")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _linear_checks(lc: LinearConfig, ws, offsets):
+    """(moe_linear_config, specs of the workspace and offsets, leading shape of w and bias)."""
+    c = lc.c()
+    need = linear_workspace_size(lc)
+    _required(workspace=ws)
+    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
+    if 0 <= n < need:
+        raise ValueError(f"workspace: {n} bytes, the config needs {need}")
+    if (offsets is None) != (lc.E == 0):
+        raise ValueError("offsets: given if and only if E > 0")
+    return c, [("workspace", ws, (n,), torch.uint8), ("offsets", offsets, (lc.E + 1,), torch.int32)], \
+        ((lc.E,) if lc.E else ())
+
+
+def moe_linear_forward(lc: LinearConfig, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, ws: torch.Tensor,
+                       bias=None, residual=None, z=None, offsets=None, stream=None):
+    """y = act(x w^T + bias) + residual; z, if given, keeps x w^T + bias for the backward.  With E > 0
+    rows offsets[e] .. offsets[e + 1] take w[e], bias[e].  residual may be y itself."""
+    _required(x=x, w=w, y=y)
+    c, specs, lead = _linear_checks(lc, ws, offsets)
+    dt, mn = lc.dtype, (lc.M, lc.N)
+    _check_tensors(specs + [("x", x, (lc.M, lc.K), dt), ("w", w, (*lead, lc.N, lc.K), dt), ("y", y, mn, dt),
+                            ("bias", bias, (*lead, lc.N), dt), ("residual", residual, mn, dt), ("z", z, mn, dt)])
+    _check(lib().moe_linear_forward(c, _ptr(offsets), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
+                                    y.data_ptr(), _ptr(z), ws.data_ptr(), ws.numel(), _stream(stream)),
+           "moe_linear_forward")
+
+
+def moe_linear_backward(lc: LinearConfig, x, w, z, dy: torch.Tensor, ws: torch.Tensor, dx=None, dw=None, db=None,
+                        offsets=None, stream=None):
+    """The gradients whose output is given: dx = dz w, dw = dz^T x, db = sum of dz, with dz = dy act'(z)
+    (z as moe_linear_forward kept it; not read if act is "none").  x is needed for dw, w for dx.  The
+    residual's gradient is dy itself."""
+    _required(dy=dy)
+    if lc.act != "none":
+        _required(z=z)
+    if dx is not None:
+        _required(w=w)
+    if dw is not None:
+        _required(x=x)
+    if dx is None and dw is None and db is None:
+        raise ValueError("dx, dw, db: at least one is needed")
+    c, specs, lead = _linear_checks(lc, ws, offsets)
+    dt, mn, mk, nk = lc.dtype, (lc.M, lc.N), (lc.M, lc.K), (*lead, lc.N, lc.K)
+    _check_tensors(specs + [("x", x, mk, dt), ("w", w, nk, dt), ("z", z, mn, dt), ("dy", dy, mn, dt),
+                            ("dx", dx, mk, dt), ("dw", dw, nk, dt), ("db", db, (*lead, lc.N), dt)])
+    _check(lib().moe_linear_backward(c, _ptr(offsets), _ptr(x), _ptr(w), _ptr(z), dy.data_ptr(), _ptr(dx), _ptr(dw),
+                                     _ptr(db), ws.data_ptr(), ws.numel(), _stream(stream)), "moe_linear_backward")
 
 
 # device error bits (moe_check_device_error)

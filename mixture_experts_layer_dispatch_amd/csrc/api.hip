@@ -218,7 +218,9 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 std::atomic<int> g_dev_ok[64];   // 0 unknown, 1 gfx950, 2 other
 
-bool device_ok() {
+}  // namespace
+
+bool moe::device_ok() {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
         (void)hipGetLastError();
@@ -237,6 +239,8 @@ bool device_ok() {
     if (dev < 64) g_dev_ok[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
     return ok;
 }
+
+namespace {
 
 __global__ void k_clear_word(int32_t* p) { *p = 0; }
 __global__ void k_clear_words(int32_t* p) { p[threadIdx.x] = 0; }

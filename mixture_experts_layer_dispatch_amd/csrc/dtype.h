@@ -1,0 +1,65 @@
+// Element types of the building-block operators: how 16 bytes of a type turn
+// into fp32 values and back (each value rounded once, to nearest even), and
+// for the 16-bit types the MFMA that multiplies them.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+struct Bf16 {
+    static constexpr int PER16 = 8;
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) { return pack_bf2(a, b); }
+    static __device__ __forceinline__ float lo(uint32_t v) { return lo_bf(v); }
+    static __device__ __forceinline__ float hi(uint32_t v) { return hi_bf(v); }
+    static __device__ __forceinline__ f32x4 mfma(const uint4& a, const uint4& b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+        f[0] = lo(v.x); f[1] = hi(v.x); f[2] = lo(v.y); f[3] = hi(v.y);
+        f[4] = lo(v.z); f[5] = hi(v.z); f[6] = lo(v.w); f[7] = hi(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    }
+};
+
+struct Fp16 {
+    static constexpr int PER16 = 8;
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+        f16x2 h;
+        h[0] = (_Float16)a;
+        h[1] = (_Float16)b;
+        return __builtin_bit_cast(uint32_t, h);
+    }
+    static __device__ __forceinline__ float lo(uint32_t v) { return (float)__builtin_bit_cast(f16x2, v)[0]; }
+    static __device__ __forceinline__ float hi(uint32_t v) { return (float)__builtin_bit_cast(f16x2, v)[1]; }
+    static __device__ __forceinline__ f32x4 mfma(const uint4& a, const uint4& b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
+                                                      0, 0, 0);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+        f[0] = lo(v.x); f[1] = hi(v.x); f[2] = lo(v.y); f[3] = hi(v.y);
+        f[4] = lo(v.z); f[5] = hi(v.z); f[6] = lo(v.w); f[7] = hi(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    }
+};
+
+struct Fp32 {
+    static constexpr int PER16 = 4;
+    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
+}  // namespace moe

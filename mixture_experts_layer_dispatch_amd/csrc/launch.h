@@ -367,6 +367,76 @@ int launch_router_logits(const void* x, const void* wr, float* logits, int T, in
 int launch_router_backward(const void* x, const void* wr, const float* d_logits, void* dx, void* dwr,
                            void* dl16, int T, int H, int E, hipStream_t st);
 
+// ---------------------------------------------------------------- rows to experts and back
+struct RowsArgs {
+    int T, H, k, S;
+    int dtype;                // moe_dtype
+    const int32_t* row_of_slot;
+    int32_t* err;
+};
+
+// permute.hip
+int launch_permute(const RowsArgs& a, const void* x, void* xs, hipStream_t st);
+int launch_permute_bwd(const RowsArgs& a, const void* dxs, void* dx, hipStream_t st);
+int launch_unpermute(const RowsArgs& a, const void* o, const float* w, const void* residual, void* y,
+                     hipStream_t st);
+int launch_unpermute_bwd(const RowsArgs& a, const void* o, const void* dy, const int32_t* idx, const float* w,
+                         int E, void* d_o, float* dw, float* d_logits, hipStream_t st);
+
+// ---------------------------------------------------------------- linear
+// moe_act
+enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4, LIN_ACTS = 5 };
+constexpr int kLinDzRows = 32;       // rows of a k_linear_dz tile
+
+struct LinPrefix {
+    int n;                    // prefixes wanted
+    int tm[3];                // rows of a tile
+    int lo[3], hi[3];         // the groups of lo <= n < hi rows
+    int32_t* out[3];          // [E+1]
+};
+
+// g.tile_off null: one dense group of g.dense_rows rows
+struct LinFwdArgs {
+    GroupRows g;
+    int dtype, act, N, K;
+    const uint16_t* x;        // [M, K]
+    const uint16_t* w;        // [E, N, K]
+    const uint16_t* bias;     // [E, N] or null
+    const uint16_t* residual; // [M, N] or null; may be y
+    uint16_t* y;              // [M, N]
+    uint16_t* z;              // [M, N] or null
+};
+
+struct LinDzArgs {
+    GroupRows g;              // tile_off: tiles of kLinDzRows rows
+    int dtype, act, N;
+    const uint16_t* dy;
+    const uint16_t* z;        // read unless act is LIN_NONE
+    uint16_t* dz;             // written unless act is LIN_NONE
+    float* part;              // [tiles, N] column sums, or null
+};
+
+struct LinBwdArgs {
+    GroupRows g;
+    int dtype, N, K;
+    const uint16_t* dz;       // [M, N]
+    const uint16_t* x;
+    const uint16_t* w;
+    uint16_t* dx;
+    uint16_t* dw;
+};
+
+// linear.hip
+int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st);
+int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st);
+int launch_linear_dz(const LinDzArgs& a, hipStream_t st);
+int launch_linear_db(const LinDzArgs& a, void* db, hipStream_t st);
+int launch_linear_dx(const LinBwdArgs& a, hipStream_t st);
+int launch_linear_dw(const LinBwdArgs& a, hipStream_t st);
+
+// api.hip
+bool device_ok();             // the current device is gfx950
+
 // gemm.hip
 int launch_gemm_gate_up(const GemmGateUpArgs& a, hipStream_t st);
 int launch_gemm_down(const GemmDownArgs& a, hipStream_t st);

@@ -1,0 +1,447 @@
+// y = act(x W^T + b) + residual, dense or grouped by expert, and its backward:
+//
+//   z  = x W^T + b          x [M, K], W [N, K] (per expert), b [N]
+//   y  = act(z) + residual
+//   dz = dy act'(z)
+//   dx = dz W,  dW = dz^T x,  db = sum over the rows of dz
+//
+// The products of experts that are not the layer's SwiGLU (alphalab.site
+// "Mixture-of-Kittens" section 一: each expert runs its FFN on the rows routed
+// to it) and the dense projections in front of and behind the layer.  Groups
+// are the rows offsets[e] .. offsets[e + 1] of one macrobatch; no count
+// reaches the host (arex-research.com "Cursor 放出 MoK", design section, second
+// decision): the grid covers an upper bound of tiles and each block finds its
+// tile in a prefix that k_linear_prefix builds.
+//
+// N and K are multiples of 8 (16-byte rows), M and the groups are any size:
+// operand chunks past a row's end, a group's end or a matrix's end are read
+// as zeros, results past them are not stored.  Products are sums of fp32 MFMA
+// steps in ascending order of the reduction index; bias, activation and
+// residual are applied to the fp32 sum, which is rounded once.
+#include "dtype.h"
+#include "gemm_common.h"
+#include "profile.h"
+
+namespace moe {
+
+// ================================================================ activations
+__device__ __forceinline__ float sigm(float v) { return 1.0f / (1.0f + __expf(-v)); }
+
+constexpr float kInvSqrt2 = 0.70710678118654752f;     // 1 / sqrt(2)
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1 / sqrt(2 pi)
+constexpr float kTanhC = 0.79788456080286536f;        // sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+
+// gelu_tanh: (1 + tanh u) / 2 = sigmoid(2 u), u = sqrt(2 / pi) (z + a z^3)
+template <int ACT>
+__device__ __forceinline__ float act(float z) {
+    if constexpr (ACT == LIN_RELU) return z < 0.f ? 0.f : z;
+    else if constexpr (ACT == LIN_GELU) return 0.5f * z * (1.0f + erff(z * kInvSqrt2));
+    else if constexpr (ACT == LIN_GELU_TANH) return z * sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
+    else if constexpr (ACT == LIN_SILU) return z * sigm(z);
+    else return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+    if constexpr (ACT == LIN_RELU) return z > 0.f ? 1.f : 0.f;
+    else if constexpr (ACT == LIN_GELU)
+        return 0.5f * (1.0f + erff(z * kInvSqrt2)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+    else if constexpr (ACT == LIN_GELU_TANH) {
+        const float p = sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
+        return p + z * p * (1.0f - p) * 2.0f * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
+    } else if constexpr (ACT == LIN_SILU) {
+        const float p = sigm(z);
+        return p * (1.0f + z * (1.0f - p));
+    } else return 1.f;
+}
+
+// ================================================================ tile prefixes
+// One block: for each list q, out[q][e] = sum over e' < e of
+// ceil(n_e' / tm[q]) over the groups with lo[q] <= n < hi[q] rows.
+__global__ __launch_bounds__(1024) void k_linear_prefix(const int32_t* __restrict__ offsets, int E, int rows,
+                                                        LinPrefix p, int32_t* __restrict__ err) {
+    __shared__ int32_t wsum[16];
+    const int e = threadIdx.x, lane = lane_id(), wv = threadIdx.x >> 6;
+    int cnt = 0;
+    if (e < E) {
+        const int a = offsets[e], b = offsets[e + 1];
+        if (a < 0 || b < a || b > rows) raise_err(err, ERR_BAD_OFFSETS);
+        else cnt = b - a;
+    }
+    for (int q = 0; q < p.n; ++q) {
+        const int n = cnt >= p.lo[q] && cnt < p.hi[q] ? (cnt + p.tm[q] - 1) / p.tm[q] : 0;
+        int incl = n;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 63) wsum[wv] = incl;
+        __syncthreads();
+        int pre = incl - n;
+        for (int v = 0; v < wv; ++v) pre += wsum[v];
+        if (e < E) p.out[q][e] = pre;
+        if (e == E - 1) p.out[q][E] = pre + n;
+        __syncthreads();
+    }
+}
+
+// ================================================================ operand loads
+// 16-byte chunks staged through registers; a chunk outside the operand (rows
+// past its last, reduction indices past kmax) is zero.
+template <int ROWS>
+struct LdKC {                                   // reduction index contiguous in memory
+    static constexpr int PER = ROWS * (kTK / 8) / 256;
+    const uint16_t* p[PER];
+    int off[PER], kc[PER], kmax;
+    uint4 v[PER];
+    __device__ LdKC(const uint16_t* base, int64_t ld, int row0, int nrow, int kmax_) : kmax(kmax_) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int c = threadIdx.x + 256 * q, r = c >> 3;
+            kc[q] = (c & 7) * 8;
+            p[q] = row0 + r < nrow ? base + (int64_t)(row0 + r) * ld + kc[q] : nullptr;
+            off[q] = kc_off(r, kc[q] * 2);
+        }
+    }
+    __device__ void load(int kt) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            v[q] = p[q] && kt * kTK + kc[q] < kmax ? *(const uint4*)(p[q] + (int64_t)kt * kTK) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ void store(uint16_t* s) const {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) *(uint4*)(s + off[q]) = v[q];
+    }
+};
+
+template <int ROWS>
+struct LdKS {                                   // reduction index = the memory row
+    static constexpr int CPR = ROWS / 8;
+    static constexpr int PER = kTK * CPR / 256;
+    const uint16_t* p[PER];
+    int kr[PER], cc[PER], kmax;
+    int64_t step;
+    uint4 v[PER];
+    __device__ LdKS(const uint16_t* base, int64_t ld, int col0, int ncol, int kmax_) : kmax(kmax_), step(kTK * ld) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int c = threadIdx.x + 256 * q;
+            kr[q] = c / CPR;
+            cc[q] = (c % CPR) * 8;
+            p[q] = col0 + cc[q] < ncol ? base + (int64_t)kr[q] * ld + col0 + cc[q] : nullptr;
+        }
+    }
+    __device__ void load(int kt) {
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            v[q] = p[q] && kt * kTK + kr[q] < kmax ? *(const uint4*)(p[q] + kt * step) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ void store(uint16_t* s) const {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) *(uint4*)(s + kr[q] * Tile<ROWS, true>::P + cc[q]) = v[q];
+    }
+};
+
+// ================================================================ 64 / 128 x 128 tiles
+// Four waves in a 2 x 2 grid, register-staged operands, two LDS buffers, one
+// barrier per 64-deep step.
+template <class D, int TM, int TN, bool AKS, bool BKS, class LA, class LB>
+__device__ __forceinline__ void lin_loop(LA& la, LB& lb, int nk, uint16_t* smem, f32x4 (&acc)[TM / 32][TN / 32]) {
+    using SM = Smem<TM, TN, AKS, BKS>;
+    constexpr bool PERM = AKS || BKS;
+    const int w = threadIdx.x >> 6;
+    const int wm0 = (w & 1) * (TM / 2), wn0 = (w >> 1) * (TN / 2);
+    zero_acc<TM, TN>(acc);
+    if (nk <= 0) return;
+    uint16_t* buf0 = smem;
+    uint16_t* buf1 = smem + SM::STAGE;
+    la.load(0);
+    lb.load(0);
+    la.store(buf0);
+    lb.store(buf0 + SM::A);
+    __syncthreads();
+    for (int kt = 0; kt < nk; ++kt) {
+        const uint16_t* cur = (kt & 1) ? buf1 : buf0;
+        uint16_t* nxt = (kt & 1) ? buf0 : buf1;
+        const bool more = kt + 1 < nk;
+        if (more) {
+            la.load(kt + 1);
+            lb.load(kt + 1);
+        }
+#pragma unroll
+        for (int ks = 0; ks < kTK; ks += 32) {
+            uint4 fb[TM / 32], fa[TN / 32];
+#pragma unroll
+            for (int mb = 0; mb < TM / 32; ++mb)
+                fb[mb] = __builtin_bit_cast(uint4, frag<AKS, PERM>(cur, Tile<TM, AKS>::P, wm0 + mb * 16, ks));
+#pragma unroll
+            for (int nb = 0; nb < TN / 32; ++nb)
+                fa[nb] = __builtin_bit_cast(uint4, frag<BKS, PERM>(cur + SM::A, Tile<TN, BKS>::P, wn0 + nb * 16, ks));
+#pragma unroll
+            for (int mb = 0; mb < TM / 32; ++mb)
+#pragma unroll
+                for (int nb = 0; nb < TN / 32; ++nb) acc[mb][nb] = D::mfma(fa[nb], fb[mb], acc[mb][nb]);
+        }
+        if (more) {
+            la.store(nxt);
+            lb.store(nxt + SM::A);
+        }
+        __syncthreads();
+    }
+}
+
+// Four consecutive output columns of one row: bias, activation, residual.
+template <class D, int ACT>
+__device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int64_t row, int col, const f32x4& s) {
+    const int64_t at = row * a.N + col;
+    float z[4] = {s[0], s[1], s[2], s[3]};
+    if (a.bias) {
+        const uint2 b = *(const uint2*)(a.bias + (int64_t)e * a.N + col);
+        z[0] += D::lo(b.x); z[1] += D::hi(b.x); z[2] += D::lo(b.y); z[3] += D::hi(b.y);
+    }
+    if (a.z) *(uint2*)(a.z + at) = make_uint2(D::pack2(z[0], z[1]), D::pack2(z[2], z[3]));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) z[r] = act<ACT>(z[r]);
+    if (a.residual) {
+        const uint2 b = *(const uint2*)(a.residual + at);
+        z[0] += D::lo(b.x); z[1] += D::hi(b.x); z[2] += D::lo(b.y); z[3] += D::hi(b.y);
+    }
+    *(uint2*)(a.y + at) = make_uint2(D::pack2(z[0], z[1]), D::pack2(z[2], z[3]));
+}
+
+template <class D, int ACT, int TM>
+__global__ __launch_bounds__(256, 2) void k_linear_fwd(LinFwdArgs a) {
+    constexpr int TN = 128;
+    __shared__ __attribute__((aligned(16))) uint16_t smem[2 * Smem<TM, TN, false, false>::STAGE];
+    int e, lo, hi, nt;
+    if (!map_mtile<TM>(a.g, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
+    const int n0 = nt * TN;
+    f32x4 acc[TM / 32][TN / 32];
+    LdKC<TM> la(a.x, a.K, lo, hi, a.K);
+    LdKC<TN> lb(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N, a.K);
+    lin_loop<D, TM, TN, false, false>(la, lb, (a.K + kTK - 1) / kTK, smem, acc);
+    AccPos<TM, TN> pos;
+#pragma unroll
+    for (int mb = 0; mb < TM / 32; ++mb) {
+        const int row = lo + pos.m(mb);
+        if (row >= hi) continue;
+#pragma unroll
+        for (int nb = 0; nb < TN / 32; ++nb) {
+            const int col = n0 + pos.n(nb);
+            if (col < a.N) lin_out<D, ACT>(a, e, row, col, acc[mb][nb]);
+        }
+    }
+}
+
+// dx = dz W: W read with its row (the reduction index n) as the memory row
+template <class D, int TM>
+__global__ __launch_bounds__(256, 2) void k_linear_dx(LinBwdArgs a) {
+    constexpr int TN = 128;
+    __shared__ __attribute__((aligned(16))) uint16_t smem[2 * Smem<TM, TN, false, true>::STAGE];
+    int e, lo, hi, nt;
+    if (!map_mtile<TM>(a.g, (a.K + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
+    const int n0 = nt * TN;
+    f32x4 acc[TM / 32][TN / 32];
+    LdKC<TM> la(a.dz, a.N, lo, hi, a.N);
+    LdKS<TN> lb(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K, a.N);
+    lin_loop<D, TM, TN, false, true>(la, lb, (a.N + kTK - 1) / kTK, smem, acc);
+    AccPos<TM, TN> pos;
+#pragma unroll
+    for (int mb = 0; mb < TM / 32; ++mb) {
+        const int row = lo + pos.m(mb);
+        if (row >= hi) continue;
+#pragma unroll
+        for (int nb = 0; nb < TN / 32; ++nb) {
+            const int col = n0 + pos.n(nb);
+            const f32x4 v = acc[mb][nb];
+            if (col < a.K)
+                *(uint2*)(a.dx + (int64_t)row * a.K + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+        }
+    }
+}
+
+// dW = dz^T x over a group's rows: both operands with the row as the memory row
+template <class D, int TM>
+__global__ __launch_bounds__(256, 2) void k_linear_dw(LinBwdArgs a) {
+    constexpr int TN = 128;
+    __shared__ __attribute__((aligned(16))) uint16_t smem[2 * Smem<TM, TN, true, true>::STAGE];
+    int e, mt, nt, lo, n;
+    if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
+    const int m0 = mt * TM, n0 = nt * TN;
+    f32x4 acc[TM / 32][TN / 32];
+    LdKS<TM> la(a.dz + (int64_t)lo * a.N, a.N, m0, a.N, n);
+    LdKS<TN> lb(a.x + (int64_t)lo * a.K, a.K, n0, a.K, n);
+    lin_loop<D, TM, TN, true, true>(la, lb, (n + kTK - 1) / kTK, smem, acc);
+    AccPos<TM, TN> pos;
+    uint16_t* out = a.dw + (int64_t)e * a.N * a.K;
+#pragma unroll
+    for (int mb = 0; mb < TM / 32; ++mb) {
+        const int row = m0 + pos.m(mb);
+        if (row >= a.N) continue;
+#pragma unroll
+        for (int nb = 0; nb < TN / 32; ++nb) {
+            const int col = n0 + pos.n(nb);
+            const f32x4 v = acc[mb][nb];
+            if (col < a.K)
+                *(uint2*)(out + (int64_t)row * a.K + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+        }
+    }
+}
+
+// ================================================================ dz and db
+// A block takes a tile of TR rows by 512 columns (8 per lane, rows round
+// robin over four waves): dz = dy act'(z) (rounded once, to the type the
+// products read), and the column sums of the unrounded dz, in fp32, one
+// partial row per tile.
+template <class D, int ACT, int TR>
+__global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
+    __shared__ float sums[3][64][8];
+    int e, lo, hi, nt;
+    if (!map_mtile<TR>(a.g, (a.N + 511) / 512, blockIdx.x, e, lo, hi, nt)) return;
+    const int lane = lane_id(), wv = wave_id();
+    const int col = nt * 512 + lane * 8;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (col < a.N) {
+#pragma unroll 4
+        for (int r = lo + wv; r < hi; r += 4) {
+            const int64_t at = (int64_t)r * a.N + col;
+            float g[8], z[8];
+            D::unpack(*(const uint4*)(a.dy + at), g);
+            if constexpr (ACT != LIN_NONE) {
+                D::unpack(*(const uint4*)(a.z + at), z);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) g[q] *= act_grad<ACT>(z[q]);
+                *(uint4*)(a.dz + at) = D::pack(g);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s[q] += g[q];
+        }
+    }
+    if (!a.part) return;
+    if (wv > 0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sums[wv - 1][lane][q] = s[q];
+    }
+    __syncthreads();
+    if (wv > 0 || col >= a.N) return;
+#pragma unroll
+    for (int v = 0; v < 3; ++v)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[q] += sums[v][lane][q];
+    const int tile = a.g.tile_off ? a.g.tile_off[e] + (lo - a.g.offsets[e]) / TR : lo / TR;
+    float* p = a.part + (int64_t)tile * a.N + col;
+    *(float4*)p = make_float4(s[0], s[1], s[2], s[3]);
+    *(float4*)(p + 4) = make_float4(s[4], s[5], s[6], s[7]);
+}
+
+// db[e] = the sum of its tiles' partial rows: a block per 64 columns of an
+// expert, 16 waves over the tiles
+template <class D>
+__global__ __launch_bounds__(1024) void k_linear_db(LinDzArgs a, uint16_t* __restrict__ db, int tr) {
+    __shared__ float sums[16][64];
+    const int nc = (a.N + 63) / 64;
+    const int e = blockIdx.x / nc, col = (blockIdx.x % nc) * 64 + lane_id(), wv = wave_id();
+    int t0 = 0, t1 = (a.g.dense_rows + tr - 1) / tr;
+    if (a.g.tile_off) {
+        t0 = a.g.tile_off[e];
+        t1 = a.g.tile_off[e + 1];
+    }
+    float s = 0.f;
+    if (col < a.N)
+        for (int t = t0 + wv; t < t1; t += 16) s += a.part[(int64_t)t * a.N + col];
+    sums[wv][lane_id()] = s;
+    __syncthreads();
+    if (wv > 0 || col >= a.N) return;
+#pragma unroll
+    for (int v = 1; v < 16; ++v) s += sums[v][lane_id()];
+    db[(int64_t)e * a.N + col] = (uint16_t)D::pack2(s, 0.f);
+}
+
+// ================================================================ launchers
+// upper bound of the row tiles of the groups (or of the dense group)
+static int64_t row_tiles(const GroupRows& g, int tm) {
+    if (!g.tile_off) return ((int64_t)g.dense_rows + tm - 1) / tm;
+    const int64_t b = ((int64_t)g.rows + (int64_t)g.E * (tm - 1)) / tm;
+    return b < g.rows ? b : g.rows;
+}
+
+static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
+
+int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st) {
+    ProfScope prof_(st, "linear_prefix");
+    k_linear_prefix<<<1, 1024, 0, st>>>(offsets, E, rows, p, err);
+    return ok();
+}
+
+template <class D, class F>
+static int with_act(int act, const F& f) {
+    switch (act) {
+        case LIN_RELU: return f(std::integral_constant<int, LIN_RELU>{});
+        case LIN_GELU: return f(std::integral_constant<int, LIN_GELU>{});
+        case LIN_GELU_TANH: return f(std::integral_constant<int, LIN_GELU_TANH>{});
+        case LIN_SILU: return f(std::integral_constant<int, LIN_SILU>{});
+        default: return f(std::integral_constant<int, LIN_NONE>{});
+    }
+}
+
+template <class D>
+static int fwd_(const LinFwdArgs& a, hipStream_t st) {
+    const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.N + 127) / 128);
+    return with_act<D>(a.act, [&](auto A) {
+        if (a.g.tm == 128) k_linear_fwd<D, A(), 128><<<(unsigned)grid, 256, 0, st>>>(a);
+        else k_linear_fwd<D, A(), 64><<<(unsigned)grid, 256, 0, st>>>(a);
+        return ok();
+    });
+}
+
+int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st) {
+    ProfScope prof_(st, "linear_fwd");
+    return a.dtype == 0 ? fwd_<Bf16>(a, st) : fwd_<Fp16>(a, st);
+}
+
+template <class D>
+static int dx_(const LinBwdArgs& a, hipStream_t st) {
+    const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.K + 127) / 128);
+    if (a.g.tm == 128) k_linear_dx<D, 128><<<(unsigned)grid, 256, 0, st>>>(a);
+    else k_linear_dx<D, 64><<<(unsigned)grid, 256, 0, st>>>(a);
+    return ok();
+}
+
+int launch_linear_dx(const LinBwdArgs& a, hipStream_t st) {
+    ProfScope prof_(st, "linear_dx");
+    return a.dtype == 0 ? dx_<Bf16>(a, st) : dx_<Fp16>(a, st);
+}
+
+int launch_linear_dw(const LinBwdArgs& a, hipStream_t st) {
+    ProfScope prof_(st, "linear_dw");
+    const int64_t grid = (int64_t)(a.g.offsets ? a.g.E : 1) * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+    if (a.dtype == 0) k_linear_dw<Bf16, 128><<<(unsigned)grid, 256, 0, st>>>(a);
+    else k_linear_dw<Fp16, 128><<<(unsigned)grid, 256, 0, st>>>(a);
+    return ok();
+}
+
+template <class D>
+static int dz_(const LinDzArgs& a, hipStream_t st) {
+    const int64_t grid = row_tiles(a.g, kLinDzRows) * ((a.N + 511) / 512);
+    return with_act<D>(a.act, [&](auto A) {
+        k_linear_dz<D, A(), kLinDzRows><<<(unsigned)grid, 256, 0, st>>>(a);
+        return ok();
+    });
+}
+
+int launch_linear_dz(const LinDzArgs& a, hipStream_t st) {
+    ProfScope prof_(st, "linear_dz");
+    return a.dtype == 0 ? dz_<Bf16>(a, st) : dz_<Fp16>(a, st);
+}
+
+int launch_linear_db(const LinDzArgs& a, void* db, hipStream_t st) {
+    ProfScope prof_(st, "linear_db");
+    const int64_t grid = (int64_t)(a.g.tile_off ? a.g.E : 1) * ((a.N + 63) / 64);
+    if (a.dtype == 0) k_linear_db<Bf16><<<(unsigned)grid, 1024, 0, st>>>(a, (uint16_t*)db, kLinDzRows);
+    else k_linear_db<Fp16><<<(unsigned)grid, 1024, 0, st>>>(a, (uint16_t*)db, kLinDzRows);
+    return ok();
+}
+
+}  // namespace moe

@@ -1,0 +1,168 @@
+"""Refusals of the building blocks, on the host: exact status codes of the C
+entry points before any device work, and the binding's checks of tensors."""
+import ctypes
+
+import pytest
+import torch
+
+from mixture_experts_layer_dispatch_amd import binding as B
+
+FAKE = 1 << 20                       # aligned, never dereferenced: the checks fail first
+BIG = 1 << 40
+
+
+def _lc(**kw):
+    base = dict(M=64, N=128, K=256, E=0, dtype=0, act=0, flags=0)
+    base.update(kw)
+    return B.moe_linear_config(**base)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({}, B.MOE_OK), ({"M": 1, "N": 8, "K": 8}, B.MOE_OK), ({"E": 1024}, B.MOE_OK), ({"M": 1 << 24}, B.MOE_OK),
+    ({"dtype": 1}, B.MOE_OK), ({"act": 4}, B.MOE_OK),
+    ({"M": 0}, B.MOE_ERR_INVALID_ARG), ({"M": (1 << 24) + 1}, B.MOE_ERR_INVALID_ARG),
+    ({"N": 0}, B.MOE_ERR_INVALID_ARG), ({"N": 12}, B.MOE_ERR_INVALID_ARG), ({"N": 65544}, B.MOE_ERR_INVALID_ARG),
+    ({"K": 4}, B.MOE_ERR_INVALID_ARG), ({"K": 100}, B.MOE_ERR_INVALID_ARG), ({"K": 65544}, B.MOE_ERR_INVALID_ARG),
+    ({"E": -1}, B.MOE_ERR_INVALID_ARG), ({"E": 1025}, B.MOE_ERR_INVALID_ARG),
+    ({"dtype": 2}, B.MOE_ERR_INVALID_ARG), ({"dtype": -1}, B.MOE_ERR_INVALID_ARG),
+    ({"act": 5}, B.MOE_ERR_INVALID_ARG), ({"act": -1}, B.MOE_ERR_INVALID_ARG), ({"flags": 1}, B.MOE_ERR_INVALID_ARG),
+])
+def test_linear_config(kw, status):
+    n = ctypes.c_size_t()
+    assert B.lib().moe_linear_workspace_size(_lc(**kw), ctypes.byref(n)) == status
+    if status == B.MOE_OK:
+        assert n.value >= 256
+
+
+def test_linear_workspace_size_needs_its_arguments():
+    n = ctypes.c_size_t()
+    assert B.lib().moe_linear_workspace_size(None, ctypes.byref(n)) == B.MOE_ERR_INVALID_ARG
+    assert B.lib().moe_linear_workspace_size(_lc(), None) == B.MOE_ERR_INVALID_ARG
+
+
+def _fwd(c=None, off=None, x=FAKE, w=FAKE, bias=None, res=None, y=FAKE, z=None, ws=FAKE, n=BIG):
+    return B.lib().moe_linear_forward(c or _lc(), off, x, w, bias, res, y, z, ws, n, None)
+
+
+def _bwd(c=None, off=None, x=FAKE, w=FAKE, z=FAKE, dy=FAKE, dx=FAKE, dw=FAKE, db=FAKE, ws=FAKE, n=BIG):
+    return B.lib().moe_linear_backward(c or _lc(act=1), off, x, w, z, dy, dx, dw, db, ws, n, None)
+
+
+@pytest.mark.parametrize("kw", [dict(x=None), dict(w=None), dict(y=None), dict(x=FAKE + 8), dict(w=FAKE + 2),
+                                dict(y=FAKE + 4), dict(bias=FAKE + 8), dict(res=FAKE + 8), dict(z=FAKE + 8),
+                                dict(off=FAKE), dict(c=_lc(E=4)), dict(c=_lc(E=4), off=FAKE + 2), dict(c=_lc(N=12))])
+def test_linear_forward_refuses(kw):
+    assert _fwd(**kw) == B.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(dy=None), dict(z=None), dict(z=FAKE + 8), dict(dx=None, dw=None, db=None),
+                                dict(w=None), dict(x=None), dict(dx=FAKE + 8), dict(dw=FAKE + 2), dict(db=FAKE + 8),
+                                dict(dy=FAKE + 8), dict(off=FAKE), dict(c=_lc(E=2, act=1))])
+def test_linear_backward_refuses(kw):
+    assert _bwd(**kw) == B.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(ws=None), dict(ws=FAKE + 128), dict(n=255)])
+def test_workspaces_are_checked(kw):
+    assert _fwd(**kw) == B.MOE_ERR_WORKSPACE
+    assert _bwd(**kw) == B.MOE_ERR_WORKSPACE
+    ws, n = kw.get("ws", FAKE), kw.get("n", BIG)
+    cfg, s = B.Config(T=8, H=128, I=128, E=4, k=2).c(), B.moe_sched(*[FAKE] * 7)
+    L = B.lib()
+    assert L.moe_permute_forward(cfg, s, 0, FAKE, FAKE, ws, n, None) == B.MOE_ERR_WORKSPACE
+    assert L.moe_unpermute_backward(cfg, s, 0, FAKE, FAKE, FAKE, FAKE, None, ws, n, None) == B.MOE_ERR_WORKSPACE
+
+
+def test_permute_and_unpermute_refuse():
+    L, bad = B.lib(), B.MOE_ERR_INVALID_ARG
+    cfg, s = B.Config(T=8, H=128, I=128, E=4, k=2).c(), B.moe_sched(*[FAKE] * 7)
+    none = B.moe_sched()
+    rows_only = B.moe_sched(row_of_slot=FAKE)
+    for f in (L.moe_permute_forward, L.moe_permute_backward):
+        assert f(cfg, s, 3, FAKE, FAKE, FAKE, 256, None) == bad
+        assert f(cfg, none, 0, FAKE, FAKE, FAKE, 256, None) == bad
+        assert f(cfg, None, 0, FAKE, FAKE, FAKE, 256, None) == bad
+        assert f(None, s, 0, FAKE, FAKE, FAKE, 256, None) == bad
+        assert f(cfg, s, 0, None, FAKE, FAKE, 256, None) == bad
+        assert f(cfg, s, 0, FAKE, FAKE + 8, FAKE, 256, None) == bad
+        assert f(B.Config(T=8, H=100, I=128, E=4, k=2).c(), s, 0, FAKE, FAKE, FAKE, 256, None) == bad
+    assert L.moe_unpermute_forward(cfg, rows_only, 0, FAKE, None, FAKE, FAKE, 256, None) == bad
+    assert L.moe_unpermute_forward(cfg, s, 0, FAKE, FAKE + 8, FAKE, FAKE, 256, None) == bad
+    assert L.moe_unpermute_forward(cfg, s, 0, FAKE, None, None, FAKE, 256, None) == bad
+    for i in range(4):                                    # o, dy, d_o, dw
+        p = [FAKE] * 4
+        p[i] = None
+        assert L.moe_unpermute_backward(cfg, s, 0, *p, FAKE, FAKE, 256, None) == bad
+    part = B.moe_sched(row_of_slot=FAKE, topk_w=FAKE)     # d_logits needs topk_idx
+    assert L.moe_unpermute_backward(cfg, part, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 256, None) == bad
+
+
+# ------------------------------------------------------------------ the binding
+BF = torch.bfloat16
+
+
+def _t(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _linear_args():
+    lc = B.LinearConfig(M=6, N=16, K=24, act="gelu")
+    return lc, dict(x=_t(6, 24), w=_t(16, 24), y=_t(6, 16), ws=torch.zeros(B.linear_workspace_size(lc), dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(x=None), "x: missing"), (dict(x=_t(6, 16)), "x: shape"), (dict(w=_t(16, 24, dtype=torch.float16)), "w: dtype"),
+    (dict(y=_t(16, 6).t()), "y: must be contiguous"), (dict(bias=_t(24)), "bias: shape"),
+    (dict(residual=_t(6, 24)), "residual: shape"), (dict(z=_t(6, 16, dtype=torch.float32)), "z: dtype"),
+    (dict(ws=torch.zeros(256, dtype=torch.uint8)), "workspace: 256 bytes"), (dict(ws=None), "workspace: missing"),
+    (dict(offsets=torch.zeros(2, dtype=torch.int32)), "offsets"), (dict(x=[1.0]), "expected a torch.Tensor"),
+    ({}, "must be on the GPU"),
+])
+def test_linear_binding(change, match):
+    lc, a = _linear_args()
+    a.update(change)
+    with pytest.raises(ValueError, match=match):
+        B.moe_linear_forward(lc, **a)
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(z=None), "z: missing"), (dict(w=None), "w: missing"), (dict(x=None), "x: missing"),
+    (dict(dx=None, dw=None, db=None), "at least one"), (dict(dw=_t(24, 16)), "dw: shape"), (dict(db=_t(24)), "db: shape"),
+    ({}, "must be on the GPU"),
+])
+def test_linear_backward_binding(change, match):
+    lc, a = _linear_args()
+    a.pop("y")
+    a.update(z=_t(6, 16), dy=_t(6, 16), dx=_t(6, 24), dw=_t(16, 24), db=_t(16))
+    a.update(change)
+    with pytest.raises(ValueError, match=match):
+        B.moe_linear_backward(lc, **a)
+
+
+def test_linear_config_names_are_checked():
+    with pytest.raises(ValueError, match="act"):
+        B.linear_workspace_size(B.LinearConfig(M=1, N=8, K=8, act="tanh"))
+    with pytest.raises(ValueError, match="dtype"):
+        B.linear_workspace_size(B.LinearConfig(M=1, N=8, K=8, dtype=torch.float32))
+    with pytest.raises(B.MoEError):
+        B.linear_workspace_size(B.LinearConfig(M=1, N=9, K=8))
+    lc = B.LinearConfig(M=4, N=8, K=8, E=3)
+    with pytest.raises(ValueError, match="offsets"):
+        B.moe_linear_forward(lc, _t(4, 8), _t(3, 8, 8), _t(4, 8), torch.zeros(1 << 16, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="offsets: shape"):
+        B.moe_linear_forward(lc, _t(4, 8), _t(3, 8, 8), _t(4, 8), torch.zeros(1 << 16, dtype=torch.uint8),
+                             offsets=torch.zeros(3, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(o=_t(15, 128)), "o: shape"), (dict(o=_t(16, 128, dtype=torch.float64)), "o: expected"),
+    (dict(residual=_t(8, 128, dtype=torch.float16)), "residual: dtype"), (dict(y=None), "y: missing"),
+    (dict(ws=torch.zeros(8, dtype=torch.uint8)), "workspace: 8 bytes"), (dict(ws=None), "workspace: missing"),
+    (dict(sched={}), "row_of_slot"), ({}, "must be on the GPU"),
+])
+def test_unpermute_binding(change, match):
+    cfg = B.Config(T=8, H=128, I=128, E=4, k=2)
+    a = dict(sched=B.alloc_schedule(cfg, "cpu"), o=_t(16, 128), y=_t(8, 128), ws=B.alloc_error_word("cpu"))
+    a.update(change)
+    with pytest.raises(ValueError, match=match):
+        B.moe_unpermute_forward(cfg, **a)

@@ -1,0 +1,310 @@
+"""GPU parity of the linear operator (dense and grouped by expert) against the
+64-bit reference, forward and backward: every activation and type, one row to
+many, sizes that fill no tile, empty and one-row groups, rows in no group,
+weights past 32-bit offsets, bad offsets, other streams, captured graphs."""
+import numpy as np
+import pytest
+import torch
+
+from block_cases import (ACT_ERR, ACT_SLOPE, BF, FP, TINY, U, assert_within, gen, group_offsets, n64, randn, sum_err)
+from mixture_experts_layer_dispatch_amd import binding as B
+from oracle import blocks
+
+pytestmark = pytest.mark.gpu
+IDS = {BF: "bf16", FP: "fp16"}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+class Lin:
+    def __init__(self, seed, M, N, K, dtype=BF, act="none", counts=None, bias=True, residual=True):
+        """counts: the groups' sizes (their sum may be below M: the rows behind are in no group)."""
+        g = gen(seed)
+        E = 0 if counts is None else len(counts)
+        lead = (E,) if E else ()
+        self.lc = B.LinearConfig(M=M, N=N, K=K, E=E, dtype=dtype, act=act)
+        self.x, self.w = randn(g, (M, K), dtype), randn(g, (*lead, N, K), dtype, K ** -0.5)
+        self.bias = randn(g, (*lead, N), dtype) if bias else None
+        self.res = randn(g, (M, N), dtype) if residual else None
+        self.dy = randn(g, (M, N), dtype)
+        self.off = None if counts is None else group_offsets(counts)
+        self.off_list = None if counts is None else self.off.tolist()
+        self.live = M if counts is None else sum(counts)
+        self.ws = B.alloc_linear_workspace(self.lc)
+
+    def outputs(self, fill=-77.0):
+        lc, dt = self.lc, self.lc.dtype
+        full = lambda like: torch.full(like, fill, dtype=dt, device="cuda")  # noqa: E731
+        return {"y": full((lc.M, lc.N)), "z": full((lc.M, lc.N)), "dx": full((lc.M, lc.K)),
+                "dw": full(tuple(self.w.shape)), "db": full((*self.w.shape[:-1],))}
+
+    def run(self, out, stream=None):
+        B.moe_linear_forward(self.lc, self.x, self.w, out["y"], self.ws, bias=self.bias, residual=self.res,
+                             z=out["z"], offsets=self.off, stream=stream)
+        B.moe_linear_backward(self.lc, self.x, self.w, out["z"], self.dy, self.ws, dx=out["dx"], dw=out["dw"],
+                              db=out["db"], offsets=self.off, stream=stream)
+
+    def check(self, out, untouched=-77.0):
+        n = self.live
+        check_linear(out, self.x, self.w, self.bias, self.res, self.dy, self.lc, self.off_list, n)
+        for name in ("y", "z", "dx"):
+            assert (out[name][n:] == untouched).all(), f"{name}: rows in no group were written"
+        assert B.moe_check_device_error(self.ws) == 0
+
+
+def check_linear(out, x, w, b, r, dy, lc, off, n):
+    """Forward and backward outputs of the first n rows against the 64-bit reference."""
+    dt, act = lc.dtype, lc.act
+    u, tiny = U[dt], TINY[dt]
+    x, w, b, r, dy = (n64(t) for t in (x, w, b, r, dy))
+    y, z, mag = blocks.linear(x, w, b, r, act, off)
+    zerr = sum_err(lc.K + 2, mag)
+    assert_within("z", out["z"][:n], z[:n], (u * np.abs(z) + zerr + tiny)[:n])
+    yerr = ACT_SLOPE * zerr + ACT_ERR * np.maximum(np.abs(z), 1) if act != "none" else zerr
+    big = np.abs(y) + (np.abs(r) if r is not None else 0)
+    assert_within("y", out["y"][:n], y[:n], (u * np.abs(y) + (1 + u) * yerr + 2.0 ** -23 * big + tiny)[:n])
+    # the backward reads the stored z
+    zs = n64(out["z"])
+    ref = blocks.linear_backward(x, w, zs, dy, act, off)
+    # dz: rounded once to the type (exact for act "none"), and fp32 errors of act'
+    rel = u if act != "none" else 0.0
+    gerr = np.abs(dy) * (ACT_ERR * np.maximum(np.abs(zs), 1) if act != "none" else 0) + tiny
+    one = blocks.linear_backward(np.abs(x), np.abs(w), zs, gerr, "none", off)
+    for name, red in (("dx", lc.N), ("dw", lc.M), ("db", lc.M)):
+        if out.get(name) is None:
+            continue
+        want, m = ref[name], ref["mag"][name]
+        tol = u * np.abs(want) + (1 + u) * ((rel if name != "db" else 0) * m + one[name] + sum_err(red, m)) + tiny
+        got = out[name]
+        if name == "dx":
+            got, want, tol = got[:n], want[:n], tol[:n]
+        assert_within(name, got, want, tol)
+
+
+DENSE = [(1, 8, 8), (1, 4096, 1024), (3, 264, 136), (16, 128, 64), (17, 1000, 520), (64, 72, 8), (65, 136, 200),
+         (129, 384, 328), (300, 1032, 256), (777, 520, 1544), (1024, 512, 768), (1300, 2056, 264)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_dense_sizes(M, N, K, dtype):
+    c = Lin(M + N + K, M, N, K, dtype, "silu")
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("act", list(B.ACTS))
+@pytest.mark.parametrize("bias,residual", [(True, True), (False, False)])
+@pytest.mark.parametrize("M", [5, 200])
+def test_activations_biases_residuals(M, act, bias, residual, dtype):
+    c = Lin(91, M, 136, 192, dtype, act, None, bias, residual)
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+
+
+COUNTS = [[0, 0, 0], [1], [0, 1, 0, 5, 64], [65, 0, 63, 128, 1], [300, 7, 0, 520], [3] * 70, [40] * 33,
+          [1000, 0, 0, 2], [257, 256, 255, 511, 513]]
+
+
+@pytest.mark.parametrize("behind", [0, 9])
+@pytest.mark.parametrize("counts", COUNTS, ids=[f"groups{i}" for i in range(len(COUNTS))])
+@pytest.mark.parametrize("N,K,dtype", [(136, 200, BF), (512, 256, BF), (264, 320, FP)])
+def test_groups(counts, behind, N, K, dtype):
+    c = Lin(17, sum(counts) + behind or 1, N, K, dtype, "gelu_tanh", counts)
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+    again = c.outputs()
+    c.run(again)
+    for n in out:
+        assert torch.equal(out[n], again[n]), n
+
+
+def test_many_experts():
+    rng = np.random.default_rng(5)
+    c = Lin(18, 700, 64, 72, BF, "relu", list(np.bincount(rng.integers(0, 1024, 700), minlength=1024)))
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+
+
+def test_large_dense_and_grouped_sizes():
+    """Sizes that the largest tiles take."""
+    for counts, M, N, K in ((None, 2500, 2048, 1024), ([900, 0, 1100, 500], 2500, 1024, 520)):
+        c = Lin(19, M, N, K, BF, "gelu", counts)
+        out = c.outputs()
+        c.run(out)
+        c.check(out)
+
+
+def test_residual_may_be_the_output():
+    for M in (3, 300):
+        c = Lin(20, M, 264, 136, BF, "relu")
+        out = c.outputs()
+        c.run(out)
+        y = c.res.clone()
+        B.moe_linear_forward(c.lc, c.x, c.w, y, c.ws, bias=c.bias, residual=y)
+        assert torch.equal(y, out["y"])
+
+
+@pytest.mark.parametrize("counts", [None, [60, 0, 140]])
+def test_each_gradient_alone(counts):
+    c = Lin(21, 200, 136, 72, BF, "silu", counts)
+    out = c.outputs()
+    c.run(out)
+    for name in ("dx", "dw", "db"):
+        one = c.outputs()
+        B.moe_linear_backward(c.lc, c.x if name == "dw" else None, c.w if name == "dx" else None, out["z"], c.dy, c.ws,
+                              offsets=c.off, **{name: one[name]})
+        assert torch.equal(one[name], out[name]), name
+
+
+def test_rows_and_experts_do_not_mix():
+    """Infinities and NaN stay in their row (or expert); rows in no group are not read."""
+    counts = [30, 0, 50, 20]
+    c = Lin(22, 110, 72, 136, BF, "none", counts, residual=False)
+    out = c.outputs()
+    c.run(out)
+    nan, inf = float("nan"), float("inf")
+    c.x[35] = inf
+    c.x[100:] = nan                                       # behind the last group
+    c.dy[100:] = nan
+    c.w[3, 5, 6] = nan
+    got = c.outputs()
+    c.run(got)
+    rows = [r for r in range(100) if r != 35]
+    for n in ("y", "z"):
+        cols = [j for j in range(72) if j != 5]
+        assert torch.equal(got[n][rows][:, cols], out[n][rows][:, cols]), n
+        assert torch.equal(got[n][:80][[r for r in rows if r < 80]], out[n][:80][[r for r in rows if r < 80]]), n
+        assert torch.isnan(got[n][80:100, 5]).all() and not torch.isfinite(got[n][35]).any()
+    assert torch.equal(got["dx"][:80], out["dx"][:80])
+    for n in ("dw", "db"):
+        assert torch.equal(got[n][0], out[n][0]) and torch.equal(got[n][3], out[n][3]), n
+        assert (got[n][1] == 0).all(), n
+    assert torch.equal(got["db"], out["db"])
+    assert (got["y"][100:] == -77).all() and (got["dx"][100:] == -77).all()
+
+
+def test_ragged_edges_do_not_read_their_neighbours():
+    """K and N that end inside a tile, with NaN right behind every operand."""
+    M, N, K = 70, 72, 200
+    c = Lin(23, M, N, K, FP, "silu")
+    out = c.outputs()
+    c.run(out)
+
+    def fenced(t):
+        buf = torch.full((t.numel() + 4096,), float("nan"), dtype=t.dtype, device="cuda")
+        v = buf[2048:2048 + t.numel()].view(t.shape)
+        v.copy_(t)
+        return buf, v
+
+    keep = []
+    for name in ("x", "w", "bias", "res", "dy"):
+        buf, v = fenced(getattr(c, name))
+        keep.append(buf)
+        setattr(c, name, v)
+    got = {}
+    for n, t in c.outputs().items():
+        buf, got[n] = fenced(t)
+        keep.append(buf)
+    c.run(got)
+    for n in out:
+        assert torch.equal(got[n], out[n]), n
+    for buf in keep:
+        assert torch.isnan(buf[:2048]).all() and torch.isnan(buf[buf.numel() - 2048:]).all()
+
+
+def test_bad_offsets_are_skipped_and_reported():
+    c = Lin(24, 100, 72, 64, BF, "relu", [20, 30, 40])
+    good = c.outputs()
+    c.run(good)
+    c.off = torch.tensor([0, 20, 10, 10], dtype=torch.int32, device="cuda")       # expert 1's group runs backwards
+    out = c.outputs()
+    c.run(out)
+    assert B.moe_check_device_error(c.ws) == B.DEVERR_BAD_OFFSETS
+    assert B.moe_check_device_error(c.ws) == 0            # read and cleared
+    assert torch.equal(out["y"][:20], good["y"][:20]) and (out["y"][20:] == -77).all()
+    assert torch.equal(out["dw"][0], good["dw"][0]) and torch.equal(out["dx"][:20], good["dx"][:20])
+    assert (out["dw"][1:] == 0).all() and (out["db"][1:] == 0).all()
+    c.off = torch.tensor([0, 20, 50, 101], dtype=torch.int32, device="cuda")      # the last one ends past M
+    out = c.outputs()
+    c.run(out)
+    assert B.moe_check_device_error(c.ws) == B.DEVERR_BAD_OFFSETS
+    assert torch.equal(out["y"][:50], good["y"][:50]) and (out["y"][50:] == -77).all()
+    assert (out["dw"][2] == 0).all()
+
+
+def test_weights_past_32_bit_offsets():
+    E, N, K = 540, 1024, 4096                             # 2.3e9 weights
+    n = [0] * E
+    n[0], n[511], n[512], n[539] = 3, 70, 1, 200
+    M = sum(n)
+    lc = B.LinearConfig(M=M, N=N, K=K, E=E, act="gelu")
+    ws, off = B.alloc_linear_workspace(lc), group_offsets(n)
+    w = torch.randn(E, N, K, generator=gen(1), device="cuda", dtype=BF).mul_(K ** -0.5)
+    x, dy = (torch.randn(M, s, generator=gen(2), device="cuda", dtype=BF) for s in (K, N))
+    y, z, dx = torch.empty(M, N, dtype=BF, device="cuda"), torch.empty(M, N, dtype=BF, device="cuda"), torch.empty_like(x)
+    dw = torch.full_like(w, 9.0)
+    B.moe_linear_forward(lc, x, w, y, ws, z=z, offsets=off)
+    B.moe_linear_backward(lc, x, w, z, dy, ws, dx=dx, dw=dw, offsets=off)
+    assert B.moe_check_device_error(ws) == 0
+    lo = 0
+    for e in (0, 511, 512, 539):
+        rows = slice(lo, lo + n[e])
+        lo += n[e]
+        one = B.LinearConfig(M=n[e], N=N, K=K, act="gelu")
+        out = {"y": y[rows], "z": z[rows], "dx": dx[rows], "dw": dw[e]}
+        check_linear(out, x[rows], w[e], None, None, dy[rows], one, None, n[e])
+    for e in range(E):
+        if n[e] == 0:
+            assert not dw[e].any(), e
+
+
+def test_two_calls_at_once_on_two_streams():
+    a, b = Lin(25, 300, 264, 520, BF, "gelu"), Lin(26, 90, 512, 1024, FP, "silu", [50, 0, 40])
+    want = []
+    for c in (a, b):
+        out = c.outputs()
+        c.run(out)
+        want.append(out)
+    got = [a.outputs(), b.outputs()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, out, s in zip((a, b), got, streams):
+            c.run(out, stream=s)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for n in w:
+            assert torch.equal(w[n], g[n]), n
+
+
+@pytest.mark.parametrize("M,N,K,counts", [(4, 512, 1024, None), (200, 264, 520, None), (600, 512, 256, [300, 0, 290]),
+                                          (96, 128, 256, [4] * 24)])
+def test_replayed_from_a_graph(M, N, K, counts):
+    c = Lin(27, M, N, K, BF, "gelu", counts)
+    want = c.outputs()
+    c.run(want)
+    out = c.outputs()
+    c.run(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out)
+    for i in range(3):
+        for t in out.values():
+            t.fill_(-77.0)
+        c.ws[256:].fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(out[n], want[n]), (i, n)
