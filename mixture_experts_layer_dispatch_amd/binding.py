@@ -8,6 +8,7 @@ is missing, every entry point raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -166,8 +167,15 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without the Stream object that
+# torch.cuda.current_stream() builds (0.1 us instead of 3), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -568,6 +576,13 @@ class LinearConfig:
     dtype: torch.dtype = torch.bfloat16
     act: str = "none"
 
+    @functools.cached_property
+    def checked(self) -> tuple:
+        """(moe_linear_config, bytes of workspace); raises what is wrong with the config."""
+        c, v = self.c(), ctypes.c_size_t()
+        _check(lib().moe_linear_workspace_size(c, ctypes.byref(v)), "moe_linear_workspace_size")
+        return c, v.value
+
     def c(self) -> moe_linear_config:
         if self.act not in ACTS:
             raise ValueError(f"act: {self.act!r}, expected one of {', '.join(ACTS)}")
@@ -577,9 +592,7 @@ class LinearConfig:
 
 
 def linear_workspace_size(lc: LinearConfig) -> int:
-    v = ctypes.c_size_t()
-    _check(lib().moe_linear_workspace_size(ctypes.byref(lc.c()), ctypes.byref(v)), "moe_linear_workspace_size")
-    return v.value
+    return lc.checked[1]
 
 
 def alloc_linear_workspace(lc: LinearConfig, device="cuda") -> torch.Tensor:
@@ -609,15 +622,16 @@ def _check_tensors(specs):
             raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous")
-    here = None
+    here = -1
     for name, t, _, _ in specs:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device() if t.is_cuda else -1
+        if at < 0:
             raise ValueError(f"{name}: must be on the GPU, found on {t.device}")
-        if here is None:
+        if here < 0:
             here = torch.cuda.current_device()
-        if t.get_device() != here:
+        if at != here:
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
 
 
@@ -706,8 +720,7 @@ def _ptr(t):
 
 def _linear_checks(lc: LinearConfig, ws, offsets):
     """(moe_linear_config, specs of the workspace and offsets, leading shape of w and bias)."""
-    c = lc.c()
-    need = linear_workspace_size(lc)
+    c, need = lc.checked
     _required(workspace=ws)
     n = ws.numel() if isinstance(ws, torch.Tensor) else -1
     if 0 <= n < need:

@@ -57,9 +57,6 @@ LinLayout lin_layout(const moe_linear_config& c) {
     return L;
 }
 
-// 128-row tiles once the mean group holds as many rows
-int lin_row_tile(const moe_linear_config& c) { return c.M >= 128LL * (c.E > 0 ? c.E : 1) ? 128 : 64; }
-
 GroupRows lin_group(const moe_linear_config& c, const int32_t* offsets, char* ws) {
     GroupRows g{};
     g.E = c.E > 0 ? c.E : 1;
@@ -68,6 +65,31 @@ GroupRows lin_group(const moe_linear_config& c, const int32_t* offsets, char* ws
     if (c.E > 0) g.offsets = offsets;
     else g.dense_rows = c.M;
     return g;
+}
+
+// The tile forms of one product and, for groups, the prefixes of its tiles
+// (and of the kLinDzRows-row tiles, if wanted) in one launch.
+int lin_tiles(const moe_linear_config& c, const int32_t* offsets, const LinForm& f, int32_t* tiles, int32_t* big,
+              int32_t* rows32, GroupRows& g, hipStream_t st) {
+    if (c.E == 0) {
+        g.tm = f.dense_big ? 256 : f.small;
+        return 0;
+    }
+    g.tm = f.small;
+    g.tile_off = tiles;
+    LinPrefix p{1, {f.small}, {0}, {f.split ? 256 : INT32_MAX}, {tiles}};
+    auto add = [&](int tm, int lo, int32_t* out) {
+        p.tm[p.n] = tm;
+        p.lo[p.n] = lo;
+        p.hi[p.n] = INT32_MAX;
+        p.out[p.n++] = out;
+    };
+    if (f.split) {
+        add(256, 256, big);
+        g.tile_big = big;
+    }
+    if (rows32) add(kLinDzRows, 0, rows32);
+    return launch_linear_prefix(offsets, c.E, c.M, p, g.err, st);
 }
 
 moe_status lin_common(const moe_linear_config* c, const int32_t* offsets, void* ws, size_t ws_bytes, LinLayout& L) {
@@ -152,13 +174,8 @@ moe_status moe_linear_forward(const moe_linear_config* c, const int32_t* offsets
     char* ws = (char*)workspace;
     LinFwdArgs a{lin_group(*c, offsets, ws), c->dtype, c->act, c->N, c->K, (const uint16_t*)x, (const uint16_t*)w,
                  (const uint16_t*)bias, (const uint16_t*)residual, (uint16_t*)y, (uint16_t*)z};
-    a.g.tm = lin_row_tile(*c);
-    if (c->E > 0) {
-        int32_t* tiles = (int32_t*)(ws + L.tiles);
-        if (launch_linear_prefix(offsets, c->E, c->M, {1, {a.g.tm}, {0}, {INT32_MAX}, {tiles}}, a.g.err, st))
-            return MOE_ERR_HIP;
-        a.g.tile_off = tiles;
-    }
+    int32_t *tiles = (int32_t*)(ws + L.tiles), *big = (int32_t*)(ws + L.big);
+    if (lin_tiles(*c, offsets, linear_form(c->M, c->E, c->N), tiles, big, nullptr, a.g, st)) return MOE_ERR_HIP;
     return launch_linear_fwd(a, st) ? MOE_ERR_HIP : MOE_OK;
 }
 
@@ -176,12 +193,9 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     const GroupRows g = lin_group(*c, offsets, ws);
-    const int tm = lin_row_tile(*c);
-    int32_t *tiles = (int32_t*)(ws + L.tiles), *rows32 = (int32_t*)(ws + L.rows32);
-    if (c->E > 0) {
-        const LinPrefix p{2, {tm, kLinDzRows}, {0, 0}, {INT32_MAX, INT32_MAX}, {tiles, rows32}};
-        if (launch_linear_prefix(offsets, c->E, c->M, p, g.err, st)) return MOE_ERR_HIP;
-    }
+    int32_t *tiles = (int32_t*)(ws + L.tiles), *big = (int32_t*)(ws + L.big), *rows32 = (int32_t*)(ws + L.rows32);
+    GroupRows gx = g;                                 // dx's tiles
+    if (lin_tiles(*c, offsets, linear_form(c->M, c->E, c->K), tiles, big, rows32, gx, st)) return MOE_ERR_HIP;
     uint16_t* dz = (uint16_t*)(ws + L.dz);
     LinDzArgs d{g, c->dtype, c->act, c->N, (const uint16_t*)dy, (const uint16_t*)z, dz,
                 db ? (float*)(ws + L.part) : nullptr};
@@ -189,10 +203,9 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     if ((db || !none) && launch_linear_dz(d, st)) return MOE_ERR_HIP;
     if (db && launch_linear_db(d, db, st)) return MOE_ERR_HIP;
     LinBwdArgs b{g, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x, (const uint16_t*)w,
-                 (uint16_t*)dx, (uint16_t*)dw};
-    b.g.tm = tm;
+                 (uint16_t*)dx, (uint16_t*)dw, linear_dw_big(c->M, c->E, c->N, c->K)};
     if (dw && launch_linear_dw(b, st)) return MOE_ERR_HIP;
-    if (c->E > 0) b.g.tile_off = tiles;
+    b.g = gx;
     if (dx && launch_linear_dx(b, st)) return MOE_ERR_HIP;
     return MOE_OK;
 }

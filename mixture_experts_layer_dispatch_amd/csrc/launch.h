@@ -424,9 +424,19 @@ struct LinBwdArgs {
     const uint16_t* w;
     uint16_t* dx;
     uint16_t* dw;
+    int dw_big;               // dW in 256 x 256 tiles
+};
+
+// Tile forms of a product: rows of the small tiles (64 or 128); a dense one
+// whole in 256 x 256 tiles; the groups of at least 256 rows in those.
+struct LinForm {
+    int small;
+    bool dense_big, split;
 };
 
 // linear.hip
+LinForm linear_form(int M, int E, int C);
+bool linear_dw_big(int M, int E, int N, int K);
 int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st);
 int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st);
 int launch_linear_dz(const LinDzArgs& a, hipStream_t st);

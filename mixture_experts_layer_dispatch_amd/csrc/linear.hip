@@ -21,6 +21,7 @@
 #include "dtype.h"
 #include "gemm_common.h"
 #include "profile.h"
+#include "tile256.h"
 
 namespace moe {
 
@@ -290,6 +291,108 @@ __global__ __launch_bounds__(256, 2) void k_linear_dw(LinBwdArgs a) {
     }
 }
 
+// ================================================================ 256 x 256 tiles
+// Tile b of the groups in tile_big (or of the dense group) with nNt column
+// tiles: an XCD's consecutive tiles are 4 row tiles by 8 column tiles, so that
+// its L2 holds 12 operand strips for 32 tiles.
+__device__ __forceinline__ bool map_tile256(const GroupRows& g, int nNt, int b, int& e, int& lo, int& hi, int& nt) {
+    const int ntiles = g.tile_off ? g.tile_big[g.E] : (g.dense_rows + 255) / 256;
+    if (b >= ntiles * nNt) return false;
+    const int L = xcd_remap(b, ntiles * nNt);
+    const int band = L / (4 * nNt), r = L - band * 4 * nNt, rows = min(4, ntiles - 4 * band);
+    nt = r / rows;
+    const int mt = 4 * band + (r - nt * rows);
+    if (!g.tile_off) {
+        e = 0;
+        lo = mt * 256;
+        hi = min(lo + 256, g.dense_rows);
+        return true;
+    }
+    int a = 0, z = g.E;
+    while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (g.tile_big[mid] <= mt) a = mid;
+        else z = mid;
+    }
+    e = a;
+    lo = g.offsets[e] + (mt - g.tile_big[e]) * 256;
+    hi = min(lo + 256, g.offsets[e + 1]);
+    return true;
+}
+
+template <class D, int ACT>
+__global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
+    int e, lo, hi, nt;
+    if (!map_tile256(a.g, (a.N + 255) / 256, blockIdx.x, e, lo, hi, nt)) return;
+    T2Acc acc;
+    {
+        const T2Operand<false> oa(a.x, a.K, lo, hi);
+        const T2Operand<false> ob(a.w + (int64_t)e * a.N * a.K, a.K, nt * 256, a.N);
+        t2_mainloop<D, false, false>(oa, ob, a.K, acc);
+    }
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+            const int row = lo + t2_row(ha, mb);
+            if (row >= hi) continue;
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb) {
+                    const int col = nt * 256 + t2_col(hb, nb);
+                    if (col < a.N) lin_out<D, ACT>(a, e, row, col, acc[ha][hb][mb][nb]);
+                }
+        }
+}
+
+// rows r0 .. r1 - 1 of the tile at (r0, c0) to out [., ncol]
+template <class D>
+__device__ __forceinline__ void t2_store(uint16_t* out, int r0, int r1, int c0, int ncol, const T2Acc& acc) {
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+            const int row = r0 + t2_row(ha, mb);
+            if (row >= r1) continue;
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb) {
+                    const int col = c0 + t2_col(hb, nb);
+                    const f32x4 v = acc[ha][hb][mb][nb];
+                    if (col < ncol)
+                        *(uint2*)(out + (int64_t)row * ncol + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+                }
+        }
+}
+
+template <class D>
+__global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
+    int e, lo, hi, nt;
+    if (!map_tile256(a.g, (a.K + 255) / 256, blockIdx.x, e, lo, hi, nt)) return;
+    T2Acc acc;
+    {
+        const T2Operand<false> oa(a.dz, a.N, lo, hi);
+        const T2Operand<true> ob(a.w + (int64_t)e * a.N * a.K, a.K, nt * 256, a.K);
+        t2_mainloop<D, false, true>(oa, ob, a.N, acc);
+    }
+    t2_store<D>(a.dx, lo, hi, nt * 256, a.K, acc);
+}
+
+template <class D>
+__global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
+    int e, mt, nt, lo, n;
+    if (!map_ktile(a.g, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
+    T2Acc acc;
+    {
+        const T2Operand<true> oa(a.dz + (int64_t)lo * a.N, a.N, mt * 256, a.N);
+        const T2Operand<true> ob(a.x + (int64_t)lo * a.K, a.K, nt * 256, a.K);
+        t2_mainloop<D, true, true>(oa, ob, n, acc);
+    }
+    t2_store<D>(a.dw + (int64_t)e * a.N * a.K, mt * 256, a.N, nt * 256, a.K, acc);
+}
+
 // ================================================================ dz and db
 // A block takes a tile of TR rows by 512 columns (8 per lane, rows round
 // robin over four waves): dz = dy act'(z) (rounded once, to the type the
@@ -386,10 +489,42 @@ static int with_act(int act, const F& f) {
     }
 }
 
+// The groups in tiles of 256 rows come first, the others follow in a launch
+// of their own; a dense product is one or the other.
+static int64_t big_tiles(const GroupRows& g) {
+    if (!g.tile_off) return g.tm == 256 ? ((int64_t)g.dense_rows + 255) / 256 : 0;
+    if (!g.tile_big) return 0;
+    // groups of n >= 256 rows take ceil(n / 256) <= n / 128 tiles
+    const int64_t x = (int64_t)g.rows / 128, y = ((int64_t)g.rows + (int64_t)g.E * 255) / 256;
+    return x < y ? x : y;
+}
+
+// Row tiles and forms of x W^T (and dz W) with C output columns.
+LinForm linear_form(int M, int E, int C) {
+    const int64_t groups = E > 0 ? E : 1;
+    LinForm f{};
+    f.small = M >= 128 * groups ? 128 : 64;
+    if (E == 0) f.dense_big = ((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 128;
+    else f.split = M >= 192 * groups;
+    return f;
+}
+
+// dW in 256 x 256 tiles (else 128 x 128)
+bool linear_dw_big(int M, int E, int N, int K) {
+    const int64_t groups = E > 0 ? E : 1;
+    return M >= 256 * groups && groups * ((N + 255) / 256) * ((K + 255) / 256) >= 128;
+}
+
 template <class D>
 static int fwd_(const LinFwdArgs& a, hipStream_t st) {
-    const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.N + 127) / 128);
     return with_act<D>(a.act, [&](auto A) {
+        const int64_t big = big_tiles(a.g) * ((a.N + 255) / 256);
+        if (big > 0) {
+            k_linear_fwd256<D, A()><<<(unsigned)big, kT2Threads, 0, st>>>(a);
+            if (ok()) return -1;
+        }
+        if (a.g.tm == 256) return 0;
+        const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.N + 127) / 128);
         if (a.g.tm == 128) k_linear_fwd<D, A(), 128><<<(unsigned)grid, 256, 0, st>>>(a);
         else k_linear_fwd<D, A(), 64><<<(unsigned)grid, 256, 0, st>>>(a);
         return ok();
@@ -403,6 +538,12 @@ int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st) {
 
 template <class D>
 static int dx_(const LinBwdArgs& a, hipStream_t st) {
+    const int64_t big = big_tiles(a.g) * ((a.K + 255) / 256);
+    if (big > 0) {
+        k_linear_dx256<D><<<(unsigned)big, kT2Threads, 0, st>>>(a);
+        if (ok()) return -1;
+    }
+    if (a.g.tm == 256) return 0;
     const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.K + 127) / 128);
     if (a.g.tm == 128) k_linear_dx<D, 128><<<(unsigned)grid, 256, 0, st>>>(a);
     else k_linear_dx<D, 64><<<(unsigned)grid, 256, 0, st>>>(a);
@@ -414,12 +555,22 @@ int launch_linear_dx(const LinBwdArgs& a, hipStream_t st) {
     return a.dtype == 0 ? dx_<Bf16>(a, st) : dx_<Fp16>(a, st);
 }
 
+template <class D>
+static int dw_(const LinBwdArgs& a, hipStream_t st) {
+    const int64_t groups = a.g.offsets ? a.g.E : 1;
+    if (a.dw_big) {
+        const int64_t grid = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+        k_linear_dw256<D><<<(unsigned)grid, kT2Threads, 0, st>>>(a);
+    } else {
+        const int64_t grid = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+        k_linear_dw<D, 128><<<(unsigned)grid, 256, 0, st>>>(a);
+    }
+    return ok();
+}
+
 int launch_linear_dw(const LinBwdArgs& a, hipStream_t st) {
     ProfScope prof_(st, "linear_dw");
-    const int64_t grid = (int64_t)(a.g.offsets ? a.g.E : 1) * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-    if (a.dtype == 0) k_linear_dw<Bf16, 128><<<(unsigned)grid, 256, 0, st>>>(a);
-    else k_linear_dw<Fp16, 128><<<(unsigned)grid, 256, 0, st>>>(a);
-    return ok();
+    return a.dtype == 0 ? dw_<Bf16>(a, st) : dw_<Fp16>(a, st);
 }
 
 template <class D>

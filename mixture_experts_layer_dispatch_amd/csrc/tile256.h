@@ -1,0 +1,286 @@
+// 256 x 256 output tiles on MFMA for products with hundreds of rows or more.
+//
+// A block is eight waves (two per SIMD) and owns a CU: two LDS stages of
+// 64 KB, each four 16 KB halves (rows 0-127 / 128-255 of the A tile, columns
+// 0-127 / 128-255 of the B tile, 64 reduction indices deep).  Wave w computes
+// 64 + 64 rows (64 (w >> 2) of either half) by 32 + 32 columns (32 (w & 3) of
+// either half), four quarters of 64 x 32, one per phase of a step:
+//
+//   phase 1  reads A half 0 and B half 0,  A0 x B0
+//   phase 2  reads B half 1,               A0 x B1
+//   phase 3  reads A half 1,               A1 x B1
+//   phase 4  reads nothing,                A1 x B0
+//
+// A phase is a memory part (its LDS reads, and the copies of one half of a
+// later step from global memory straight into the half that every wave has
+// read) and a product part (16 MFMAs), each ended by a barrier.  Waves 4-7 run
+// one barrier behind waves 0-3, so each SIMD has one wave in its product part
+// while the other one's reads and copies are issued.  The copies run five
+// halves (80 KB) ahead of the reads and are never drained in the loop: each
+// memory part waits only until the half the next phase reads has landed
+// (vmcnt 10, two copies per thread and half).
+#pragma once
+
+#include "dtype.h"
+#include "gemm_common.h"
+
+namespace moe {
+
+constexpr int kT2Threads = 512;
+constexpr int kT2Half = 128 * kTK;             // uint16 of one half: 128 rows (or columns) by kTK
+
+// Compiler fence around the barriers: no LDS access moves across it.
+__device__ __forceinline__ void t2_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void t2_barrier() {
+    t2_fence();
+    __builtin_amdgcn_s_barrier();
+    t2_fence();
+}
+// wait until this wave's LDS reads are done and at most N copies are in flight
+template <int N>
+__device__ __forceinline__ void t2_wait() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
+}
+
+// ---------------------------------------------------------------- operands
+// KC: the reduction index is contiguous in memory.  A half is 128 rows of
+// 128 bytes; 16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7) (kc_off).
+// KS: the reduction index is the memory row.  A half is 64 memory rows of 128
+// columns (256 bytes); chunk c of memory row k sits at slot c ^ 2 s(k),
+// s(k) = (k & 3) + 4 ((k >> 3) & 1): the eight memory rows that a 32-lane pass
+// of the transpose load reads fall on eight different 32-byte bank windows.
+// Copy q (0, 1) of thread t moves chunk q * 512 + t of a half.  Rows (columns)
+// past the operand's last are read from its last one; their results are not
+// stored.
+template <bool KS>
+struct T2Operand {
+    const char* base;             // at the tile's first row or column, reduction index 0
+    int64_t step;                 // bytes from one 64-deep step to the next
+    uint32_t off[2][2];           // [half][copy]
+    int kpos[2];                  // [copy] the chunk's reduction index (KC: its first of eight)
+
+    // r0: first row (KC) or column (KS) of the tile, n: the operand's count of them
+    __device__ __forceinline__ T2Operand(const uint16_t* p, int64_t ld, int r0, int n) {
+        base = (const char*)(KS ? p + r0 : p + (int64_t)r0 * ld);
+        step = KS ? kTK * ld * 2 : kTK * 2;
+        const int t = threadIdx.x;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int g = q * kT2Threads + t;
+            if constexpr (KS) {
+                const int k = g >> 4, s = (k & 3) | ((k >> 1) & 4);
+                const int c = (g & 15) ^ (s << 1);
+                kpos[q] = k;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = min(h * 128 + c * 8, n - r0 - 8);
+                    off[h][q] = (uint32_t)(k * (int)ld + col) * 2;
+                }
+            } else {
+                const int r = g >> 3, c = (g & 7) ^ ((r >> 1) & 7);
+                kpos[q] = c * 8;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = min(h * 128 + r, n - r0 - 1);
+                    off[h][q] = (uint32_t)(row * (int)ld + c * 8) * 2;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void copy(int h, int kt, uint16_t* half) const {
+        const char* b = base + kt * step;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t o = off[h][q];
+            asm volatile("" : "+v"(o));            // a scalar base and a 32-bit offset, not 64-bit lane addresses
+            __builtin_amdgcn_global_load_lds((glb_void_t*)(b + o),
+                                             (lds_void_t*)(half + (q * kT2Threads + wave_id() * 64) * 8), 16, 0, 0);
+        }
+    }
+    // the last, partial step through registers: `left` reduction indices, zeros behind them
+    __device__ __forceinline__ void copy_tail(int h, int kt, int left, uint16_t* half) const {
+        const char* b = base + kt * step;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint4 v = kpos[q] < left ? *(const uint4*)(b + off[h][q]) : make_uint4(0, 0, 0, 0);
+            *(uint4*)(half + (q * kT2Threads + threadIdx.x) * 8) = v;
+        }
+    }
+};
+
+// The fragment of 16 rows (columns) from r and the reduction indices ks .. ks + 31 of a half:
+// lane l holds row r + (l & 15), reduction indices ks + 8 (l >> 4) + 0 .. 7.
+template <bool KS>
+__device__ __forceinline__ uint4 t2_frag(const uint16_t* half, int r, int ks) {
+    const int lane = lane_id(), g = lane >> 4, j = lane & 15;
+    if constexpr (KS) {
+        const int s = (j >> 2) | ((g & 1) << 2);
+        const int col = r + 4 * (j & 3);
+        const uint16_t* p = half + (ks + 8 * g + (j >> 2)) * 128 + ((((col >> 3) ^ (s << 1)) << 3) | (col & 7));
+        const v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p);
+        const v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * 128));
+        return make_uint4(__builtin_bit_cast(uint2, a).x, __builtin_bit_cast(uint2, a).y,
+                          __builtin_bit_cast(uint2, b).x, __builtin_bit_cast(uint2, b).y);
+    } else {
+        return *(const uint4*)(half + kc_off(r + j, 2 * (ks + 8 * g)));
+    }
+}
+
+// A wave's four quarters: acc[ha][hb][mb][nb] is rows 128 ha + 64 (w >> 2) + 16 mb + (lane & 15),
+// columns 128 hb + 32 (w & 3) + 16 nb + 4 (lane >> 4) + 0 .. 3.
+typedef f32x4 T2Acc[2][2][4][2];
+
+template <class D, bool AKS, bool BKS>
+struct T2Loop {
+    const T2Operand<AKS>& a;
+    const T2Operand<BKS>& b;
+    T2Acc& acc;
+    int wr, wc;                   // first row / column of the wave in a half
+    uint4 fa[4][2], fb[2][2][2];  // fa[mb][ks], fb[half][nb][ks]
+
+    __device__ __forceinline__ T2Loop(const T2Operand<AKS>& a_, const T2Operand<BKS>& b_, T2Acc& acc_)
+        : a(a_), b(b_), acc(acc_), wr(64 * (wave_id() >> 2)), wc(32 * (wave_id() & 3)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) acc[i][j][mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __device__ __forceinline__ void read_a(const uint16_t* half) {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) fa[mb][s] = t2_frag<AKS>(half, wr + 16 * mb, 32 * s);
+    }
+    __device__ __forceinline__ void read_b(int h, const uint16_t* half) {
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) fb[h][nb][s] = t2_frag<BKS>(half, wc + 16 * nb, 32 * s);
+    }
+    __device__ __forceinline__ void product(int ha, int hb) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+                    acc[ha][hb][mb][nb] = D::mfma(fb[hb][nb][s], fa[mb][s], acc[ha][hb][mb][nb]);
+        __builtin_amdgcn_s_setprio(0);
+    }
+    // Step kt of nk on one stage while the copies of later steps go out: A half
+    // 1 of step kt + 1, then A half 0, B half 0 and B half 1 of step kt + 2.
+    // The waits leave in flight what was issued after the half the next phase
+    // reads: five halves, fewer in the last two steps.
+    // FULL: the caller knows that there are two more steps (branches here make
+    // the compiler lose track of the copies and drain them all once a step).
+    template <bool FULL>
+    __device__ __forceinline__ void step(int kt, int nk, uint16_t* a0, const uint16_t* a1, uint16_t* b0,
+                                         uint16_t* b1, uint16_t* na1) {
+        const bool m1 = FULL || kt + 1 < nk, m2 = FULL || kt + 2 < nk;
+        read_b(0, b0);
+        read_a(a0);
+        if (m1) {
+            a.copy(1, kt + 1, na1);
+            t2_wait<10>();
+        } else {
+            t2_wait<2>();
+        }
+        t2_barrier();
+        product(0, 0);
+        t2_barrier();
+        read_b(1, b1);
+        if (m2) {
+            a.copy(0, kt + 2, a0);
+            t2_wait<10>();
+        } else if (m1) {
+            t2_wait<8>();
+        } else {
+            t2_wait<0>();
+        }
+        t2_barrier();
+        product(0, 1);
+        t2_barrier();
+        read_a(a1);
+        if (m2) b.copy(0, kt + 2, b0);
+        t2_wait<63>();
+        t2_barrier();
+        product(1, 1);
+        t2_barrier();
+        if (m2) {
+            b.copy(1, kt + 2, b1);
+            t2_wait<10>();
+        } else {
+            t2_wait<4>();
+        }
+        t2_barrier();
+        product(1, 0);
+        t2_barrier();
+    }
+};
+
+// acc = A (x) B over `len` reduction indices.
+template <class D, bool AKS, bool BKS>
+__device__ __forceinline__ void t2_mainloop(const T2Operand<AKS>& a, const T2Operand<BKS>& b, int len, T2Acc& acc) {
+    __shared__ __attribute__((aligned(16))) uint16_t a00[kT2Half], a01[kT2Half], b00[kT2Half], b01[kT2Half];
+    __shared__ __attribute__((aligned(16))) uint16_t a10[kT2Half], a11[kT2Half], b10[kT2Half], b11[kT2Half];
+    T2Loop<D, AKS, BKS> l(a, b, acc);
+    const int nk = len / kTK, left = len % kTK;
+    const bool late = wave_id() >= 4;
+    if (nk > 0) {
+        a.copy(0, 0, a00);
+        b.copy(0, 0, b00);
+        b.copy(1, 0, b01);
+        a.copy(1, 0, a01);
+        const int k1 = min(1, nk - 1);             // a single step: copied twice, so that the waits count the same
+        a.copy(0, k1, a10);
+        b.copy(0, k1, b10);
+        b.copy(1, k1, b11);
+        t2_wait<10>();
+        t2_barrier();
+        if (late) t2_barrier();
+        int kt = 0;
+        for (; kt + 3 < nk; kt += 2) {
+            l.template step<true>(kt, nk, a00, a01, b00, b01, a11);
+            l.template step<true>(kt + 1, nk, a10, a11, b10, b11, a01);
+        }
+        for (; kt < nk; kt += 2) {                 // the last one to three
+            l.template step<false>(kt, nk, a00, a01, b00, b01, a11);
+            if (kt + 1 < nk) l.template step<false>(kt + 1, nk, a10, a11, b10, b11, a01);
+        }
+        if (!late) t2_barrier();
+    }
+    if (left > 0) {
+        __syncthreads();
+        a.copy_tail(0, nk, left, a00);
+        a.copy_tail(1, nk, left, a01);
+        b.copy_tail(0, nk, left, b00);
+        b.copy_tail(1, nk, left, b01);
+        __syncthreads();
+        l.read_b(0, b00);
+        l.read_a(a00);
+        l.product(0, 0);
+        l.read_b(1, b01);
+        l.product(0, 1);
+        l.read_a(a01);
+        l.product(1, 1);
+        l.product(1, 0);
+    }
+}
+
+// rows and columns of acc[ha][hb][mb][nb] in the tile
+__device__ __forceinline__ int t2_row(int ha, int mb) {
+    return 128 * ha + 64 * (wave_id() >> 2) + 16 * mb + (lane_id() & 15);
+}
+__device__ __forceinline__ int t2_col(int hb, int nb) {
+    return 128 * hb + 32 * (wave_id() & 3) + 16 * nb + 4 * (lane_id() >> 4);
+}
+
+}  // namespace moe

@@ -68,7 +68,16 @@ def check_linear(out, x, w, b, r, dy, lc, off, n):
     big = np.abs(y) + (np.abs(r) if r is not None else 0)
     assert_within("y", out["y"][:n], y[:n], (u * np.abs(y) + (1 + u) * yerr + 2.0 ** -23 * big + tiny)[:n])
     # the backward reads the stored z
-    zs = n64(out["z"])
+    check_products(out, x, w, n64(out["z"]), dy, lc, off, n)
+
+
+def check_products(out, x, w, zs, dy, lc, off, n):
+    """Those of dx, dw and db that are in `out`, for the stored z."""
+    dt, act = lc.dtype, lc.act
+    u, tiny = U[dt], TINY[dt]
+    x, w, zs, dy = (n64(t) if isinstance(t, torch.Tensor) else t for t in (x, w, zs, dy))
+    if not {"dx", "dw", "db"} & set(out):
+        return
     ref = blocks.linear_backward(x, w, zs, dy, act, off)
     # dz: rounded once to the type (exact for act "none"), and fp32 errors of act'
     rel = u if act != "none" else 0.0
@@ -135,13 +144,41 @@ def test_many_experts():
     c.check(out)
 
 
-def test_large_dense_and_grouped_sizes():
-    """Sizes that the largest tiles take."""
-    for counts, M, N, K in ((None, 2500, 2048, 1024), ([900, 0, 1100, 500], 2500, 1024, 520)):
-        c = Lin(19, M, N, K, BF, "gelu", counts)
+# sizes whose products have enough 256 x 256 tiles to take them, with reduction
+# lengths of no, one and several 64-deep steps and remainders of all kinds
+@pytest.mark.parametrize("K", [8, 64, 72, 128, 192, 200, 256, 328, 520])
+def test_large_dense_forward(K):
+    c = Lin(19, 4100, 2056, K, BF if K % 16 else FP, "gelu")
+    out = c.outputs()
+    for _ in range(3):
+        B.moe_linear_forward(c.lc, c.x, c.w, out["y"], c.ws, bias=c.bias, residual=c.res, z=out["z"])
+        check_linear({"y": out["y"], "z": out["z"]}, c.x, c.w, c.bias, c.res, c.dy, c.lc, None, 4100)
         out = c.outputs()
-        c.run(out)
-        c.check(out)
+
+
+@pytest.mark.parametrize("N", [8, 64, 72, 128, 192, 200, 256, 328, 520])
+def test_large_dense_input_gradient(N):
+    c = Lin(29, 4100, N, 2056, BF if N % 16 else FP, "none")
+    dx = torch.full_like(c.x, -77.0)
+    B.moe_linear_backward(c.lc, None, c.w, None, c.dy, c.ws, dx=dx)
+    check_products({"dx": dx}, c.x, c.w, c.dy, c.dy, c.lc, None, 4100)
+
+
+@pytest.mark.parametrize("M", [256, 264, 300, 321, 383, 448, 577])
+def test_large_dense_weight_gradient(M):
+    c = Lin(39, M, 2056, 4104, BF if M % 2 else FP, "relu")
+    dw = torch.full_like(c.w, -77.0)
+    z = randn(gen(5), (M, 2056), c.lc.dtype)
+    B.moe_linear_backward(c.lc, c.x, None, z, c.dy, c.ws, dw=dw)
+    check_products({"dw": dw}, c.x, c.w, z, c.dy, c.lc, None, M)
+
+
+@pytest.mark.parametrize("counts", [[900, 0, 1100, 500], [257, 256, 255, 511, 513], [1300, 1, 64, 0, 700]])
+def test_large_groups(counts):
+    c = Lin(49, sum(counts) + 3, 1032, 2056, BF, "silu", counts)
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
 
 
 def test_residual_may_be_the_output():
