@@ -175,7 +175,9 @@ moe_status moe_linear_forward(const moe_linear_config* c, const int32_t* offsets
     LinFwdArgs a{lin_group(*c, offsets, ws), c->dtype, c->act, c->N, c->K, (const uint16_t*)x, (const uint16_t*)w,
                  (const uint16_t*)bias, (const uint16_t*)residual, (uint16_t*)y, (uint16_t*)z};
     int32_t *tiles = (int32_t*)(ws + L.tiles), *big = (int32_t*)(ws + L.big);
-    if (lin_tiles(*c, offsets, linear_form(c->M, c->E, c->N), tiles, big, nullptr, a.g, st)) return MOE_ERR_HIP;
+    const LinForm f = linear_form(c->M, c->E, c->N, false);
+    a.stream = f.stream;
+    if (lin_tiles(*c, offsets, f, tiles, big, nullptr, a.g, st)) return MOE_ERR_HIP;
     return launch_linear_fwd(a, st) ? MOE_ERR_HIP : MOE_OK;
 }
 
@@ -195,7 +197,7 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     const GroupRows g = lin_group(*c, offsets, ws);
     int32_t *tiles = (int32_t*)(ws + L.tiles), *big = (int32_t*)(ws + L.big), *rows32 = (int32_t*)(ws + L.rows32);
     GroupRows gx = g;                                 // dx's tiles
-    if (lin_tiles(*c, offsets, linear_form(c->M, c->E, c->K), tiles, big, rows32, gx, st)) return MOE_ERR_HIP;
+    if (lin_tiles(*c, offsets, linear_form(c->M, c->E, c->K, true), tiles, big, rows32, gx, st)) return MOE_ERR_HIP;
     uint16_t* dz = (uint16_t*)(ws + L.dz);
     LinDzArgs d{g, c->dtype, c->act, c->N, (const uint16_t*)dy, (const uint16_t*)z, dz,
                 db ? (float*)(ws + L.part) : nullptr};

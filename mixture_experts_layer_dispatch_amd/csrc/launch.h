@@ -405,6 +405,7 @@ struct LinFwdArgs {
     const uint16_t* residual; // [M, N] or null; may be y
     uint16_t* y;              // [M, N]
     uint16_t* z;              // [M, N] or null
+    int stream;               // k_linear_stream's form, g.tm 16, 32 or 64
 };
 
 struct LinDzArgs {
@@ -427,15 +428,16 @@ struct LinBwdArgs {
     int dw_big;               // dW in 256 x 256 tiles
 };
 
-// Tile forms of a product: rows of the small tiles (64 or 128); a dense one
-// whole in 256 x 256 tiles; the groups of at least 256 rows in those.
+// Tile forms of a product: rows of the small tiles (64 or 128; 16, 32 or 64 of
+// the streaming form); a dense one whole in 256 x 256 tiles; the groups of at
+// least 256 rows in those.
 struct LinForm {
     int small;
-    bool dense_big, split;
+    bool dense_big, split, stream;
 };
 
 // linear.hip
-LinForm linear_form(int M, int E, int C);
+LinForm linear_form(int M, int E, int C, bool dx);
 bool linear_dw_big(int M, int E, int N, int K);
 int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st);
 int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st);

@@ -88,110 +88,10 @@ __global__ __launch_bounds__(1024) void k_linear_prefix(const int32_t* __restric
     }
 }
 
-// ================================================================ operand loads
-// 16-byte chunks staged through registers; a chunk outside the operand (rows
-// past its last, reduction indices past kmax) is zero.
-template <int ROWS>
-struct LdKC {                                   // reduction index contiguous in memory
-    static constexpr int PER = ROWS * (kTK / 8) / 256;
-    const uint16_t* p[PER];
-    int off[PER], kc[PER], kmax;
-    uint4 v[PER];
-    __device__ LdKC(const uint16_t* base, int64_t ld, int row0, int nrow, int kmax_) : kmax(kmax_) {
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            const int c = threadIdx.x + 256 * q, r = c >> 3;
-            kc[q] = (c & 7) * 8;
-            p[q] = row0 + r < nrow ? base + (int64_t)(row0 + r) * ld + kc[q] : nullptr;
-            off[q] = kc_off(r, kc[q] * 2);
-        }
-    }
-    __device__ void load(int kt) {
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-            v[q] = p[q] && kt * kTK + kc[q] < kmax ? *(const uint4*)(p[q] + (int64_t)kt * kTK) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ void store(uint16_t* s) const {
-#pragma unroll
-        for (int q = 0; q < PER; ++q) *(uint4*)(s + off[q]) = v[q];
-    }
-};
-
-template <int ROWS>
-struct LdKS {                                   // reduction index = the memory row
-    static constexpr int CPR = ROWS / 8;
-    static constexpr int PER = kTK * CPR / 256;
-    const uint16_t* p[PER];
-    int kr[PER], cc[PER], kmax;
-    int64_t step;
-    uint4 v[PER];
-    __device__ LdKS(const uint16_t* base, int64_t ld, int col0, int ncol, int kmax_) : kmax(kmax_), step(kTK * ld) {
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            const int c = threadIdx.x + 256 * q;
-            kr[q] = c / CPR;
-            cc[q] = (c % CPR) * 8;
-            p[q] = col0 + cc[q] < ncol ? base + (int64_t)kr[q] * ld + col0 + cc[q] : nullptr;
-        }
-    }
-    __device__ void load(int kt) {
-#pragma unroll
-        for (int q = 0; q < PER; ++q)
-            v[q] = p[q] && kt * kTK + kr[q] < kmax ? *(const uint4*)(p[q] + kt * step) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ void store(uint16_t* s) const {
-#pragma unroll
-        for (int q = 0; q < PER; ++q) *(uint4*)(s + kr[q] * Tile<ROWS, true>::P + cc[q]) = v[q];
-    }
-};
-
 // ================================================================ 64 / 128 x 128 tiles
-// Four waves in a 2 x 2 grid, register-staged operands, two LDS buffers, one
-// barrier per 64-deep step.
-template <class D, int TM, int TN, bool AKS, bool BKS, class LA, class LB>
-__device__ __forceinline__ void lin_loop(LA& la, LB& lb, int nk, uint16_t* smem, f32x4 (&acc)[TM / 32][TN / 32]) {
-    using SM = Smem<TM, TN, AKS, BKS>;
-    constexpr bool PERM = AKS || BKS;
-    const int w = threadIdx.x >> 6;
-    const int wm0 = (w & 1) * (TM / 2), wn0 = (w >> 1) * (TN / 2);
-    zero_acc<TM, TN>(acc);
-    if (nk <= 0) return;
-    uint16_t* buf0 = smem;
-    uint16_t* buf1 = smem + SM::STAGE;
-    la.load(0);
-    lb.load(0);
-    la.store(buf0);
-    lb.store(buf0 + SM::A);
-    __syncthreads();
-    for (int kt = 0; kt < nk; ++kt) {
-        const uint16_t* cur = (kt & 1) ? buf1 : buf0;
-        uint16_t* nxt = (kt & 1) ? buf0 : buf1;
-        const bool more = kt + 1 < nk;
-        if (more) {
-            la.load(kt + 1);
-            lb.load(kt + 1);
-        }
-#pragma unroll
-        for (int ks = 0; ks < kTK; ks += 32) {
-            uint4 fb[TM / 32], fa[TN / 32];
-#pragma unroll
-            for (int mb = 0; mb < TM / 32; ++mb)
-                fb[mb] = __builtin_bit_cast(uint4, frag<AKS, PERM>(cur, Tile<TM, AKS>::P, wm0 + mb * 16, ks));
-#pragma unroll
-            for (int nb = 0; nb < TN / 32; ++nb)
-                fa[nb] = __builtin_bit_cast(uint4, frag<BKS, PERM>(cur + SM::A, Tile<TN, BKS>::P, wn0 + nb * 16, ks));
-#pragma unroll
-            for (int mb = 0; mb < TM / 32; ++mb)
-#pragma unroll
-                for (int nb = 0; nb < TN / 32; ++nb) acc[mb][nb] = D::mfma(fa[nb], fb[mb], acc[mb][nb]);
-        }
-        if (more) {
-            la.store(nxt);
-            lb.store(nxt + SM::A);
-        }
-        __syncthreads();
-    }
-}
+// stages of the ring: two blocks of 64-row tiles share a CU
+template <int TM>
+constexpr int lin_stages() { return TM == 64 ? 3 : 4; }
 
 // Four consecutive output columns of one row: bias, activation, residual.
 template <class D, int ACT>
@@ -213,16 +113,17 @@ __device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int64_t row,
 }
 
 template <class D, int ACT, int TM>
-__global__ __launch_bounds__(256, 2) void k_linear_fwd(LinFwdArgs a) {
+__global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
     constexpr int TN = 128;
-    __shared__ __attribute__((aligned(16))) uint16_t smem[2 * Smem<TM, TN, false, false>::STAGE];
     int e, lo, hi, nt;
     if (!map_mtile<TM>(a.g, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
     const int n0 = nt * TN;
-    f32x4 acc[TM / 32][TN / 32];
-    LdKC<TM> la(a.x, a.K, lo, hi, a.K);
-    LdKC<TN> lb(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N, a.K);
-    lin_loop<D, TM, TN, false, false>(la, lb, (a.K + kTK - 1) / kTK, smem, acc);
+    T1Acc<TM> acc;
+    {
+        const TileOperand<false, TM, 1, kT1Threads> oa(a.x, a.K, lo, hi);
+        const TileOperand<false, TN, 1, kT1Threads> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N);
+        t1_mainloop<D, false, false, TM, lin_stages<TM>()>(oa, ob, a.K, acc);
+    }
     AccPos<TM, TN> pos;
 #pragma unroll
     for (int mb = 0; mb < TM / 32; ++mb) {
@@ -236,18 +137,106 @@ __global__ __launch_bounds__(256, 2) void k_linear_fwd(LinFwdArgs a) {
     }
 }
 
+// ================================================================ few rows
+// A handful of rows: the weights are read once and everything else is small,
+// so the product is a stream.  A block computes 16 MB rows by 16 NB columns;
+// its W waves split the reduction, each reading pieces of S * 64 bytes of every
+// weight row (neighbouring waves neighbouring pieces) straight into MFMA
+// fragments: no LDS and no barrier until the waves' sums are added, in wave
+// order, at the end.  The loads run one unit ahead.
+template <class D, int ACT, int MB, int NB, int S, int W>
+__global__ __launch_bounds__(64 * W) void k_linear_stream(LinFwdArgs a) {
+    constexpr int TM = 16 * MB, TN = 16 * NB, U = 32 * S;
+    __shared__ f32x4 sums[W][MB * NB][64];
+    int e, lo, hi, nt;
+    if (!map_mtile<TM>(a.g, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
+    const int lane = lane_id(), wv = wave_id(), j = lane & 15, kg = 8 * (lane >> 4);
+    const uint16_t *xp[MB], *wp[NB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xp[m] = a.x + (int64_t)min(lo + 16 * m + j, hi - 1) * a.K + kg;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+        wp[n] = a.w + ((int64_t)e * a.N + min(nt * TN + 16 * n + j, a.N - 1)) * a.K + kg;
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Unit {
+        uint4 x[MB][S], w[NB][S];
+    } u0, u1;
+    auto load = [&](Unit& u, int k0) {
+        if (k0 + U <= a.K) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n) u.w[n][s] = *(const uint4*)(wp[n] + k0 + 32 * s);
+#pragma unroll
+                for (int m = 0; m < MB; ++m) u.x[m][s] = *(const uint4*)(xp[m] + k0 + 32 * s);
+            }
+        } else {                                           // the last unit: zeros behind the row
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const bool in = k0 + 32 * s + kg < a.K;
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    u.w[n][s] = in ? *(const uint4*)(wp[n] + k0 + 32 * s) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+                    u.x[m][s] = in ? *(const uint4*)(xp[m] + k0 + 32 * s) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    auto add = [&](const Unit& u) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int n = 0; n < NB; ++n) acc[m][n] = D::mfma(u.w[n][s], u.x[m][s], acc[m][n]);
+    };
+    int k0 = wv * U;
+    if (k0 < a.K) {
+        load(u0, k0);
+        for (;;) {
+            const int k1 = k0 + W * U, k2 = k1 + W * U;
+            if (k1 < a.K) load(u1, k1);
+            add(u0);
+            if (k1 >= a.K) break;
+            if (k2 < a.K) load(u0, k2);
+            add(u1);
+            if (k2 >= a.K) break;
+            k0 = k2;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sums[wv][m * NB + n][lane] = acc[m][n];
+    __syncthreads();
+    for (int i = threadIdx.x; i < MB * NB * 64; i += 64 * W) {
+        const int b = i >> 6, l = i & 63;
+        f32x4 v = sums[0][b][l];
+#pragma unroll
+        for (int q = 1; q < W; ++q) v += sums[q][b][l];
+        const int row = lo + 16 * (b / NB) + (l & 15), col = nt * TN + 16 * (b % NB) + 4 * (l >> 4);
+        if (row < hi && col < a.N) lin_out<D, ACT>(a, e, row, col, v);
+    }
+}
+
 // dx = dz W: W read with its row (the reduction index n) as the memory row
 template <class D, int TM>
-__global__ __launch_bounds__(256, 2) void k_linear_dx(LinBwdArgs a) {
+__global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
     constexpr int TN = 128;
-    __shared__ __attribute__((aligned(16))) uint16_t smem[2 * Smem<TM, TN, false, true>::STAGE];
     int e, lo, hi, nt;
     if (!map_mtile<TM>(a.g, (a.K + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
     const int n0 = nt * TN;
-    f32x4 acc[TM / 32][TN / 32];
-    LdKC<TM> la(a.dz, a.N, lo, hi, a.N);
-    LdKS<TN> lb(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K, a.N);
-    lin_loop<D, TM, TN, false, true>(la, lb, (a.N + kTK - 1) / kTK, smem, acc);
+    T1Acc<TM> acc;
+    {
+        const TileOperand<false, TM, 1, kT1Threads> oa(a.dz, a.N, lo, hi);
+        const TileOperand<true, TN, 1, kT1Threads> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
+        t1_mainloop<D, false, true, TM, lin_stages<TM>()>(oa, ob, a.N, acc);
+    }
     AccPos<TM, TN> pos;
 #pragma unroll
     for (int mb = 0; mb < TM / 32; ++mb) {
@@ -264,17 +253,18 @@ __global__ __launch_bounds__(256, 2) void k_linear_dx(LinBwdArgs a) {
 }
 
 // dW = dz^T x over a group's rows: both operands with the row as the memory row
-template <class D, int TM>
-__global__ __launch_bounds__(256, 2) void k_linear_dw(LinBwdArgs a) {
-    constexpr int TN = 128;
-    __shared__ __attribute__((aligned(16))) uint16_t smem[2 * Smem<TM, TN, true, true>::STAGE];
+template <class D>
+__global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
+    constexpr int TM = 128, TN = 128;
     int e, mt, nt, lo, n;
     if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
-    f32x4 acc[TM / 32][TN / 32];
-    LdKS<TM> la(a.dz + (int64_t)lo * a.N, a.N, m0, a.N, n);
-    LdKS<TN> lb(a.x + (int64_t)lo * a.K, a.K, n0, a.K, n);
-    lin_loop<D, TM, TN, true, true>(la, lb, (n + kTK - 1) / kTK, smem, acc);
+    T1Acc<TM> acc;
+    {
+        const TileOperand<true, TM, 1, kT1Threads> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
+        const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
+        t1_mainloop<D, true, true, TM, lin_stages<TM>()>(oa, ob, n, acc);
+    }
     AccPos<TM, TN> pos;
     uint16_t* out = a.dw + (int64_t)e * a.N * a.K;
 #pragma unroll
@@ -499,11 +489,16 @@ static int64_t big_tiles(const GroupRows& g) {
     return x < y ? x : y;
 }
 
-// Row tiles and forms of x W^T (and dz W) with C output columns.
-LinForm linear_form(int M, int E, int C) {
+// Row tiles and forms of x W^T with C output columns (or, `dx`, of dz W).
+LinForm linear_form(int M, int E, int C, bool dx) {
     const int64_t groups = E > 0 ? E : 1;
     LinForm f{};
     f.small = M >= 128 * groups ? 128 : 64;
+    if (!dx && (E == 0 ? M <= 512 : M <= 8 * groups)) {
+        f.stream = true;
+        f.small = E > 0 || M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        return f;
+    }
     if (E == 0) f.dense_big = ((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 128;
     else f.split = M >= 192 * groups;
     return f;
@@ -524,6 +519,20 @@ static int fwd_(const LinFwdArgs& a, hipStream_t st) {
             if (ok()) return -1;
         }
         if (a.g.tm == 256) return 0;
+        if (a.stream) {
+            auto go = [&](auto kern, int tn, int waves) {
+                kern<<<(unsigned)(row_tiles(a.g, a.g.tm) * ((a.N + tn - 1) / tn)), 64 * waves, 0, st>>>(a);
+                return ok();
+            };
+            const bool dense = !a.g.tile_off;
+            if (a.g.tm == 16) {
+                if (dense) return go(k_linear_stream<D, A(), 1, 1, 4, 8>, 16, 8);
+                return go(k_linear_stream<D, A(), 1, 2, 4, 8>, 32, 8);
+            }
+            if (a.g.tm == 32) return go(k_linear_stream<D, A(), 2, 1, 4, 8>, 16, 8);
+            if (a.g.dense_rows <= 64) return go(k_linear_stream<D, A(), 4, 1, 2, 8>, 16, 8);
+            return go(k_linear_stream<D, A(), 4, 4, 2, 8>, 64, 8);
+        }
         const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.N + 127) / 128);
         if (a.g.tm == 128) k_linear_fwd<D, A(), 128><<<(unsigned)grid, 256, 0, st>>>(a);
         else k_linear_fwd<D, A(), 64><<<(unsigned)grid, 256, 0, st>>>(a);
@@ -563,7 +572,7 @@ static int dw_(const LinBwdArgs& a, hipStream_t st) {
         k_linear_dw256<D><<<(unsigned)grid, kT2Threads, 0, st>>>(a);
     } else {
         const int64_t grid = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-        k_linear_dw<D, 128><<<(unsigned)grid, 256, 0, st>>>(a);
+        k_linear_dw<D><<<(unsigned)grid, 256, 0, st>>>(a);
     }
     return ok();
 }

@@ -52,64 +52,70 @@ __device__ __forceinline__ void t2_wait() {
 // columns (256 bytes); chunk c of memory row k sits at slot c ^ 2 s(k),
 // s(k) = (k & 3) + 4 ((k >> 3) & 1): the eight memory rows that a 32-lane pass
 // of the transpose load reads fall on eight different 32-byte bank windows.
-// Copy q (0, 1) of thread t moves chunk q * 512 + t of a half.  Rows (columns)
-// past the operand's last are read from its last one; their results are not
-// stored.
-template <bool KS>
-struct T2Operand {
+// Copy q of thread t moves chunk q * (threads) + t.  Rows (columns) past the
+// operand's last are read from its last one; their results are not stored.
+// A tile holds the operand in NH arrays of ROWS rows (columns) each, copied by
+// THR threads.
+template <bool KS, int ROWS, int NH, int THR>
+struct TileOperand {
+    static constexpr int PER = ROWS * (kTK / 8) / THR;
+    static_assert(!KS || ROWS == 128, "KS arrays are 128 columns wide");
     const char* base;             // at the tile's first row or column, reduction index 0
     int64_t step;                 // bytes from one 64-deep step to the next
-    uint32_t off[2][2];           // [half][copy]
-    int kpos[2];                  // [copy] the chunk's reduction index (KC: its first of eight)
+    uint32_t off[NH][PER];        // [array][copy]
+    int kpos[PER];                // [copy] the chunk's reduction index (KC: its first of eight)
 
     // r0: first row (KC) or column (KS) of the tile, n: the operand's count of them
-    __device__ __forceinline__ T2Operand(const uint16_t* p, int64_t ld, int r0, int n) {
+    __device__ __forceinline__ TileOperand(const uint16_t* p, int64_t ld, int r0, int n) {
         base = (const char*)(KS ? p + r0 : p + (int64_t)r0 * ld);
         step = KS ? kTK * ld * 2 : kTK * 2;
         const int t = threadIdx.x;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int g = q * kT2Threads + t;
+        for (int q = 0; q < PER; ++q) {
+            const int g = q * THR + t;
             if constexpr (KS) {
                 const int k = g >> 4, s = (k & 3) | ((k >> 1) & 4);
                 const int c = (g & 15) ^ (s << 1);
                 kpos[q] = k;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = min(h * 128 + c * 8, n - r0 - 8);
+                for (int h = 0; h < NH; ++h) {
+                    const int col = min(h * ROWS + c * 8, n - r0 - 8);
                     off[h][q] = (uint32_t)(k * (int)ld + col) * 2;
                 }
             } else {
                 const int r = g >> 3, c = (g & 7) ^ ((r >> 1) & 7);
                 kpos[q] = c * 8;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = min(h * 128 + r, n - r0 - 1);
+                for (int h = 0; h < NH; ++h) {
+                    const int row = min(h * ROWS + r, n - r0 - 1);
                     off[h][q] = (uint32_t)(row * (int)ld + c * 8) * 2;
                 }
             }
         }
     }
-    __device__ __forceinline__ void copy(int h, int kt, uint16_t* half) const {
+    __device__ __forceinline__ void copy(int h, int kt, uint16_t* dst) const {
         const char* b = base + kt * step;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < PER; ++q) {
             uint32_t o = off[h][q];
             asm volatile("" : "+v"(o));            // a scalar base and a 32-bit offset, not 64-bit lane addresses
             __builtin_amdgcn_global_load_lds((glb_void_t*)(b + o),
-                                             (lds_void_t*)(half + (q * kT2Threads + wave_id() * 64) * 8), 16, 0, 0);
+                                             (lds_void_t*)(dst + (q * THR + wave_id() * 64) * 8), 16, 0, 0);
         }
     }
     // the last, partial step through registers: `left` reduction indices, zeros behind them
-    __device__ __forceinline__ void copy_tail(int h, int kt, int left, uint16_t* half) const {
+    __device__ __forceinline__ void copy_tail(int h, int kt, int left, uint16_t* dst) const {
         const char* b = base + kt * step;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < PER; ++q) {
             const uint4 v = kpos[q] < left ? *(const uint4*)(b + off[h][q]) : make_uint4(0, 0, 0, 0);
-            *(uint4*)(half + (q * kT2Threads + threadIdx.x) * 8) = v;
+            *(uint4*)(dst + (q * THR + threadIdx.x) * 8) = v;
         }
     }
 };
+
+template <bool KS>
+using T2Operand = TileOperand<KS, 128, 2, kT2Threads>;
 
 // The fragment of 16 rows (columns) from r and the reduction indices ks .. ks + 31 of a half:
 // lane l holds row r + (l & 15), reduction indices ks + 8 (l >> 4) + 0 .. 7.
@@ -281,6 +287,125 @@ __device__ __forceinline__ int t2_row(int ha, int mb) {
 }
 __device__ __forceinline__ int t2_col(int hb, int nb) {
     return 128 * hb + 32 * (wave_id() & 3) + 16 * nb + 4 * (lane_id() >> 4);
+}
+
+// ================================================================ 64 / 128 x 128 tiles
+// Fewer rows, or too few 256 x 256 tiles for the chip: four waves in a 2 x 2
+// grid, each TM / 2 rows by 64 columns, over a ring of NST stages of 64
+// reduction indices that copies fill NST - 1 steps ahead; one barrier a step,
+// after which the stage read a step before is filled again.  A block at a time
+// on a CU then has up to 96 KB of copies in flight: with one step in flight
+// (register-staged) such a product took about 1 us a step, the latency of a
+// load from HBM.
+constexpr int kT1Threads = 256;
+
+template <int TM>
+using T1Acc = f32x4[TM / 32][4];
+
+template <class D, bool AKS, bool BKS, int TM, int NST>
+struct T1Loop {
+    using OpA = TileOperand<AKS, TM, 1, kT1Threads>;
+    using OpB = TileOperand<BKS, 128, 1, kT1Threads>;
+    static constexpr int PER = OpA::PER + OpB::PER;      // copies per thread and step
+    const OpA& a;
+    const OpB& b;
+    T1Acc<TM>& acc;
+    int wm, wn;
+
+    __device__ __forceinline__ T1Loop(const OpA& a_, const OpB& b_, T1Acc<TM>& acc_)
+        : a(a_), b(b_), acc(acc_), wm((TM / 2) * (wave_id() & 1)), wn(64 * (wave_id() >> 1)) {
+#pragma unroll
+        for (int mb = 0; mb < TM / 32; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __device__ __forceinline__ void product(const uint16_t* sa, const uint16_t* sb) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint4 fa[TM / 32], fb[4];
+#pragma unroll
+            for (int mb = 0; mb < TM / 32; ++mb) fa[mb] = t2_frag<AKS>(sa, wm + 16 * mb, 32 * s);
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) fb[nb] = t2_frag<BKS>(sb, wn + 16 * nb, 32 * s);
+#pragma unroll
+            for (int mb = 0; mb < TM / 32; ++mb)
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = D::mfma(fb[nb], fa[mb], acc[mb][nb]);
+        }
+    }
+    // step kt on (sa, sb) while step kt + NST - 1 is copied to (na, nb)
+    template <bool FULL>
+    __device__ __forceinline__ void step(int kt, int nk, const uint16_t* sa, const uint16_t* sb, uint16_t* na,
+                                         uint16_t* nb) {
+        const int later = FULL ? NST : nk - 1 - kt;       // steps behind this one
+        if (later >= NST - 2) t2_wait<(NST - 2) * PER>();
+        else if (NST > 3 && later == 1) t2_wait<PER>();
+        else t2_wait<0>();
+        t2_barrier();
+        if (later >= NST - 1) {
+            a.copy(0, kt + NST - 1, na);
+            b.copy(0, kt + NST - 1, nb);
+        }
+        product(sa, sb);
+    }
+};
+
+// acc = A (x) B over `len` reduction indices
+template <class D, bool AKS, bool BKS, int TM, int NST>
+__device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Threads>& a,
+                                            const TileOperand<BKS, 128, 1, kT1Threads>& b, int len, T1Acc<TM>& acc) {
+    static_assert(NST == 3 || NST == 4, "");
+    constexpr int SA = TM * kTK, SB = 128 * kTK;
+    __shared__ __attribute__((aligned(16))) uint16_t a0[SA], a1[SA], a2[SA], b0[SB], b1[SB], b2[SB];
+    __shared__ __attribute__((aligned(16))) uint16_t a3[NST == 4 ? SA : 8], b3[NST == 4 ? SB : 8];
+    T1Loop<D, AKS, BKS, TM, NST> l(a, b, acc);
+    const int nk = len / kTK, left = len % kTK;
+    if (nk > 0) {
+        // steps 0 .. NST - 2; what is past the last one is the last one again,
+        // so that the waits count the same
+        a.copy(0, 0, a0);
+        b.copy(0, 0, b0);
+        a.copy(0, min(1, nk - 1), a1);
+        b.copy(0, min(1, nk - 1), b1);
+        if constexpr (NST == 4) {
+            a.copy(0, min(2, nk - 1), a2);
+            b.copy(0, min(2, nk - 1), b2);
+        }
+        int kt = 0;
+        if constexpr (NST == 4) {
+            for (; kt + 6 < nk; kt += 4) {
+                l.template step<true>(kt, nk, a0, b0, a3, b3);
+                l.template step<true>(kt + 1, nk, a1, b1, a0, b0);
+                l.template step<true>(kt + 2, nk, a2, b2, a1, b1);
+                l.template step<true>(kt + 3, nk, a3, b3, a2, b2);
+            }
+            for (; kt < nk; kt += 4) {
+                l.template step<false>(kt, nk, a0, b0, a3, b3);
+                if (kt + 1 < nk) l.template step<false>(kt + 1, nk, a1, b1, a0, b0);
+                if (kt + 2 < nk) l.template step<false>(kt + 2, nk, a2, b2, a1, b1);
+                if (kt + 3 < nk) l.template step<false>(kt + 3, nk, a3, b3, a2, b2);
+            }
+        } else {
+            for (; kt + 4 < nk; kt += 3) {
+                l.template step<true>(kt, nk, a0, b0, a2, b2);
+                l.template step<true>(kt + 1, nk, a1, b1, a0, b0);
+                l.template step<true>(kt + 2, nk, a2, b2, a1, b1);
+            }
+            for (; kt < nk; kt += 3) {
+                l.template step<false>(kt, nk, a0, b0, a2, b2);
+                if (kt + 1 < nk) l.template step<false>(kt + 1, nk, a1, b1, a0, b0);
+                if (kt + 2 < nk) l.template step<false>(kt + 2, nk, a2, b2, a1, b1);
+            }
+        }
+        t2_wait<0>();                              // (one or two steps: the repeated copies)
+    }
+    if (left > 0) {
+        __syncthreads();
+        a.copy_tail(0, nk, left, a0);
+        b.copy_tail(0, nk, left, b0);
+        __syncthreads();
+        l.product(a0, b0);
+    }
 }
 
 }  // namespace moe
