@@ -203,12 +203,10 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
                 db ? (float*)(ws + L.part) : nullptr};
     if (c->E > 0) d.g.tile_off = rows32;
     if ((db || !none) && launch_linear_dz(d, st)) return MOE_ERR_HIP;
-    if (db && launch_linear_db(d, db, st)) return MOE_ERR_HIP;
-    LinBwdArgs b{g, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x, (const uint16_t*)w,
-                 (uint16_t*)dx, (uint16_t*)dw, linear_dw_big(c->M, c->E, c->N, c->K)};
-    if (dw && launch_linear_dw(b, st)) return MOE_ERR_HIP;
-    b.g = gx;
-    if (dx && launch_linear_dx(b, st)) return MOE_ERR_HIP;
+    const LinBwdArgs b{gx, d.g, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x,
+                       (const uint16_t*)w, (uint16_t*)dx, (uint16_t*)dw, (uint16_t*)db, d.part,
+                       linear_dw_form(c->M, c->E, c->N, c->K), 0, 0};
+    if (launch_linear_bwd(b, st)) return MOE_ERR_HIP;
     return MOE_OK;
 }
 

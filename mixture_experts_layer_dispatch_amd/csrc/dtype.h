@@ -7,12 +7,17 @@
 
 namespace moe {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 struct Bf16 {
     static constexpr int PER16 = 8;
-    static __device__ __forceinline__ uint32_t pack2(float a, float b) { return pack_bf2(a, b); }
+    // (gfx950 converts a pair in one instruction, to nearest even, NaN quiet)
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    }
     static __device__ __forceinline__ float lo(uint32_t v) { return lo_bf(v); }
     static __device__ __forceinline__ float hi(uint32_t v) { return hi_bf(v); }
     static __device__ __forceinline__ f32x4 mfma(const uint4& a, const uint4& b, f32x4 c) {

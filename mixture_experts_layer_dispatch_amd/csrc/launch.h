@@ -417,15 +417,23 @@ struct LinDzArgs {
     float* part;              // [tiles, N] column sums, or null
 };
 
+// forms of dW
+enum { LIN_DW_256 = 0, LIN_DW_RING = 1, LIN_DW_FEW = 2 };
+
+// dx, dw, db: null = not wanted
 struct LinBwdArgs {
-    GroupRows g;
+    GroupRows g;              // dx's row tiles; dW's groups
+    GroupRows grows;          // the tiles of part (kLinDzRows rows)
     int dtype, N, K;
     const uint16_t* dz;       // [M, N]
     const uint16_t* x;
     const uint16_t* w;
     uint16_t* dx;
     uint16_t* dw;
-    int dw_big;               // dW in 256 x 256 tiles
+    uint16_t* db;
+    const float* part;        // k_linear_dz's column sums
+    int dw_form;
+    int ndw, ndx;             // (k_linear_bwd: blocks of dW and of dx)
 };
 
 // Tile forms of a product: rows of the small tiles (64 or 128; 16, 32 or 64 of
@@ -438,13 +446,11 @@ struct LinForm {
 
 // linear.hip
 LinForm linear_form(int M, int E, int C, bool dx);
-bool linear_dw_big(int M, int E, int N, int K);
+int linear_dw_form(int M, int E, int N, int K);
 int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st);
 int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st);
 int launch_linear_dz(const LinDzArgs& a, hipStream_t st);
-int launch_linear_db(const LinDzArgs& a, void* db, hipStream_t st);
-int launch_linear_dx(const LinBwdArgs& a, hipStream_t st);
-int launch_linear_dw(const LinBwdArgs& a, hipStream_t st);
+int launch_linear_bwd(const LinBwdArgs& a, hipStream_t st);    // all that follows dz
 
 // api.hip
 bool device_ok();             // the current device is gfx950

@@ -26,19 +26,42 @@
 namespace moe {
 
 // ================================================================ activations
-__device__ __forceinline__ float sigm(float v) { return 1.0f / (1.0f + __expf(-v)); }
+// (reciprocals by v_rcp_f32, 1 ulp: an IEEE division is ten instructions, and
+// with erff the epilogue of a 256 x 256 tile took 15 percent of a 4096-deep product)
+__device__ __forceinline__ float sigm(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 
-constexpr float kInvSqrt2 = 0.70710678118654752f;     // 1 / sqrt(2)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1 / sqrt(2 pi)
 constexpr float kTanhC = 0.79788456080286536f;        // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
+
+// The standard normal's distribution function, and e = exp(-z^2 / 2).  With
+// x = |z| / sqrt(2): Phi(-|z|) = erfc(x) / 2 = e erfcx(x) / 2, and erfcx(x) is a
+// polynomial of degree 8 in t = 1 / (1 + 0.43 x), without a constant term,
+// fitted by iteratively reweighted least squares to a relative error of 8.4e-8
+// over x in [0, 9.5] (4.0e-7 with its evaluation in fp32).
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    e = __expf(-0.5f * z * z);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.304055916f, fabsf(z), 1.0f));
+    float p = 3.685406223e-02f;
+    p = fmaf(p, t, -1.551871300e-01f);
+    p = fmaf(p, t, 1.918536574e-01f);
+    p = fmaf(p, t, -4.286365956e-02f);
+    p = fmaf(p, t, 1.234226599e-01f);
+    p = fmaf(p, t, 1.024754047e-01f);
+    p = fmaf(p, t, 1.221877486e-01f);
+    p = fmaf(p, t, 1.212573051e-01f);
+    const float q = e * (p * t);
+    return z < 0.f ? q : 1.0f - q;
+}
 
 // gelu_tanh: (1 + tanh u) / 2 = sigmoid(2 u), u = sqrt(2 / pi) (z + a z^3)
 template <int ACT>
 __device__ __forceinline__ float act(float z) {
     if constexpr (ACT == LIN_RELU) return z < 0.f ? 0.f : z;
-    else if constexpr (ACT == LIN_GELU) return 0.5f * z * (1.0f + erff(z * kInvSqrt2));
-    else if constexpr (ACT == LIN_GELU_TANH) return z * sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
+    else if constexpr (ACT == LIN_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    } else if constexpr (ACT == LIN_GELU_TANH) return z * sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
     else if constexpr (ACT == LIN_SILU) return z * sigm(z);
     else return z;
 }
@@ -46,9 +69,11 @@ __device__ __forceinline__ float act(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
     if constexpr (ACT == LIN_RELU) return z > 0.f ? 1.f : 0.f;
-    else if constexpr (ACT == LIN_GELU)
-        return 0.5f * (1.0f + erff(z * kInvSqrt2)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
-    else if constexpr (ACT == LIN_GELU_TANH) {
+    else if constexpr (ACT == LIN_GELU) {
+        float e;
+        const float c = normal_cdf(z, e);
+        return c + z * e * kInvSqrt2Pi;
+    } else if constexpr (ACT == LIN_GELU_TANH) {
         const float p = sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
         return p + z * p * (1.0f - p) * 2.0f * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
     } else if constexpr (ACT == LIN_SILU) {
@@ -118,11 +143,12 @@ __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(Lin
     int e, lo, hi, nt;
     if (!map_mtile<TM>(a.g, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
     const int n0 = nt * TN;
+    T1_RING(ring, TM, lin_stages<TM>());
     T1Acc<TM> acc;
     {
         const TileOperand<false, TM, 1, kT1Threads> oa(a.x, a.K, lo, hi);
         const TileOperand<false, TN, 1, kT1Threads> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N);
-        t1_mainloop<D, false, false, TM, lin_stages<TM>()>(oa, ob, a.K, acc);
+        t1_mainloop<D, false, false, TM, lin_stages<TM>()>(oa, ob, a.K, acc, ring);
     }
     AccPos<TM, TN> pos;
 #pragma unroll
@@ -224,18 +250,19 @@ __global__ __launch_bounds__(64 * W) void k_linear_stream(LinFwdArgs a) {
     }
 }
 
+// ================================================================ backward, small tiles
 // dx = dz W: W read with its row (the reduction index n) as the memory row
 template <class D, int TM>
-__global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
+__device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
     constexpr int TN = 128;
     int e, lo, hi, nt;
-    if (!map_mtile<TM>(a.g, (a.K + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
+    if (!map_mtile<TM>(a.g, (a.K + TN - 1) / TN, block, e, lo, hi, nt)) return;
     const int n0 = nt * TN;
     T1Acc<TM> acc;
     {
         const TileOperand<false, TM, 1, kT1Threads> oa(a.dz, a.N, lo, hi);
         const TileOperand<true, TN, 1, kT1Threads> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
-        t1_mainloop<D, false, true, TM, lin_stages<TM>()>(oa, ob, a.N, acc);
+        t1_mainloop<D, false, true, TM, lin_stages<TM>()>(oa, ob, a.N, acc, ring);
     }
     AccPos<TM, TN> pos;
 #pragma unroll
@@ -252,18 +279,24 @@ __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinB
     }
 }
 
+template <class D, int TM>
+__global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
+    T1_RING(ring, TM, lin_stages<TM>());
+    dx_tile<D, TM>(a, blockIdx.x, ring);
+}
+
 // dW = dz^T x over a group's rows: both operands with the row as the memory row
 template <class D>
-__global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
+__device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
     constexpr int TM = 128, TN = 128;
     int e, mt, nt, lo, n;
-    if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
+    if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
     T1Acc<TM> acc;
     {
         const TileOperand<true, TM, 1, kT1Threads> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
         const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
-        t1_mainloop<D, true, true, TM, lin_stages<TM>()>(oa, ob, n, acc);
+        t1_mainloop<D, true, true, TM, lin_stages<TM>()>(oa, ob, n, acc, ring);
     }
     AccPos<TM, TN> pos;
     uint16_t* out = a.dw + (int64_t)e * a.N * a.K;
@@ -279,6 +312,107 @@ __global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
                 *(uint2*)(out + (int64_t)row * a.K + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
         }
     }
+}
+
+template <class D>
+__global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
+    T1_RING(ring, 128, 4);
+    dw_tile<D>(a, blockIdx.x, ring);
+}
+
+// Groups of few rows: dW's write is all the work.  Blocks of 32 KB of LDS,
+// four to a CU, so that some wait for their operands while others store: one
+// stage, no ring; the tile goes out through LDS as whole 256-byte row pieces.
+// (The ring form, a block to a CU, took 3160 us where 512 experts of 40 rows
+// write 4.3 GB, register-staged tiles stored from their fragments 1540 us.)
+template <class D>
+__global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
+    constexpr int TM = 128, TN = 128;
+    __shared__ __attribute__((aligned(16))) uint16_t sm[TM * TN];
+    static_assert(TM * TN == 2 * kT2Half, "the operands' stage and the tile take the same LDS");
+    int e, mt, nt, lo, n;
+    if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
+    const int m0 = mt * TM, n0 = nt * TN;
+    uint16_t *const sa = sm, *const sb = sm + kT2Half;
+    T1Acc<TM> acc;
+    {
+        const TileOperand<true, TM, 1, kT1Threads> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
+        const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
+        T1Loop<D, true, true, TM, 3> l(oa, ob, acc);
+        const int nk = n / kTK, left = n % kTK;
+        for (int kt = 0; kt < nk; ++kt) {
+            oa.copy(0, kt, sa);
+            ob.copy(0, kt, sb);
+            t2_wait<0>();
+            t2_barrier();
+            l.product(sa, sb);
+            __syncthreads();
+        }
+        if (left > 0) {
+            oa.copy_tail(0, nk, left, sa);
+            ob.copy_tail(0, nk, left, sb);
+            __syncthreads();
+            l.product(sa, sb);
+            __syncthreads();
+        }
+    }
+    // 16-byte chunk c of row r at slot c ^ (r & 15)
+    AccPos<TM, TN> pos;
+#pragma unroll
+    for (int mb = 0; mb < TM / 32; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < TN / 32; ++nb) {
+            const int r = pos.m(mb), c = pos.n(nb);
+            const f32x4 v = acc[mb][nb];
+            *(uint2*)(sm + r * TN + (((c >> 3) ^ (r & 15)) << 3) + (c & 7)) =
+                make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+        }
+    __syncthreads();
+    const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    if (n0 + 8 * c >= a.K) return;
+    uint16_t* out = a.dw + ((int64_t)e * a.N + m0) * a.K + n0 + 8 * c;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int r = r0 + 16 * q;
+        if (m0 + r < a.N) *(uint4*)(out + (int64_t)r * a.K) = *(const uint4*)(sm + r * TN + ((c ^ (r & 15)) << 3));
+    }
+}
+
+// db[e] = the sum of its tiles' partial rows (k_linear_dz): 64 columns of an
+// expert, `waves` waves over the tiles
+template <class D>
+__device__ __forceinline__ void db_columns(const float* part, const GroupRows& g, int N, int block, int waves,
+                                           float* sums, uint16_t* db) {
+    const int nc = (N + 63) / 64;
+    const int e = block / nc, col = (block % nc) * 64 + lane_id(), wv = wave_id();
+    int t0 = 0, t1 = (g.dense_rows + kLinDzRows - 1) / kLinDzRows;
+    if (g.tile_off) {
+        t0 = g.tile_off[e];
+        t1 = g.tile_off[e + 1];
+    }
+    float s = 0.f;
+    if (col < N)
+        for (int t = t0 + wv; t < t1; t += waves) s += part[(int64_t)t * N + col];
+    sums[wv * 64 + lane_id()] = s;
+    __syncthreads();
+    if (wv > 0 || col >= N) return;
+    for (int v = 1; v < waves; ++v) s += sums[v * 64 + lane_id()];
+    db[(int64_t)e * N + col] = (uint16_t)D::pack2(s, 0.f);
+}
+
+// All that follows dz in one launch, for products whose tiles leave CUs idle:
+// blocks of dW's tiles, dx's tiles and db's columns.
+template <class D>
+__global__ __launch_bounds__(kT1Threads, 1) void k_linear_bwd(LinBwdArgs a) {
+    T1_RING(ring, 128, 4);
+    int b = blockIdx.x;
+    if (b < a.ndw) {
+        dw_tile<D>(a, b, ring);
+        return;
+    }
+    b -= a.ndw;
+    if (b < a.ndx) dx_tile<D, 128>(a, b, ring);
+    else db_columns<D>(a.part, a.grows, a.N, b - a.ndx, kT1Threads / 64, (float*)ring.a0, a.db);
 }
 
 // ================================================================ 256 x 256 tiles
@@ -429,27 +563,10 @@ __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
     *(float4*)(p + 4) = make_float4(s[4], s[5], s[6], s[7]);
 }
 
-// db[e] = the sum of its tiles' partial rows: a block per 64 columns of an
-// expert, 16 waves over the tiles
 template <class D>
-__global__ __launch_bounds__(1024) void k_linear_db(LinDzArgs a, uint16_t* __restrict__ db, int tr) {
-    __shared__ float sums[16][64];
-    const int nc = (a.N + 63) / 64;
-    const int e = blockIdx.x / nc, col = (blockIdx.x % nc) * 64 + lane_id(), wv = wave_id();
-    int t0 = 0, t1 = (a.g.dense_rows + tr - 1) / tr;
-    if (a.g.tile_off) {
-        t0 = a.g.tile_off[e];
-        t1 = a.g.tile_off[e + 1];
-    }
-    float s = 0.f;
-    if (col < a.N)
-        for (int t = t0 + wv; t < t1; t += 16) s += a.part[(int64_t)t * a.N + col];
-    sums[wv][lane_id()] = s;
-    __syncthreads();
-    if (wv > 0 || col >= a.N) return;
-#pragma unroll
-    for (int v = 1; v < 16; ++v) s += sums[v][lane_id()];
-    db[(int64_t)e * a.N + col] = (uint16_t)D::pack2(s, 0.f);
+__global__ __launch_bounds__(1024) void k_linear_db(LinBwdArgs a) {
+    __shared__ float sums[16 * 64];
+    db_columns<D>(a.part, a.grows, a.N, blockIdx.x, 16, sums, a.db);
 }
 
 // ================================================================ launchers
@@ -504,10 +621,12 @@ LinForm linear_form(int M, int E, int C, bool dx) {
     return f;
 }
 
-// dW in 256 x 256 tiles (else 128 x 128)
-bool linear_dw_big(int M, int E, int N, int K) {
+// Forms of dW: 256 x 256 tiles, the ring of 128 x 128 tiles, or the form of few rows.
+int linear_dw_form(int M, int E, int N, int K) {
     const int64_t groups = E > 0 ? E : 1;
-    return M >= 256 * groups && groups * ((N + 255) / 256) * ((K + 255) / 256) >= 128;
+    if (M >= 256 * groups)
+        return groups * ((N + 255) / 256) * ((K + 255) / 256) >= 128 ? LIN_DW_256 : LIN_DW_RING;
+    return LIN_DW_FEW;
 }
 
 template <class D>
@@ -559,28 +678,56 @@ static int dx_(const LinBwdArgs& a, hipStream_t st) {
     return ok();
 }
 
-int launch_linear_dx(const LinBwdArgs& a, hipStream_t st) {
-    ProfScope prof_(st, "linear_dx");
-    return a.dtype == 0 ? dx_<Bf16>(a, st) : dx_<Fp16>(a, st);
-}
-
 template <class D>
 static int dw_(const LinBwdArgs& a, hipStream_t st) {
     const int64_t groups = a.g.offsets ? a.g.E : 1;
-    if (a.dw_big) {
+    if (a.dw_form == LIN_DW_256) {
         const int64_t grid = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
         k_linear_dw256<D><<<(unsigned)grid, kT2Threads, 0, st>>>(a);
-    } else {
-        const int64_t grid = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-        k_linear_dw<D><<<(unsigned)grid, 256, 0, st>>>(a);
+        return ok();
     }
+    const int64_t grid = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+    if (a.dw_form == LIN_DW_RING) k_linear_dw<D><<<(unsigned)grid, kT1Threads, 0, st>>>(a);
+    else k_linear_dw_few<D><<<(unsigned)grid, kT1Threads, 0, st>>>(a);
     return ok();
 }
 
-int launch_linear_dw(const LinBwdArgs& a, hipStream_t st) {
-    ProfScope prof_(st, "linear_dw");
-    return a.dtype == 0 ? dw_<Bf16>(a, st) : dw_<Fp16>(a, st);
+template <class D>
+static int db_(const LinBwdArgs& a, hipStream_t st) {
+    const int64_t grid = (int64_t)(a.grows.tile_off ? a.grows.E : 1) * ((a.N + 63) / 64);
+    k_linear_db<D><<<(unsigned)grid, 1024, 0, st>>>(a);
+    return ok();
 }
+
+template <class D>
+static int bwd_(LinBwdArgs a, hipStream_t st) {
+    const int64_t groups = a.g.offsets ? a.g.E : 1;
+    const int64_t ndw = a.dw ? groups * ((a.N + 127) / 128) * ((a.K + 127) / 128) : 0;
+    const int64_t ndx = a.dx ? row_tiles(a.g, 128) * ((a.K + 127) / 128) : 0;
+    const int64_t ndb = a.db ? groups * ((a.N + 63) / 64) : 0;
+    if (a.g.tm == 128 && !a.g.tile_big && (ndw > 0) + (ndx > 0) + (ndb > 0) > 1 && ndw + ndx + ndb <= 512) {
+        ProfScope prof_(st, "linear_bwd");
+        a.ndw = (int)ndw;
+        a.ndx = (int)ndx;
+        k_linear_bwd<D><<<(unsigned)(ndw + ndx + ndb), kT1Threads, 0, st>>>(a);
+        return ok();
+    }
+    if (a.db) {
+        ProfScope prof_(st, "linear_db");
+        if (db_<D>(a, st)) return -1;
+    }
+    if (a.dw) {
+        ProfScope prof_(st, "linear_dw");
+        if (dw_<D>(a, st)) return -1;
+    }
+    if (a.dx) {
+        ProfScope prof_(st, "linear_dx");
+        if (dx_<D>(a, st)) return -1;
+    }
+    return 0;
+}
+
+int launch_linear_bwd(const LinBwdArgs& a, hipStream_t st) { return a.dtype == 0 ? bwd_<Bf16>(a, st) : bwd_<Fp16>(a, st); }
 
 template <class D>
 static int dz_(const LinDzArgs& a, hipStream_t st) {
@@ -594,14 +741,6 @@ static int dz_(const LinDzArgs& a, hipStream_t st) {
 int launch_linear_dz(const LinDzArgs& a, hipStream_t st) {
     ProfScope prof_(st, "linear_dz");
     return a.dtype == 0 ? dz_<Bf16>(a, st) : dz_<Fp16>(a, st);
-}
-
-int launch_linear_db(const LinDzArgs& a, void* db, hipStream_t st) {
-    ProfScope prof_(st, "linear_db");
-    const int64_t grid = (int64_t)(a.g.tile_off ? a.g.E : 1) * ((a.N + 63) / 64);
-    if (a.dtype == 0) k_linear_db<Bf16><<<(unsigned)grid, 1024, 0, st>>>(a, (uint16_t*)db, kLinDzRows);
-    else k_linear_db<Fp16><<<(unsigned)grid, 1024, 0, st>>>(a, (uint16_t*)db, kLinDzRows);
-    return ok();
 }
 
 }  // namespace moe

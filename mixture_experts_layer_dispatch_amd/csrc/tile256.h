@@ -350,14 +350,27 @@ struct T1Loop {
     }
 };
 
+// The ring's arrays, each of its own: the compiler waits for every copy in
+// flight before an LDS read that it cannot tell apart from the copies'
+// destination.  TM * kTK and 128 * kTK elements (a3, b3: with four stages).
+struct T1Ring {
+    uint16_t *a0, *a1, *a2, *a3, *b0, *b1, *b2, *b3;
+};
+#define T1_RING(NAME, TM, NST)                                                                             \
+    __shared__ __attribute__((aligned(16))) uint16_t NAME##a0[TM * kTK], NAME##a1[TM * kTK], NAME##a2[TM * kTK]; \
+    __shared__ __attribute__((aligned(16))) uint16_t NAME##b0[128 * kTK], NAME##b1[128 * kTK], NAME##b2[128 * kTK]; \
+    __shared__ __attribute__((aligned(16))) uint16_t NAME##a3[NST == 4 ? TM * kTK : 8];                        \
+    __shared__ __attribute__((aligned(16))) uint16_t NAME##b3[NST == 4 ? 128 * kTK : 8];                       \
+    const T1Ring NAME{NAME##a0, NAME##a1, NAME##a2, NAME##a3, NAME##b0, NAME##b1, NAME##b2, NAME##b3}
+
 // acc = A (x) B over `len` reduction indices
 template <class D, bool AKS, bool BKS, int TM, int NST>
 __device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Threads>& a,
-                                            const TileOperand<BKS, 128, 1, kT1Threads>& b, int len, T1Acc<TM>& acc) {
+                                            const TileOperand<BKS, 128, 1, kT1Threads>& b, int len, T1Acc<TM>& acc,
+                                            const T1Ring& r) {
     static_assert(NST == 3 || NST == 4, "");
-    constexpr int SA = TM * kTK, SB = 128 * kTK;
-    __shared__ __attribute__((aligned(16))) uint16_t a0[SA], a1[SA], a2[SA], b0[SB], b1[SB], b2[SB];
-    __shared__ __attribute__((aligned(16))) uint16_t a3[NST == 4 ? SA : 8], b3[NST == 4 ? SB : 8];
+    uint16_t *const a0 = r.a0, *const a1 = r.a1, *const a2 = r.a2, *const a3 = r.a3;
+    uint16_t *const b0 = r.b0, *const b1 = r.b1, *const b2 = r.b2, *const b3 = r.b3;
     T1Loop<D, AKS, BKS, TM, NST> l(a, b, acc);
     const int nk = len / kTK, left = len % kTK;
     if (nk > 0) {
