@@ -448,73 +448,81 @@ template <class D, int ACT>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
     int e, lo, hi, nt;
     if (!map_tile256(a.g, (a.N + 255) / 256, blockIdx.x, e, lo, hi, nt)) return;
+    T2_LDS(lds);
     T2Acc acc;
     {
         const T2Operand<false> oa(a.x, a.K, lo, hi);
         const T2Operand<false> ob(a.w + (int64_t)e * a.N * a.K, a.K, nt * 256, a.N);
-        t2_mainloop<D, false, false>(oa, ob, a.K, acc);
+        t2_mainloop<D, false, false>(oa, ob, a.K, acc, lds);
     }
+    if (a.bias) {
 #pragma unroll
-    for (int ha = 0; ha < 2; ++ha)
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-            const int row = lo + t2_row(ha, mb);
-            if (row >= hi) continue;
+            for (int nb = 0; nb < 2; ++nb) {
+                const int col = nt * 256 + t2_col(hb, nb);
+                const uint2 b = col < a.N ? *(const uint2*)(a.bias + (int64_t)e * a.N + col) : make_uint2(0, 0);
+                const f32x4 v{D::lo(b.x), D::hi(b.x), D::lo(b.y), D::hi(b.y)};
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
+                for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                    const int col = nt * 256 + t2_col(hb, nb);
-                    if (col < a.N) lin_out<D, ACT>(a, e, row, col, acc[ha][hb][mb][nb]);
-                }
+                    for (int mb = 0; mb < 4; ++mb) acc[ha][hb][mb][nb] += v;
+            }
+    }
+    auto pack = [](const f32x4& v) { return make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3])); };
+    if (a.z)
+        t2_put(lds, a.z, lo, hi, nt * 256, a.N,
+               [&](int ha, int hb, int mb, int nb) { return pack(acc[ha][hb][mb][nb]); });
+    t2_put(lds, a.y, lo, hi, nt * 256, a.N, [&](int ha, int hb, int mb, int nb) {
+        f32x4 v = acc[ha][hb][mb][nb];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = act<ACT>(v[r]);
+        if (a.residual) {
+            const int row = lo + t2_row(ha, mb), col = nt * 256 + t2_col(hb, nb);
+            if (row < hi && col < a.N) {
+                const uint2 b = *(const uint2*)(a.residual + (int64_t)row * a.N + col);
+                v += f32x4{D::lo(b.x), D::hi(b.x), D::lo(b.y), D::hi(b.y)};
+            }
         }
+        return pack(v);
+    });
 }
 
-// rows r0 .. r1 - 1 of the tile at (r0, c0) to out [., ncol]
 template <class D>
-__device__ __forceinline__ void t2_store(uint16_t* out, int r0, int r1, int c0, int ncol, const T2Acc& acc) {
-#pragma unroll
-    for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-            const int row = r0 + t2_row(ha, mb);
-            if (row >= r1) continue;
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                    const int col = c0 + t2_col(hb, nb);
-                    const f32x4 v = acc[ha][hb][mb][nb];
-                    if (col < ncol)
-                        *(uint2*)(out + (int64_t)row * ncol + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
-                }
-        }
+__device__ __forceinline__ void t2_store(const T2Lds& lds, uint16_t* out, int r0, int r1, int c0, int ncol,
+                                         const T2Acc& acc) {
+    t2_put(lds, out, r0, r1, c0, ncol, [&](int ha, int hb, int mb, int nb) {
+        const f32x4 v = acc[ha][hb][mb][nb];
+        return make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+    });
 }
 
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
     int e, lo, hi, nt;
     if (!map_tile256(a.g, (a.K + 255) / 256, blockIdx.x, e, lo, hi, nt)) return;
+    T2_LDS(lds);
     T2Acc acc;
     {
         const T2Operand<false> oa(a.dz, a.N, lo, hi);
         const T2Operand<true> ob(a.w + (int64_t)e * a.N * a.K, a.K, nt * 256, a.K);
-        t2_mainloop<D, false, true>(oa, ob, a.N, acc);
+        t2_mainloop<D, false, true>(oa, ob, a.N, acc, lds);
     }
-    t2_store<D>(a.dx, lo, hi, nt * 256, a.K, acc);
+    t2_store<D>(lds, a.dx, lo, hi, nt * 256, a.K, acc);
 }
 
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
     int e, mt, nt, lo, n;
     if (!map_ktile(a.g, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
+    T2_LDS(lds);
     T2Acc acc;
     {
         const T2Operand<true> oa(a.dz + (int64_t)lo * a.N, a.N, mt * 256, a.N);
         const T2Operand<true> ob(a.x + (int64_t)lo * a.K, a.K, nt * 256, a.K);
-        t2_mainloop<D, true, true>(oa, ob, n, acc);
+        t2_mainloop<D, true, true>(oa, ob, n, acc, lds);
     }
-    t2_store<D>(a.dw + (int64_t)e * a.N * a.K, mt * 256, a.N, nt * 256, a.K, acc);
+    t2_store<D>(lds, a.dw + (int64_t)e * a.N * a.K, mt * 256, a.N, nt * 256, a.K, acc);
 }
 
 // ================================================================ dz and db

@@ -232,11 +232,23 @@ struct T2Loop {
     }
 };
 
+// The stages' halves, each an array of its own: the compiler waits for every
+// copy in flight before an LDS read that it cannot tell apart from the copies'
+// destination.
+struct T2Lds {
+    uint16_t* h[8];
+};
+#define T2_LDS(NAME)                                                                                        \
+    __shared__ __attribute__((aligned(16))) uint16_t NAME##0[kT2Half], NAME##1[kT2Half], NAME##2[kT2Half], \
+        NAME##3[kT2Half], NAME##4[kT2Half], NAME##5[kT2Half], NAME##6[kT2Half], NAME##7[kT2Half];             \
+    const T2Lds NAME{{NAME##0, NAME##1, NAME##2, NAME##3, NAME##4, NAME##5, NAME##6, NAME##7}}
+
 // acc = A (x) B over `len` reduction indices.
 template <class D, bool AKS, bool BKS>
-__device__ __forceinline__ void t2_mainloop(const T2Operand<AKS>& a, const T2Operand<BKS>& b, int len, T2Acc& acc) {
-    __shared__ __attribute__((aligned(16))) uint16_t a00[kT2Half], a01[kT2Half], b00[kT2Half], b01[kT2Half];
-    __shared__ __attribute__((aligned(16))) uint16_t a10[kT2Half], a11[kT2Half], b10[kT2Half], b11[kT2Half];
+__device__ __forceinline__ void t2_mainloop(const T2Operand<AKS>& a, const T2Operand<BKS>& b, int len, T2Acc& acc,
+                                            const T2Lds& lds) {
+    uint16_t *const a00 = lds.h[0], *const a01 = lds.h[1], *const b00 = lds.h[2], *const b01 = lds.h[3];
+    uint16_t *const a10 = lds.h[4], *const a11 = lds.h[5], *const b10 = lds.h[6], *const b11 = lds.h[7];
     T2Loop<D, AKS, BKS> l(a, b, acc);
     const int nk = len / kTK, left = len % kTK;
     const bool late = wave_id() >= 4;
@@ -287,6 +299,41 @@ __device__ __forceinline__ int t2_row(int ha, int mb) {
 }
 __device__ __forceinline__ int t2_col(int hb, int nb) {
     return 128 * hb + 32 * (wave_id() & 3) + 16 * nb + 4 * (lane_id() >> 4);
+}
+
+// The tile to out [., ncol] at row r0, column c0 (rows below r1): f(ha, hb, mb,
+// nb) gives four consecutive values of a row, packed.  It goes out through the
+// stages' LDS (32 rows to an array, 16-byte chunk c of row r at slot c ^ (r &
+// 31)) as 512-byte row pieces, 16 bytes per lane: @MEASURED@
+template <class F>
+__device__ __forceinline__ void t2_put(const T2Lds& lds, uint16_t* out, int r0, int r1, int c0, int ncol, const F& f) {
+    const int wr = wave_id() >> 2, t = threadIdx.x;
+    __syncthreads();                           // the LDS is no longer read
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+            uint16_t* h = wr ? lds.h[4 * ha + 2 + (mb >> 1)] : lds.h[4 * ha + (mb >> 1)];
+            const int r = 16 * (mb & 1) + (lane_id() & 15);
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb) {
+                    const int c = t2_col(hb, nb);
+                    *(uint2*)(h + r * 256 + (((c >> 3) ^ r) << 3) + (c & 7)) = f(ha, hb, mb, nb);
+                }
+        }
+    __syncthreads();
+    const int c = t & 31;
+    if (c0 + 8 * c < ncol) {
+        uint16_t* p = out + (int64_t)r0 * ncol + c0 + 8 * c;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int r = 16 * q + (t >> 5);
+            if (r0 + r < r1)
+                *(uint4*)(p + (int64_t)r * ncol) = *(const uint4*)(lds.h[q >> 1] + (r & 31) * 256 + ((c ^ (r & 31)) << 3));
+        }
+    }
 }
 
 // ================================================================ 64 / 128 x 128 tiles
