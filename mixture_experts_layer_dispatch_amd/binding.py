@@ -611,27 +611,35 @@ def _check_tensors(specs):
     """_validate for the building blocks: tensors (name, tensor, shape, dtype;
     a None tensor is an optional one that was not given), which have to be
     on the current device, where the call's work is enqueued."""
+    at = -1
     for name, t, shape, dtype in specs:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-    here = -1
-    for name, t, _, _ in specs:
-        if t is None:
-            continue
-        at = t.get_device() if t.is_cuda else -1
+        if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
+            _refuse(name, t, shape, dtype)
         if at < 0:
+            at = t.get_device()
+    if at < 0 or at != torch.cuda.current_device() or any(t is not None and t.get_device() != at for _, t, _, _ in specs):
+        _refuse_device(specs)
+
+
+def _refuse(name, t, shape, dtype):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _refuse_device(specs):
+    for name, t, _, _ in specs:
+        if t is not None and not t.is_cuda:
             raise ValueError(f"{name}: must be on the GPU, found on {t.device}")
-        if here < 0:
-            here = torch.cuda.current_device()
-        if at != here:
+    here = torch.cuda.current_device()
+    for name, t, _, _ in specs:
+        if t is not None and t.get_device() != here:
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
 
 
@@ -645,17 +653,22 @@ def _rows_checks(cfg: Config, sched: dict, ws, first: str, data, names):
     """Checks what every permute / unpermute call takes; returns the tensors' dtype code."""
     if not isinstance(data, torch.Tensor) or data.dtype not in DTYPES:
         raise ValueError(f"{first}: expected a bf16, fp16 or fp32 tensor")
+    if ws is None:
+        raise ValueError("workspace: missing")
     n = ws.numel() if isinstance(ws, torch.Tensor) else -1
     if 0 <= n < 256:
         raise ValueError(f"workspace: {n} bytes, at least 256 are needed")
-    i32 = torch.int32
-    want = {"row_of_slot": ((cfg.S,), i32), "topk_w": ((cfg.T, cfg.k), torch.float32), "topk_idx": ((cfg.T, cfg.k), i32)}
+    specs = [("workspace", ws, (n,), torch.uint8)]
     for name in names:
         if sched.get(name) is None:
             raise ValueError(f"sched[{name!r}]: missing")
-    _required(workspace=ws)
-    return DTYPES[data.dtype], [("workspace", ws, (n,), torch.uint8)] + [
-        (f"sched[{name!r}]", sched[name], *want[name]) for name in names]
+        if name == "row_of_slot":
+            specs.append(("sched['row_of_slot']", sched[name], (cfg.S,), torch.int32))
+        elif name == "topk_w":
+            specs.append(("sched['topk_w']", sched[name], (cfg.T, cfg.k), torch.float32))
+        else:
+            specs.append(("sched['topk_idx']", sched[name], (cfg.T, cfg.k), torch.int32))
+    return DTYPES[data.dtype], specs
 
 
 def _some_sched(sched: dict, names) -> moe_sched:

@@ -1,6 +1,8 @@
 // C ABI of the building-block operators: argument validation, workspace
 // layout and the launch sequence of permute / unpermute and linear.  Host
 // code only.
+#include <initializer_list>
+
 #include "../../include/moe.h"
 #include "common.h"
 #include "launch.h"
@@ -27,7 +29,7 @@ moe_status rows_args(const moe_config* cfg, const moe_sched* sched, int dtype, v
 
 // ---------------------------------------------------------------- linear
 struct LinLayout {
-    size_t tiles, big, rows32, dz, part, total;
+    size_t lists[3], dz, part, sums, total;
 };
 
 moe_status lin_check(const moe_linear_config* c) {
@@ -47,49 +49,35 @@ LinLayout lin_layout(const moe_linear_config& c) {
         n += up256(bytes);
         return here;
     };
-    const size_t pre = (size_t)(c.E + 1) * 4;
-    L.tiles = take(pre);
-    L.big = take(pre);
-    L.rows32 = take(pre);
+    for (size_t& l : L.lists) l = take((size_t)(c.E + 1) * 4);
     L.dz = take(c.act == MOE_ACT_NONE ? 0 : (size_t)c.M * c.N * 2);
     L.part = take(((size_t)(c.M + kLinDzRows - 1) / kLinDzRows + c.E) * c.N * 4);
+    const size_t f = linear_part_floats(linear_plan(c.M, c.E, c.K, c.N, false), c.M, c.N);
+    const size_t b = linear_part_floats(linear_plan(c.M, c.E, c.N, c.K, true), c.M, c.K);
+    L.sums = take((f > b ? f : b) * 4);
     L.total = n;
     return L;
 }
 
-GroupRows lin_group(const moe_linear_config& c, const int32_t* offsets, char* ws) {
-    GroupRows g{};
-    g.E = c.E > 0 ? c.E : 1;
-    g.rows = c.M;
-    g.err = (int32_t*)ws;
-    if (c.E > 0) g.offsets = offsets;
-    else g.dense_rows = c.M;
-    return g;
-}
-
-// The tile forms of one product and, for groups, the prefixes of its tiles
-// (and of the kLinDzRows-row tiles, if wanted) in one launch.
-int lin_tiles(const moe_linear_config& c, const int32_t* offsets, const LinForm& f, int32_t* tiles, int32_t* big,
-              int32_t* rows32, GroupRows& g, hipStream_t st) {
-    if (c.E == 0) {
-        g.tm = f.dense_big ? 256 : f.small;
-        return 0;
+// Fills in the tiles of a call: the offsets, and a list for each set whose
+// blocks do not find their tiles themselves, all lists in one launch.  C: the
+// columns of its product's output.
+struct Tiles {
+    LinTiles* t;
+    int C, tn;
+};
+int lin_tiles(const moe_linear_config& c, const int32_t* offsets, char* ws, const LinLayout& L,
+              std::initializer_list<Tiles> sets, hipStream_t st) {
+    LinPrefix p{};
+    for (const Tiles& s : sets) {
+        s.t->err = (int32_t*)ws;
+        if (c.E == 0) continue;
+        s.t->offsets = offsets;
+        if (s.t->tm == 0 || linear_inline_tiles(*s.t, s.C, s.tn)) continue;
+        s.t->list = (const int32_t*)(ws + L.lists[p.n]);
+        p.t[p.n++] = *s.t;
     }
-    g.tm = f.small;
-    g.tile_off = tiles;
-    LinPrefix p{1, {f.small}, {0}, {f.split ? 256 : INT32_MAX}, {tiles}};
-    auto add = [&](int tm, int lo, int32_t* out) {
-        p.tm[p.n] = tm;
-        p.lo[p.n] = lo;
-        p.hi[p.n] = INT32_MAX;
-        p.out[p.n++] = out;
-    };
-    if (f.split) {
-        add(256, 256, big);
-        g.tile_big = big;
-    }
-    if (rows32) add(kLinDzRows, 0, rows32);
-    return launch_linear_prefix(offsets, c.E, c.M, p, g.err, st);
+    return p.n ? launch_linear_prefix(p, st) : 0;
 }
 
 moe_status lin_common(const moe_linear_config* c, const int32_t* offsets, void* ws, size_t ws_bytes, LinLayout& L) {
@@ -172,13 +160,12 @@ moe_status moe_linear_forward(const moe_linear_config* c, const int32_t* offsets
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
-    LinFwdArgs a{lin_group(*c, offsets, ws), c->dtype, c->act, c->N, c->K, (const uint16_t*)x, (const uint16_t*)w,
-                 (const uint16_t*)bias, (const uint16_t*)residual, (uint16_t*)y, (uint16_t*)z};
-    int32_t *tiles = (int32_t*)(ws + L.tiles), *big = (int32_t*)(ws + L.big);
-    const LinForm f = linear_form(c->M, c->E, c->N, false);
-    a.stream = f.stream;
-    if (lin_tiles(*c, offsets, f, tiles, big, nullptr, a.g, st)) return MOE_ERR_HIP;
-    return launch_linear_fwd(a, st) ? MOE_ERR_HIP : MOE_OK;
+    LinPlan p = linear_plan(c->M, c->E, c->K, c->N, false);
+    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->N, p.stream ? 32 : 128}, {&p.big, c->N, 256}}, st)) return MOE_ERR_HIP;
+    const LinFwdArgs a{{}, c->dtype, c->act, c->N, c->K, (const uint16_t*)x, (const uint16_t*)w,
+                       (const uint16_t*)bias, (const uint16_t*)residual, (uint16_t*)y, (uint16_t*)z, 1,
+                       (float*)(ws + L.sums)};
+    return launch_linear_fwd(p, a, st) ? MOE_ERR_HIP : MOE_OK;
 }
 
 moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offsets, const void* x, const void* w,
@@ -194,19 +181,18 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
-    const GroupRows g = lin_group(*c, offsets, ws);
-    int32_t *tiles = (int32_t*)(ws + L.tiles), *big = (int32_t*)(ws + L.big), *rows32 = (int32_t*)(ws + L.rows32);
-    GroupRows gx = g;                                 // dx's tiles
-    if (lin_tiles(*c, offsets, linear_form(c->M, c->E, c->K, true), tiles, big, rows32, gx, st)) return MOE_ERR_HIP;
+    LinPlan p = linear_plan(c->M, c->E, c->N, c->K, true);
+    LinTiles rows32{nullptr, nullptr, c->E, c->M, kLinDzRows, 0, INT32_MAX, nullptr};
+    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->K, 128}, {&p.big, c->K, 256}, {&rows32, c->N, 512}}, st))
+        return MOE_ERR_HIP;
     uint16_t* dz = (uint16_t*)(ws + L.dz);
-    LinDzArgs d{g, c->dtype, c->act, c->N, (const uint16_t*)dy, (const uint16_t*)z, dz,
-                db ? (float*)(ws + L.part) : nullptr};
-    if (c->E > 0) d.g.tile_off = rows32;
+    float* part = db ? (float*)(ws + L.part) : nullptr;
+    const LinDzArgs d{rows32, c->dtype, c->act, c->N, (const uint16_t*)dy, (const uint16_t*)z, dz, part};
     if ((db || !none) && launch_linear_dz(d, st)) return MOE_ERR_HIP;
-    const LinBwdArgs b{gx, d.g, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x,
-                       (const uint16_t*)w, (uint16_t*)dx, (uint16_t*)dw, (uint16_t*)db, d.part,
-                       linear_dw_form(c->M, c->E, c->N, c->K), 0, 0};
-    if (launch_linear_bwd(b, st)) return MOE_ERR_HIP;
+    const LinBwdArgs b{p.small, rows32, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x,
+                       (const uint16_t*)w, (uint16_t*)dx, (uint16_t*)dw, (uint16_t*)db, part,
+                       (float*)(ws + L.sums), 0, 0};
+    if (launch_linear_bwd(p, b, st)) return MOE_ERR_HIP;
     return MOE_OK;
 }
 

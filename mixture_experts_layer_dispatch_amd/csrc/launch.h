@@ -388,16 +388,32 @@ int launch_unpermute_bwd(const RowsArgs& a, const void* o, const void* dy, const
 enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4, LIN_ACTS = 5 };
 constexpr int kLinDzRows = 32;       // rows of a k_linear_dz tile
 
-struct LinPrefix {
-    int n;                    // prefixes wanted
-    int tm[3];                // rows of a tile
-    int lo[3], hi[3];         // the groups of lo <= n < hi rows
-    int32_t* out[3];          // [E+1]
+// Row tiles of tm rows (0: none) over the groups of lo <= n < hi rows, or over
+// one dense group of `rows` rows (offsets null).
+struct LinTiles {
+    const int32_t* offsets;   // [E+1]
+    const int32_t* list;      // [E+1] tiles before each group (k_linear_prefix), or null: each block counts (E <= 64)
+    int E, rows;              // rows of the whole matrix
+    int tm, lo, hi;
+    int32_t* err;
 };
 
-// g.tile_off null: one dense group of g.dense_rows rows
+// Tiles of one product: the groups of many rows (or the dense group) in 256 x
+// 256 tiles, the others in small ones.
+struct LinPlan {
+    LinTiles small, big;
+    bool stream;              // small: k_linear_stream, 16 or 32 rows
+    bool once;                // small: each weight tile feeds one row tile
+    int ksplit;               // parts the reduction is split into (dense)
+};
+
+struct LinPrefix {
+    int n;                    // sets of tiles whose lists to write
+    LinTiles t[3];
+};
+
 struct LinFwdArgs {
-    GroupRows g;
+    LinTiles t;
     int dtype, act, N, K;
     const uint16_t* x;        // [M, K]
     const uint16_t* w;        // [E, N, K]
@@ -405,11 +421,12 @@ struct LinFwdArgs {
     const uint16_t* residual; // [M, N] or null; may be y
     uint16_t* y;              // [M, N]
     uint16_t* z;              // [M, N] or null
-    int stream;               // k_linear_stream's form, g.tm 16, 32 or 64
+    int ksplit;
+    float* part;              // [ksplit, M, N]
 };
 
 struct LinDzArgs {
-    GroupRows g;              // tile_off: tiles of kLinDzRows rows
+    LinTiles t;               // of kLinDzRows rows
     int dtype, act, N;
     const uint16_t* dy;
     const uint16_t* z;        // read unless act is LIN_NONE
@@ -417,13 +434,10 @@ struct LinDzArgs {
     float* part;              // [tiles, N] column sums, or null
 };
 
-// forms of dW
-enum { LIN_DW_256 = 0, LIN_DW_RING = 1, LIN_DW_FEW = 2 };
-
 // dx, dw, db: null = not wanted
 struct LinBwdArgs {
-    GroupRows g;              // dx's row tiles; dW's groups
-    GroupRows grows;          // the tiles of part (kLinDzRows rows)
+    LinTiles t;               // dx's row tiles; dW's groups
+    LinTiles rows32;          // the tiles of part (kLinDzRows rows)
     int dtype, N, K;
     const uint16_t* dz;       // [M, N]
     const uint16_t* x;
@@ -432,25 +446,18 @@ struct LinBwdArgs {
     uint16_t* dw;
     uint16_t* db;
     const float* part;        // k_linear_dz's column sums
-    int dw_form;
+    float* sums;              // dx's parts, if its plan splits the reduction
     int ndw, ndx;             // (k_linear_bwd: blocks of dW and of dx)
 };
 
-// Tile forms of a product: rows of the small tiles (64 or 128; 16, 32 or 64 of
-// the streaming form); a dense one whole in 256 x 256 tiles; the groups of at
-// least 256 rows in those.
-struct LinForm {
-    int small;
-    bool dense_big, split, stream;
-};
-
 // linear.hip
-LinForm linear_form(int M, int E, int C, bool dx);
-int linear_dw_form(int M, int E, int N, int K);
-int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st);
-int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st);
+LinPlan linear_plan(int M, int E, int R, int C, bool dx);
+size_t linear_part_floats(const LinPlan& p, int M, int C);
+bool linear_inline_tiles(const LinTiles& t, int C, int tn);
+int launch_linear_prefix(const LinPrefix& p, hipStream_t st);
+int launch_linear_fwd(const LinPlan& p, const LinFwdArgs& a, hipStream_t st);
 int launch_linear_dz(const LinDzArgs& a, hipStream_t st);
-int launch_linear_bwd(const LinBwdArgs& a, hipStream_t st);    // all that follows dz
+int launch_linear_bwd(const LinPlan& p, const LinBwdArgs& a, hipStream_t st);    // all that follows dz
 
 // api.hip
 bool device_ok();             // the current device is gfx950

@@ -11,13 +11,14 @@
 // are the rows offsets[e] .. offsets[e + 1] of one macrobatch; no count
 // reaches the host (arex-research.com "Cursor 放出 MoK", design section, second
 // decision): the grid covers an upper bound of tiles and each block finds its
-// tile in a prefix that k_linear_prefix builds.
+// tile from the offsets.
 //
 // N and K are multiples of 8 (16-byte rows), M and the groups are any size:
-// operand chunks past a row's end, a group's end or a matrix's end are read
-// as zeros, results past them are not stored.  Products are sums of fp32 MFMA
-// steps in ascending order of the reduction index; bias, activation and
-// residual are applied to the fp32 sum, which is rounded once.
+// reduction indices past a row's or a group's end are read as zeros, rows and
+// columns past an operand's last are read from its last one and their results
+// are not stored.  Products are sums of fp32 MFMA steps in ascending order of
+// the reduction index (or of a few ascending parts, added in order); bias,
+// activation and residual are applied to the fp32 sum, which is rounded once.
 #include "dtype.h"
 #include "gemm_common.h"
 #include "profile.h"
@@ -34,23 +35,24 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1 / sqrt(2 pi)
 constexpr float kTanhC = 0.79788456080286536f;        // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 
-// The standard normal's distribution function, and e = exp(-z^2 / 2).  With
-// x = |z| / sqrt(2): Phi(-|z|) = erfc(x) / 2 = e erfcx(x) / 2, and erfcx(x) is a
-// polynomial of degree 8 in t = 1 / (1 + 0.43 x), without a constant term,
-// fitted by iteratively reweighted least squares to a relative error of 8.4e-8
-// over x in [0, 9.5] (4.0e-7 with its evaluation in fp32).
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    e = __expf(-0.5f * z * z);
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.304055916f, fabsf(z), 1.0f));
-    float p = 3.685406223e-02f;
-    p = fmaf(p, t, -1.551871300e-01f);
-    p = fmaf(p, t, 1.918536574e-01f);
-    p = fmaf(p, t, -4.286365956e-02f);
-    p = fmaf(p, t, 1.234226599e-01f);
-    p = fmaf(p, t, 1.024754047e-01f);
-    p = fmaf(p, t, 1.221877486e-01f);
-    p = fmaf(p, t, 1.212573051e-01f);
-    const float q = e * (p * t);
+// The standard normal's distribution function, as 2^p(|z|) below zero and one
+// minus that above: log2 of the tail is nearly a parabola, and p is its
+// least-squares fit of degree 7, reweighted towards the least largest error,
+// over |z| <= 6: the tail's relative error is below 6.5e-6 and |z| times its
+// error below 5.6e-7 (with the evaluation in fp32); beyond 6 the tail (1e-9)
+// is taken as 0.  One transcendental instruction and seven fused
+// multiply-adds where erff takes about 40 instructions.
+__device__ __forceinline__ float normal_cdf(float z) {
+    const float a = fabsf(z);
+    float p = -1.834812566e-06f;
+    p = fmaf(p, a, 6.159831682e-05f);
+    p = fmaf(p, a, -9.305250343e-04f);
+    p = fmaf(p, a, 8.507891679e-03f);
+    p = fmaf(p, a, -5.396007077e-02f);
+    p = fmaf(p, a, -4.584643916e-01f);
+    p = fmaf(p, a, -1.151251046e+00f);
+    p = fmaf(p, a, -9.999952944e-01f);
+    const float q = a <= 6.0f ? __builtin_amdgcn_exp2f(p) : 0.0f;
     return z < 0.f ? q : 1.0f - q;
 }
 
@@ -58,10 +60,8 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
 template <int ACT>
 __device__ __forceinline__ float act(float z) {
     if constexpr (ACT == LIN_RELU) return z < 0.f ? 0.f : z;
-    else if constexpr (ACT == LIN_GELU) {
-        float e;
-        return z * normal_cdf(z, e);
-    } else if constexpr (ACT == LIN_GELU_TANH) return z * sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
+    else if constexpr (ACT == LIN_GELU) return z * normal_cdf(z);
+    else if constexpr (ACT == LIN_GELU_TANH) return z * sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
     else if constexpr (ACT == LIN_SILU) return z * sigm(z);
     else return z;
 }
@@ -69,11 +69,8 @@ __device__ __forceinline__ float act(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
     if constexpr (ACT == LIN_RELU) return z > 0.f ? 1.f : 0.f;
-    else if constexpr (ACT == LIN_GELU) {
-        float e;
-        const float c = normal_cdf(z, e);
-        return c + z * e * kInvSqrt2Pi;
-    } else if constexpr (ACT == LIN_GELU_TANH) {
+    else if constexpr (ACT == LIN_GELU) return normal_cdf(z) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+    else if constexpr (ACT == LIN_GELU_TANH) {
         const float p = sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
         return p + z * p * (1.0f - p) * 2.0f * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
     } else if constexpr (ACT == LIN_SILU) {
@@ -82,21 +79,31 @@ __device__ __forceinline__ float act_grad(float z) {
     } else return 1.f;
 }
 
-// ================================================================ tile prefixes
-// One block: for each list q, out[q][e] = sum over e' < e of
-// ceil(n_e' / tm[q]) over the groups with lo[q] <= n < hi[q] rows.
-__global__ __launch_bounds__(1024) void k_linear_prefix(const int32_t* __restrict__ offsets, int E, int rows,
-                                                        LinPrefix p, int32_t* __restrict__ err) {
-    __shared__ int32_t wsum[16];
-    const int e = threadIdx.x, lane = lane_id(), wv = threadIdx.x >> 6;
-    int cnt = 0;
-    if (e < E) {
-        const int a = offsets[e], b = offsets[e + 1];
-        if (a < 0 || b < a || b > rows) raise_err(err, ERR_BAD_OFFSETS);
-        else cnt = b - a;
+// ================================================================ row tiles
+// The rows of group e, 0 if its offsets are not ascending inside the matrix.
+__device__ __forceinline__ int group_rows(const LinTiles& t, int e, int& lo, bool tell) {
+    const int a = t.offsets[e], b = t.offsets[e + 1];
+    lo = a;
+    if (a < 0 || b < a || b > t.rows) {
+        if (tell) raise_err(t.err, ERR_BAD_OFFSETS);
+        return 0;
     }
+    return b - a;
+}
+
+__device__ __forceinline__ int group_tiles(const LinTiles& t, int n) {
+    return n >= t.lo && n < t.hi ? (n + t.tm - 1) / t.tm : 0;
+}
+
+// One block: for each of up to three sets of tiles, list[e] = the tiles of the
+// groups before e, list[E] their number.
+__global__ __launch_bounds__(1024) void k_linear_prefix(LinPrefix p) {
+    __shared__ int32_t wsum[16];
+    const int E = p.t[0].E, e = threadIdx.x, lane = lane_id(), wv = threadIdx.x >> 6;
+    int lo, cnt = 0;
+    if (e < E) cnt = group_rows(p.t[0], e, lo, true);
     for (int q = 0; q < p.n; ++q) {
-        const int n = cnt >= p.lo[q] && cnt < p.hi[q] ? (cnt + p.tm[q] - 1) / p.tm[q] : 0;
+        const int n = e < E ? group_tiles(p.t[q], cnt) : 0;
         int incl = n;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -107,10 +114,96 @@ __global__ __launch_bounds__(1024) void k_linear_prefix(const int32_t* __restric
         __syncthreads();
         int pre = incl - n;
         for (int v = 0; v < wv; ++v) pre += wsum[v];
-        if (e < E) p.out[q][e] = pre;
-        if (e == E - 1) p.out[q][E] = pre + n;
+        int32_t* out = const_cast<int32_t*>(p.t[q].list);
+        if (e < E) out[e] = pre;
+        if (e == E - 1) out[E] = pre + n;
         __syncthreads();
     }
+}
+
+// The same by one wave, for at most 64 groups: lane e has group e's first row,
+// rows and the tiles before it; returns their number.  Saves a launch where the
+// product itself is short (grouped products of few tiles: 15 -> 11 us a call).
+struct WaveTiles {
+    int lo, n, pre, total;
+};
+__device__ __forceinline__ WaveTiles wave_tiles(const LinTiles& t, bool tell) {
+    const int lane = lane_id();
+    WaveTiles w{0, 0, 0, 0};
+    if (lane < t.E) w.n = group_rows(t, lane, w.lo, tell);
+    const int n = lane < t.E ? group_tiles(t, w.n) : 0;
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(incl, off);
+        if (lane >= off) incl += o;
+    }
+    w.pre = incl - n;
+    w.total = __builtin_amdgcn_readlane(incl, 63);
+    return w;
+}
+
+// Block b's tile: expert e, rows lo .. hi - 1, column tile nt, and its number
+// mt among the row tiles.  An XCD's consecutive tiles are BAND row tiles by the
+// column tiles one after the other: with 256 x 256 tiles and BAND 4, 4 by 8
+// for its 32 CUs, so that its L2 holds 12 operand strips for 32 tiles.
+template <int TM, int BAND>
+__device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int& e, int& lo, int& hi, int& nt,
+                                         int& mt) {
+    WaveTiles w;
+    int ntiles;
+    if (!t.offsets) ntiles = (t.rows + TM - 1) / TM;
+    else if (t.list) ntiles = t.list[t.E];
+    else {
+        w = wave_tiles(t, b == 0);
+        ntiles = w.total;
+    }
+    if (b >= ntiles * nNt) return false;
+    const int L = xcd_remap(b, ntiles * nNt);
+    const int band = L / (BAND * nNt), r = L - band * BAND * nNt, rows = min(BAND, ntiles - BAND * band);
+    nt = r / rows;
+    mt = BAND * band + (r - nt * rows);
+    if (!t.offsets) {
+        e = 0;
+        lo = mt * TM;
+        hi = min(lo + TM, t.rows);
+        return true;
+    }
+    if (t.list) {
+        int a = 0, z = t.E;
+        while (z - a > 1) {
+            const int mid = (a + z) >> 1;
+            if (t.list[mid] <= mt) a = mid;
+            else z = mid;
+        }
+        e = a;
+        const int a0 = t.offsets[e];
+        lo = a0 + (mt - t.list[e]) * TM;
+        hi = min(lo + TM, t.offsets[e + 1]);
+    } else {
+        // the last group whose tiles start at or before mt (one without tiles starts where the next one does)
+        const uint64_t m = __ballot(lane_id() < t.E && w.pre <= mt);
+        e = 63 - __builtin_clzll(m);
+        const int a0 = __builtin_amdgcn_readlane(w.lo, e), n = __builtin_amdgcn_readlane(w.n, e);
+        lo = a0 + (mt - __builtin_amdgcn_readlane(w.pre, e)) * TM;
+        hi = min(lo + TM, a0 + n);
+    }
+    return true;
+}
+
+// dW: block b's expert e, tile (mt, nt) of nMt by nNt, and the expert's rows lo, n.
+__device__ __forceinline__ bool lin_wtile(const LinTiles& t, int nMt, int nNt, int b, int& e, int& mt, int& nt,
+                                          int& lo, int& n) {
+    const int per = nMt * nNt, total = (t.offsets ? t.E : 1) * per;
+    if (b >= total) return false;
+    const int L = xcd_remap(b, total), rem = L % per;
+    e = L / per;
+    mt = rem / nNt;
+    nt = rem - mt * nNt;
+    lo = 0;
+    n = t.rows;
+    if (t.offsets) n = group_rows(t, e, lo, true);
+    return true;
 }
 
 // ================================================================ 64 / 128 x 128 tiles
@@ -137,18 +230,21 @@ __device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int64_t row,
     *(uint2*)(a.y + at) = make_uint2(D::pack2(z[0], z[1]), D::pack2(z[2], z[3]));
 }
 
-template <class D, int ACT, int TM>
+// ONCE: a weight tile feeds one row tile, so it is copied non-temporally (512
+// experts of 40 rows, 4.3 GB of weights: 801 -> 698 us, 6.45 TB/s; where two
+// row tiles read it: 39 -> 46 us).
+template <class D, int ACT, int TM, bool ONCE>
 __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
     constexpr int TN = 128;
-    int e, lo, hi, nt;
-    if (!map_mtile<TM>(a.g, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
     const int n0 = nt * TN;
     T1_RING(ring, TM, lin_stages<TM>());
     T1Acc<TM> acc;
     {
         const TileOperand<false, TM, 1, kT1Threads> oa(a.x, a.K, lo, hi);
-        const TileOperand<false, TN, 1, kT1Threads> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N);
-        t1_mainloop<D, false, false, TM, lin_stages<TM>()>(oa, ob, a.K, acc, ring);
+        const TileOperand<false, TN, 1, kT1Threads, ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N);
+        t1_mainloop<D, false, false, TM, lin_stages<TM>(), ONCE>(oa, ob, a.K, acc, ring);
     }
     AccPos<TM, TN> pos;
 #pragma unroll
@@ -163,19 +259,64 @@ __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(Lin
     }
 }
 
+// ================================================================ split reductions
+// Too few tiles for the chip (dense): each tile's reduction is split into
+// ksplit ascending parts of whole 64-deep steps, a block each, whose fp32 sums
+// k_linear_sum adds in order (128 x 4096 x 4096: @SPLIT@).  N: output columns,
+// K: reduction length, w: [N, K], or (BKS) [K, N].
+template <class D, bool BKS, int TM>
+__global__ __launch_bounds__(kT1Threads, 1) void k_linear_part(LinFwdArgs a) {
+    constexpr int TN = 128;
+    const int part = blockIdx.x % a.ksplit;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x / a.ksplit, e, lo, hi, nt, mt)) return;
+    const int steps = (a.K + kTK - 1) / kTK, k0 = steps * part / a.ksplit * kTK;
+    const int k1 = min(steps * (part + 1) / a.ksplit * kTK, a.K), n0 = nt * TN;
+    T1_RING(ring, TM, 4);
+    T1Acc<TM> acc;
+    {
+        const TileOperand<false, TM, 1, kT1Threads> oa(a.x + k0, a.K, lo, hi);
+        const TileOperand<BKS, TN, 1, kT1Threads> ob(BKS ? a.w + (int64_t)k0 * a.N : a.w + k0, BKS ? a.N : a.K, n0, a.N);
+        t1_mainloop<D, false, BKS, TM, 4>(oa, ob, k1 - k0, acc, ring);
+    }
+    AccPos<TM, TN> pos;
+#pragma unroll
+    for (int mb = 0; mb < TM / 32; ++mb) {
+        const int row = lo + pos.m(mb);
+        if (row >= hi) continue;
+#pragma unroll
+        for (int nb = 0; nb < TN / 32; ++nb) {
+            const int col = n0 + pos.n(nb);
+            if (col < a.N) *(f32x4*)(a.part + ((int64_t)part * a.t.rows + row) * a.N + col) = acc[mb][nb];
+        }
+    }
+}
+
+template <class D, int ACT>
+__global__ __launch_bounds__(256) void k_linear_sum(LinFwdArgs a) {
+    const int n4 = a.N / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / n4;
+    if (row >= a.t.rows) return;
+    const int col = (int)(i - row * n4) * 4;
+    f32x4 v = *(const f32x4*)(a.part + row * a.N + col);
+    for (int q = 1; q < a.ksplit; ++q) v += *(const f32x4*)(a.part + ((int64_t)q * a.t.rows + row) * a.N + col);
+    lin_out<D, ACT>(a, 0, row, col, v);
+}
+
 // ================================================================ few rows
 // A handful of rows: the weights are read once and everything else is small,
 // so the product is a stream.  A block computes 16 MB rows by 16 NB columns;
 // its W waves split the reduction, each reading pieces of S * 64 bytes of every
 // weight row (neighbouring waves neighbouring pieces) straight into MFMA
 // fragments: no LDS and no barrier until the waves' sums are added, in wave
-// order, at the end.  The loads run one unit ahead.
+// order, at the end.  The loads run one unit ahead.  (Non-temporal loads of the
+// weights: 4 x 4096 x 4096 10.1 -> 10.4 us, 160 rows at 512 experts 190 -> 221.)
 template <class D, int ACT, int MB, int NB, int S, int W>
 __global__ __launch_bounds__(64 * W) void k_linear_stream(LinFwdArgs a) {
     constexpr int TM = 16 * MB, TN = 16 * NB, U = 32 * S;
     __shared__ f32x4 sums[W][MB * NB][64];
-    int e, lo, hi, nt;
-    if (!map_mtile<TM>(a.g, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt)) return;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
     const int lane = lane_id(), wv = wave_id(), j = lane & 15, kg = 8 * (lane >> 4);
     const uint16_t *xp[MB], *wp[NB];
 #pragma unroll
@@ -252,17 +393,17 @@ __global__ __launch_bounds__(64 * W) void k_linear_stream(LinFwdArgs a) {
 
 // ================================================================ backward, small tiles
 // dx = dz W: W read with its row (the reduction index n) as the memory row
-template <class D, int TM>
+template <class D, int TM, bool ONCE>
 __device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
     constexpr int TN = 128;
-    int e, lo, hi, nt;
-    if (!map_mtile<TM>(a.g, (a.K + TN - 1) / TN, block, e, lo, hi, nt)) return;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, 1>(a.t, (a.K + TN - 1) / TN, block, e, lo, hi, nt, mt)) return;
     const int n0 = nt * TN;
     T1Acc<TM> acc;
     {
         const TileOperand<false, TM, 1, kT1Threads> oa(a.dz, a.N, lo, hi);
-        const TileOperand<true, TN, 1, kT1Threads> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
-        t1_mainloop<D, false, true, TM, lin_stages<TM>()>(oa, ob, a.N, acc, ring);
+        const TileOperand<true, TN, 1, kT1Threads, ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
+        t1_mainloop<D, false, true, TM, lin_stages<TM>(), ONCE>(oa, ob, a.N, acc, ring);
     }
     AccPos<TM, TN> pos;
 #pragma unroll
@@ -279,10 +420,10 @@ __device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1
     }
 }
 
-template <class D, int TM>
+template <class D, int TM, bool ONCE>
 __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
     T1_RING(ring, TM, lin_stages<TM>());
-    dx_tile<D, TM>(a, blockIdx.x, ring);
+    dx_tile<D, TM, ONCE>(a, blockIdx.x, ring);
 }
 
 // dW = dz^T x over a group's rows: both operands with the row as the memory row
@@ -290,7 +431,7 @@ template <class D>
 __device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
     constexpr int TM = 128, TN = 128;
     int e, mt, nt, lo, n;
-    if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
+    if (!lin_wtile(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
     T1Acc<TM> acc;
     {
@@ -331,7 +472,7 @@ __global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
     __shared__ __attribute__((aligned(16))) uint16_t sm[TM * TN];
     static_assert(TM * TN == 2 * kT2Half, "the operands' stage and the tile take the same LDS");
     int e, mt, nt, lo, n;
-    if (!map_ktile(a.g, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
+    if (!lin_wtile(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
     uint16_t *const sa = sm, *const sb = sm + kT2Half;
     T1Acc<TM> acc;
@@ -381,18 +522,22 @@ __global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
 // db[e] = the sum of its tiles' partial rows (k_linear_dz): 64 columns of an
 // expert, `waves` waves over the tiles
 template <class D>
-__device__ __forceinline__ void db_columns(const float* part, const GroupRows& g, int N, int block, int waves,
+__device__ __forceinline__ void db_columns(const float* part, const LinTiles& t, int N, int block, int waves,
                                            float* sums, uint16_t* db) {
     const int nc = (N + 63) / 64;
     const int e = block / nc, col = (block % nc) * 64 + lane_id(), wv = wave_id();
-    int t0 = 0, t1 = (g.dense_rows + kLinDzRows - 1) / kLinDzRows;
-    if (g.tile_off) {
-        t0 = g.tile_off[e];
-        t1 = g.tile_off[e + 1];
+    int t0 = 0, t1 = (t.rows + t.tm - 1) / t.tm;
+    if (t.offsets && t.list) {
+        t0 = t.list[e];
+        t1 = t.list[e + 1];
+    } else if (t.offsets) {
+        const WaveTiles w = wave_tiles(t, false);
+        t0 = __builtin_amdgcn_readlane(w.pre, e);
+        t1 = t0 + group_tiles(t, __builtin_amdgcn_readlane(w.n, e));
     }
     float s = 0.f;
     if (col < N)
-        for (int t = t0 + wv; t < t1; t += waves) s += part[(int64_t)t * N + col];
+        for (int i = t0 + wv; i < t1; i += waves) s += part[(int64_t)i * N + col];
     sums[wv * 64 + lane_id()] = s;
     __syncthreads();
     if (wv > 0 || col >= N) return;
@@ -411,43 +556,15 @@ __global__ __launch_bounds__(kT1Threads, 1) void k_linear_bwd(LinBwdArgs a) {
         return;
     }
     b -= a.ndw;
-    if (b < a.ndx) dx_tile<D, 128>(a, b, ring);
-    else db_columns<D>(a.part, a.grows, a.N, b - a.ndx, kT1Threads / 64, (float*)ring.a0, a.db);
+    if (b < a.ndx) dx_tile<D, 128, false>(a, b, ring);
+    else db_columns<D>(a.part, a.rows32, a.N, b - a.ndx, kT1Threads / 64, (float*)ring.a0, a.db);
 }
 
 // ================================================================ 256 x 256 tiles
-// Tile b of the groups in tile_big (or of the dense group) with nNt column
-// tiles: an XCD's consecutive tiles are 4 row tiles by 8 column tiles, so that
-// its L2 holds 12 operand strips for 32 tiles.
-__device__ __forceinline__ bool map_tile256(const GroupRows& g, int nNt, int b, int& e, int& lo, int& hi, int& nt) {
-    const int ntiles = g.tile_off ? g.tile_big[g.E] : (g.dense_rows + 255) / 256;
-    if (b >= ntiles * nNt) return false;
-    const int L = xcd_remap(b, ntiles * nNt);
-    const int band = L / (4 * nNt), r = L - band * 4 * nNt, rows = min(4, ntiles - 4 * band);
-    nt = r / rows;
-    const int mt = 4 * band + (r - nt * rows);
-    if (!g.tile_off) {
-        e = 0;
-        lo = mt * 256;
-        hi = min(lo + 256, g.dense_rows);
-        return true;
-    }
-    int a = 0, z = g.E;
-    while (z - a > 1) {
-        const int mid = (a + z) >> 1;
-        if (g.tile_big[mid] <= mt) a = mid;
-        else z = mid;
-    }
-    e = a;
-    lo = g.offsets[e] + (mt - g.tile_big[e]) * 256;
-    hi = min(lo + 256, g.offsets[e + 1]);
-    return true;
-}
-
 template <class D, int ACT>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
-    int e, lo, hi, nt;
-    if (!map_tile256(a.g, (a.N + 255) / 256, blockIdx.x, e, lo, hi, nt)) return;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<256, 4>(a.t, (a.N + 255) / 256, blockIdx.x, e, lo, hi, nt, mt)) return;
     T2_LDS(lds);
     T2Acc acc;
     {
@@ -499,8 +616,8 @@ __device__ __forceinline__ void t2_store(const T2Lds& lds, uint16_t* out, int r0
 
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
-    int e, lo, hi, nt;
-    if (!map_tile256(a.g, (a.K + 255) / 256, blockIdx.x, e, lo, hi, nt)) return;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<256, 4>(a.t, (a.K + 255) / 256, blockIdx.x, e, lo, hi, nt, mt)) return;
     T2_LDS(lds);
     T2Acc acc;
     {
@@ -514,7 +631,7 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
     int e, mt, nt, lo, n;
-    if (!map_ktile(a.g, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
+    if (!lin_wtile(a.t, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
     T2_LDS(lds);
     T2Acc acc;
     {
@@ -533,8 +650,8 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
 template <class D, int ACT, int TR>
 __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
     __shared__ float sums[3][64][8];
-    int e, lo, hi, nt;
-    if (!map_mtile<TR>(a.g, (a.N + 511) / 512, blockIdx.x, e, lo, hi, nt)) return;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TR, 1>(a.t, (a.N + 511) / 512, blockIdx.x, e, lo, hi, nt, mt)) return;
     const int lane = lane_id(), wv = wave_id();
     const int col = nt * 512 + lane * 8;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -565,8 +682,7 @@ __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
     for (int v = 0; v < 3; ++v)
 #pragma unroll
         for (int q = 0; q < 8; ++q) s[q] += sums[v][lane][q];
-    const int tile = a.g.tile_off ? a.g.tile_off[e] + (lo - a.g.offsets[e]) / TR : lo / TR;
-    float* p = a.part + (int64_t)tile * a.N + col;
+    float* p = a.part + (int64_t)mt * a.N + col;
     *(float4*)p = make_float4(s[0], s[1], s[2], s[3]);
     *(float4*)(p + 4) = make_float4(s[4], s[5], s[6], s[7]);
 }
@@ -574,26 +690,76 @@ __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
 template <class D>
 __global__ __launch_bounds__(1024) void k_linear_db(LinBwdArgs a) {
     __shared__ float sums[16 * 64];
-    db_columns<D>(a.part, a.grows, a.N, blockIdx.x, 16, sums, a.db);
+    db_columns<D>(a.part, a.rows32, a.N, blockIdx.x, 16, sums, a.db);
 }
 
 // ================================================================ launchers
-// upper bound of the row tiles of the groups (or of the dense group)
-static int64_t row_tiles(const GroupRows& g, int tm) {
-    if (!g.tile_off) return ((int64_t)g.dense_rows + tm - 1) / tm;
-    const int64_t b = ((int64_t)g.rows + (int64_t)g.E * (tm - 1)) / tm;
-    return b < g.rows ? b : g.rows;
-}
-
 static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
 
-int launch_linear_prefix(const int32_t* offsets, int E, int rows, const LinPrefix& p, int32_t* err, hipStream_t st) {
+// upper bound of the tiles of a set
+static int64_t max_tiles(const LinTiles& t) {
+    if (t.tm == 0) return 0;
+    if (!t.offsets) return ((int64_t)t.rows + t.tm - 1) / t.tm;
+    // groups of n >= lo rows take ceil(n / tm) tiles: at most rows / tm + groups, groups <= rows / lo
+    const int64_t groups = t.lo > 1 && t.rows / t.lo < t.E ? t.rows / t.lo : t.rows < t.E ? t.rows : t.E;
+    return ((int64_t)t.rows + groups * (t.tm - 1)) / t.tm;
+}
+
+// The tiles of a product with C output columns and R reduction indices: x W^T,
+// or (dx) dz W.
+LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
+    LinPlan p{};
+    p.ksplit = 1;
+    p.small = {nullptr, nullptr, E, M, 0, 0, INT32_MAX, nullptr};
+    p.big = p.small;
+    if (E > 0) {
+        p.small.tm = M >= 128LL * E ? 128 : 64;
+        // few rows and few tiles: latency, which the streaming form splits over eight waves
+        if (!dx && M <= 8LL * E && max_tiles(p.small) * ((C + 127) / 128) < 2048) {
+            p.stream = true;
+            p.small.tm = 16;
+            return p;
+        }
+        p.once = M <= 64LL * E;
+        if (M >= 192LL * E) {
+            p.small.hi = 256;
+            p.big.tm = 256;
+            p.big.lo = 256;
+        }
+        return p;
+    }
+    if (!dx && M <= 32) {
+        p.stream = true;
+        p.small.tm = M <= 16 ? 16 : 32;
+        return p;
+    }
+    if (((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 128) {
+        p.big.tm = 256;
+        return p;
+    }
+    p.small.tm = M <= 64 ? 64 : 128;
+    const int64_t tiles = max_tiles(p.small) * ((C + 127) / 128);
+    const int64_t ks = 256 / tiles < R / 256 ? 256 / tiles : R / 256;
+    p.ksplit = ks < 2 ? 1 : ks < 16 ? (int)ks : 16;
+    return p;
+}
+
+size_t linear_part_floats(const LinPlan& p, int M, int C) {
+    return p.ksplit > 1 ? (size_t)p.ksplit * M * C : 0;
+}
+
+// Whether the blocks of a product find their tiles themselves (LinTiles.list null)
+bool linear_inline_tiles(const LinTiles& t, int C, int tn) {
+    return t.E <= 64 && max_tiles(t) * ((C + tn - 1) / tn) <= 1024;
+}
+
+int launch_linear_prefix(const LinPrefix& p, hipStream_t st) {
     ProfScope prof_(st, "linear_prefix");
-    k_linear_prefix<<<1, 1024, 0, st>>>(offsets, E, rows, p, err);
+    k_linear_prefix<<<1, 1024, 0, st>>>(p);
     return ok();
 }
 
-template <class D, class F>
+template <class F>
 static int with_act(int act, const F& f) {
     switch (act) {
         case LIN_RELU: return f(std::integral_constant<int, LIN_RELU>{});
@@ -604,125 +770,118 @@ static int with_act(int act, const F& f) {
     }
 }
 
-// The groups in tiles of 256 rows come first, the others follow in a launch
-// of their own; a dense product is one or the other.
-static int64_t big_tiles(const GroupRows& g) {
-    if (!g.tile_off) return g.tm == 256 ? ((int64_t)g.dense_rows + 255) / 256 : 0;
-    if (!g.tile_big) return 0;
-    // groups of n >= 256 rows take ceil(n / 256) <= n / 128 tiles
-    const int64_t x = (int64_t)g.rows / 128, y = ((int64_t)g.rows + (int64_t)g.E * 255) / 256;
-    return x < y ? x : y;
-}
-
-// Row tiles and forms of x W^T with C output columns (or, `dx`, of dz W).
-LinForm linear_form(int M, int E, int C, bool dx) {
-    const int64_t groups = E > 0 ? E : 1;
-    LinForm f{};
-    f.small = M >= 128 * groups ? 128 : 64;
-    if (!dx && (E == 0 ? M <= 512 : M <= 8 * groups)) {
-        f.stream = true;
-        f.small = E > 0 || M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        return f;
-    }
-    if (E == 0) f.dense_big = ((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 128;
-    else f.split = M >= 192 * groups;
-    return f;
-}
-
-// Forms of dW: 256 x 256 tiles, the ring of 128 x 128 tiles, or the form of few rows.
-int linear_dw_form(int M, int E, int N, int K) {
-    const int64_t groups = E > 0 ? E : 1;
-    if (M >= 256 * groups)
-        return groups * ((N + 255) / 256) * ((K + 255) / 256) >= 128 ? LIN_DW_256 : LIN_DW_RING;
-    return LIN_DW_FEW;
+template <class K, class A>
+static int go(K kern, int64_t grid, int threads, const A& a, hipStream_t st) {
+    if (grid <= 0) return 0;
+    kern<<<(unsigned)grid, threads, 0, st>>>(a);
+    return ok();
 }
 
 template <class D>
-static int fwd_(const LinFwdArgs& a, hipStream_t st) {
-    return with_act<D>(a.act, [&](auto A) {
-        const int64_t big = big_tiles(a.g) * ((a.N + 255) / 256);
-        if (big > 0) {
-            k_linear_fwd256<D, A()><<<(unsigned)big, kT2Threads, 0, st>>>(a);
-            if (ok()) return -1;
+static int sum_parts(const LinFwdArgs& a, hipStream_t st) {
+    const int64_t grid = ((int64_t)a.t.rows * (a.N / 4) + 255) / 256;
+    return with_act(a.act, [&](auto A) { return go(k_linear_sum<D, A()>, grid, 256, a, st); });
+}
+
+template <class D>
+static int fwd_(const LinPlan& p, LinFwdArgs a, hipStream_t st) {
+    if (p.ksplit > 1) {
+        a.t = p.small;
+        a.ksplit = p.ksplit;
+        const int64_t grid = max_tiles(a.t) * ((a.N + 127) / 128) * a.ksplit;
+        if (a.t.tm == 128 ? go(k_linear_part<D, false, 128>, grid, kT1Threads, a, st)
+                          : go(k_linear_part<D, false, 64>, grid, kT1Threads, a, st))
+            return -1;
+        return sum_parts<D>(a, st);
+    }
+    return with_act(a.act, [&](auto A) {
+        if (p.big.tm) {
+            a.t = p.big;
+            if (go(k_linear_fwd256<D, A()>, max_tiles(a.t) * ((a.N + 255) / 256), kT2Threads, a, st)) return -1;
         }
-        if (a.g.tm == 256) return 0;
-        if (a.stream) {
-            auto go = [&](auto kern, int tn, int waves) {
-                kern<<<(unsigned)(row_tiles(a.g, a.g.tm) * ((a.N + tn - 1) / tn)), 64 * waves, 0, st>>>(a);
-                return ok();
-            };
-            const bool dense = !a.g.tile_off;
-            if (a.g.tm == 16) {
-                if (dense) return go(k_linear_stream<D, A(), 1, 1, 4, 8>, 16, 8);
-                return go(k_linear_stream<D, A(), 1, 2, 4, 8>, 32, 8);
-            }
-            if (a.g.tm == 32) return go(k_linear_stream<D, A(), 2, 1, 4, 8>, 16, 8);
-            if (a.g.dense_rows <= 64) return go(k_linear_stream<D, A(), 4, 1, 2, 8>, 16, 8);
-            return go(k_linear_stream<D, A(), 4, 4, 2, 8>, 64, 8);
+        if (!p.small.tm) return 0;
+        a.t = p.small;
+        const int64_t tiles = max_tiles(a.t);
+        if (p.stream) {
+            const int n16 = (a.N + 15) / 16;
+            if (a.t.tm == 16 && a.t.offsets) return go(k_linear_stream<D, A(), 1, 2, 4, 8>, tiles * ((n16 + 1) / 2), 512, a, st);
+            if (a.t.tm == 16) return go(k_linear_stream<D, A(), 1, 1, 4, 8>, tiles * n16, 512, a, st);
+            return go(k_linear_stream<D, A(), 2, 1, 4, 8>, tiles * n16, 512, a, st);
         }
-        const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.N + 127) / 128);
-        if (a.g.tm == 128) k_linear_fwd<D, A(), 128><<<(unsigned)grid, 256, 0, st>>>(a);
-        else k_linear_fwd<D, A(), 64><<<(unsigned)grid, 256, 0, st>>>(a);
-        return ok();
+        const int64_t grid = tiles * ((a.N + 127) / 128);
+        if (a.t.tm == 128) return go(k_linear_fwd<D, A(), 128, false>, grid, kT1Threads, a, st);
+        if (p.once) return go(k_linear_fwd<D, A(), 64, true>, grid, kT1Threads, a, st);
+        return go(k_linear_fwd<D, A(), 64, false>, grid, kT1Threads, a, st);
     });
 }
 
-int launch_linear_fwd(const LinFwdArgs& a, hipStream_t st) {
+int launch_linear_fwd(const LinPlan& p, const LinFwdArgs& a, hipStream_t st) {
     ProfScope prof_(st, "linear_fwd");
-    return a.dtype == 0 ? fwd_<Bf16>(a, st) : fwd_<Fp16>(a, st);
+    return a.dtype == 0 ? fwd_<Bf16>(p, a, st) : fwd_<Fp16>(p, a, st);
 }
 
 template <class D>
-static int dx_(const LinBwdArgs& a, hipStream_t st) {
-    const int64_t big = big_tiles(a.g) * ((a.K + 255) / 256);
-    if (big > 0) {
-        k_linear_dx256<D><<<(unsigned)big, kT2Threads, 0, st>>>(a);
-        if (ok()) return -1;
-    }
-    if (a.g.tm == 256) return 0;
-    const int64_t grid = row_tiles(a.g, a.g.tm) * ((a.K + 127) / 128);
-    if (a.g.tm == 128) k_linear_dx<D, 128><<<(unsigned)grid, 256, 0, st>>>(a);
-    else k_linear_dx<D, 64><<<(unsigned)grid, 256, 0, st>>>(a);
-    return ok();
+static int dz_(const LinDzArgs& a, hipStream_t st) {
+    const int64_t grid = max_tiles(a.t) * ((a.N + 511) / 512);
+    return with_act(a.act, [&](auto A) { return go(k_linear_dz<D, A(), kLinDzRows>, grid, 256, a, st); });
 }
 
+int launch_linear_dz(const LinDzArgs& a, hipStream_t st) {
+    ProfScope prof_(st, "linear_dz");
+    return a.dtype == 0 ? dz_<Bf16>(a, st) : dz_<Fp16>(a, st);
+}
+
+template <class D>
+static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
+    if (p.ksplit > 1) {                        // dz W as the sum of its parts
+        LinFwdArgs f{p.small, a.dtype, LIN_NONE, a.K, a.N, a.dz, a.w, nullptr, nullptr, a.dx, nullptr, p.ksplit, a.sums};
+        const int64_t grid = max_tiles(f.t) * ((a.K + 127) / 128) * p.ksplit;
+        if (p.small.tm == 128 ? go(k_linear_part<D, true, 128>, grid, kT1Threads, f, st)
+                              : go(k_linear_part<D, true, 64>, grid, kT1Threads, f, st))
+            return -1;
+        return sum_parts<D>(f, st);
+    }
+    if (p.big.tm) {
+        a.t = p.big;
+        if (go(k_linear_dx256<D>, max_tiles(a.t) * ((a.K + 255) / 256), kT2Threads, a, st)) return -1;
+    }
+    if (!p.small.tm) return 0;
+    a.t = p.small;
+    const int64_t grid = max_tiles(a.t) * ((a.K + 127) / 128);
+    if (a.t.tm == 128) return go(k_linear_dx<D, 128, false>, grid, kT1Threads, a, st);
+    if (p.once) return go(k_linear_dx<D, 64, true>, grid, kT1Threads, a, st);
+    return go(k_linear_dx<D, 64, false>, grid, kT1Threads, a, st);
+}
+
+// dW: 256 x 256 tiles, the ring of 128 x 128 tiles, or the form of few rows.
 template <class D>
 static int dw_(const LinBwdArgs& a, hipStream_t st) {
-    const int64_t groups = a.g.offsets ? a.g.E : 1;
-    if (a.dw_form == LIN_DW_256) {
-        const int64_t grid = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-        k_linear_dw256<D><<<(unsigned)grid, kT2Threads, 0, st>>>(a);
-        return ok();
-    }
-    const int64_t grid = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-    if (a.dw_form == LIN_DW_RING) k_linear_dw<D><<<(unsigned)grid, kT1Threads, 0, st>>>(a);
-    else k_linear_dw_few<D><<<(unsigned)grid, kT1Threads, 0, st>>>(a);
-    return ok();
+    const int64_t groups = a.t.offsets ? a.t.E : 1, M = a.t.rows;
+    const int64_t t256 = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+    const int64_t t128 = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+    if (M < 256 * groups) return go(k_linear_dw_few<D>, t128, kT1Threads, a, st);
+    if (t256 >= 128) return go(k_linear_dw256<D>, t256, kT2Threads, a, st);
+    return go(k_linear_dw<D>, t128, kT1Threads, a, st);
 }
 
 template <class D>
-static int db_(const LinBwdArgs& a, hipStream_t st) {
-    const int64_t grid = (int64_t)(a.grows.tile_off ? a.grows.E : 1) * ((a.N + 63) / 64);
-    k_linear_db<D><<<(unsigned)grid, 1024, 0, st>>>(a);
-    return ok();
-}
-
-template <class D>
-static int bwd_(LinBwdArgs a, hipStream_t st) {
-    const int64_t groups = a.g.offsets ? a.g.E : 1;
+static int bwd_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
+    const int64_t groups = a.t.offsets ? a.t.E : 1;
     const int64_t ndw = a.dw ? groups * ((a.N + 127) / 128) * ((a.K + 127) / 128) : 0;
-    const int64_t ndx = a.dx ? row_tiles(a.g, 128) * ((a.K + 127) / 128) : 0;
+    const int64_t ndx = a.dx ? max_tiles(p.small) * ((a.K + 127) / 128) : 0;
     const int64_t ndb = a.db ? groups * ((a.N + 63) / 64) : 0;
-    if (a.g.tm == 128 && !a.g.tile_big && (ndw > 0) + (ndx > 0) + (ndb > 0) > 1 && ndw + ndx + ndb <= 512) {
+    // one launch where the tiles leave CUs idle, unless dx's few long ones would be its length
+    if (p.small.tm == 128 && !p.big.tm && (ndw > 0) + (ndx > 0) + (ndb > 0) > 1 && ndw + ndx + ndb <= 512 &&
+        (p.ksplit == 1 || a.N <= 24 * kTK)) {
         ProfScope prof_(st, "linear_bwd");
+        a.t = p.small;
         a.ndw = (int)ndw;
         a.ndx = (int)ndx;
-        k_linear_bwd<D><<<(unsigned)(ndw + ndx + ndb), kT1Threads, 0, st>>>(a);
-        return ok();
+        return go(k_linear_bwd<D>, ndw + ndx + ndb, kT1Threads, a, st);
     }
     if (a.db) {
         ProfScope prof_(st, "linear_db");
-        if (db_<D>(a, st)) return -1;
+        if (go(k_linear_db<D>, ndb, 1024, a, st)) return -1;
     }
     if (a.dw) {
         ProfScope prof_(st, "linear_dw");
@@ -730,25 +889,13 @@ static int bwd_(LinBwdArgs a, hipStream_t st) {
     }
     if (a.dx) {
         ProfScope prof_(st, "linear_dx");
-        if (dx_<D>(a, st)) return -1;
+        if (dx_<D>(p, a, st)) return -1;
     }
     return 0;
 }
 
-int launch_linear_bwd(const LinBwdArgs& a, hipStream_t st) { return a.dtype == 0 ? bwd_<Bf16>(a, st) : bwd_<Fp16>(a, st); }
-
-template <class D>
-static int dz_(const LinDzArgs& a, hipStream_t st) {
-    const int64_t grid = row_tiles(a.g, kLinDzRows) * ((a.N + 511) / 512);
-    return with_act<D>(a.act, [&](auto A) {
-        k_linear_dz<D, A(), kLinDzRows><<<(unsigned)grid, 256, 0, st>>>(a);
-        return ok();
-    });
-}
-
-int launch_linear_dz(const LinDzArgs& a, hipStream_t st) {
-    ProfScope prof_(st, "linear_dz");
-    return a.dtype == 0 ? dz_<Bf16>(a, st) : dz_<Fp16>(a, st);
+int launch_linear_bwd(const LinPlan& p, const LinBwdArgs& a, hipStream_t st) {
+    return a.dtype == 0 ? bwd_<Bf16>(p, a, st) : bwd_<Fp16>(p, a, st);
 }
 
 }  // namespace moe

@@ -55,8 +55,8 @@ __device__ __forceinline__ void t2_wait() {
 // Copy q of thread t moves chunk q * (threads) + t.  Rows (columns) past the
 // operand's last are read from its last one; their results are not stored.
 // A tile holds the operand in NH arrays of ROWS rows (columns) each, copied by
-// THR threads.
-template <bool KS, int ROWS, int NH, int THR>
+// THR threads.  NT: non-temporal copies, for an operand that is read once.
+template <bool KS, int ROWS, int NH, int THR, bool NT = false>
 struct TileOperand {
     static constexpr int PER = ROWS * (kTK / 8) / THR;
     static_assert(!KS || ROWS == 128, "KS arrays are 128 columns wide");
@@ -100,7 +100,7 @@ struct TileOperand {
             uint32_t o = off[h][q];
             asm volatile("" : "+v"(o));            // a scalar base and a 32-bit offset, not 64-bit lane addresses
             __builtin_amdgcn_global_load_lds((glb_void_t*)(b + o),
-                                             (lds_void_t*)(dst + (q * THR + wave_id() * 64) * 8), 16, 0, 0);
+                                             (lds_void_t*)(dst + (q * THR + wave_id() * 64) * 8), 16, 0, NT ? 2 : 0);
         }
     }
     // the last, partial step through registers: `left` reduction indices, zeros behind them
@@ -349,10 +349,10 @@ constexpr int kT1Threads = 256;
 template <int TM>
 using T1Acc = f32x4[TM / 32][4];
 
-template <class D, bool AKS, bool BKS, int TM, int NST>
+template <class D, bool AKS, bool BKS, int TM, int NST, bool NT = false>
 struct T1Loop {
     using OpA = TileOperand<AKS, TM, 1, kT1Threads>;
-    using OpB = TileOperand<BKS, 128, 1, kT1Threads>;
+    using OpB = TileOperand<BKS, 128, 1, kT1Threads, NT>;
     static constexpr int PER = OpA::PER + OpB::PER;      // copies per thread and step
     const OpA& a;
     const OpB& b;
@@ -411,14 +411,14 @@ struct T1Ring {
     const T1Ring NAME{NAME##a0, NAME##a1, NAME##a2, NAME##a3, NAME##b0, NAME##b1, NAME##b2, NAME##b3}
 
 // acc = A (x) B over `len` reduction indices
-template <class D, bool AKS, bool BKS, int TM, int NST>
+template <class D, bool AKS, bool BKS, int TM, int NST, bool NT = false>
 __device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Threads>& a,
-                                            const TileOperand<BKS, 128, 1, kT1Threads>& b, int len, T1Acc<TM>& acc,
-                                            const T1Ring& r) {
+                                            const TileOperand<BKS, 128, 1, kT1Threads, NT>& b, int len,
+                                            T1Acc<TM>& acc, const T1Ring& r) {
     static_assert(NST == 3 || NST == 4, "");
     uint16_t *const a0 = r.a0, *const a1 = r.a1, *const a2 = r.a2, *const a3 = r.a3;
     uint16_t *const b0 = r.b0, *const b1 = r.b1, *const b2 = r.b2, *const b3 = r.b3;
-    T1Loop<D, AKS, BKS, TM, NST> l(a, b, acc);
+    T1Loop<D, AKS, BKS, TM, NST, NT> l(a, b, acc);
     const int nk = len / kTK, left = len % kTK;
     if (nk > 0) {
         // steps 0 .. NST - 2; what is past the last one is the last one again,
