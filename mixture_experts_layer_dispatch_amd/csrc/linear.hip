@@ -211,23 +211,34 @@ __device__ __forceinline__ bool lin_wtile(const LinTiles& t, int nMt, int nNt, i
 template <int TM>
 constexpr int lin_stages() { return TM == 64 ? 3 : 4; }
 
-// Four consecutive output columns of one row: bias, activation, residual.
+// Four consecutive output columns from col, values packed: the bias of expert
+// e, the activation with the residual of a row (both zero past the last column).
+template <class D>
+__device__ __forceinline__ uint2 pack4(const f32x4& v) {
+    return make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+}
+template <class D>
+__device__ __forceinline__ f32x4 unpack4(const uint2& b) {
+    return f32x4{D::lo(b.x), D::hi(b.x), D::lo(b.y), D::hi(b.y)};
+}
+template <class D>
+__device__ __forceinline__ f32x4 bias4(const LinFwdArgs& a, int e, int col) {
+    return col < a.N ? unpack4<D>(*(const uint2*)(a.bias + (int64_t)e * a.N + col)) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
 template <class D, int ACT>
-__device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int64_t row, int col, const f32x4& s) {
-    const int64_t at = row * a.N + col;
-    float z[4] = {s[0], s[1], s[2], s[3]};
-    if (a.bias) {
-        const uint2 b = *(const uint2*)(a.bias + (int64_t)e * a.N + col);
-        z[0] += D::lo(b.x); z[1] += D::hi(b.x); z[2] += D::lo(b.y); z[3] += D::hi(b.y);
-    }
-    if (a.z) *(uint2*)(a.z + at) = make_uint2(D::pack2(z[0], z[1]), D::pack2(z[2], z[3]));
+__device__ __forceinline__ f32x4 act_residual(const LinFwdArgs& a, int row, int rows, int col, f32x4 v) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) z[r] = act<ACT>(z[r]);
-    if (a.residual) {
-        const uint2 b = *(const uint2*)(a.residual + at);
-        z[0] += D::lo(b.x); z[1] += D::hi(b.x); z[2] += D::lo(b.y); z[3] += D::hi(b.y);
-    }
-    *(uint2*)(a.y + at) = make_uint2(D::pack2(z[0], z[1]), D::pack2(z[2], z[3]));
+    for (int r = 0; r < 4; ++r) v[r] = act<ACT>(v[r]);
+    if (a.residual && row < rows && col < a.N) v += unpack4<D>(*(const uint2*)(a.residual + (int64_t)row * a.N + col));
+    return v;
+}
+// all of it, stored
+template <class D, int ACT>
+__device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int row, int col, f32x4 v) {
+    const int64_t at = (int64_t)row * a.N + col;
+    if (a.bias) v += bias4<D>(a, e, col);
+    if (a.z) *(uint2*)(a.z + at) = pack4<D>(v);
+    *(uint2*)(a.y + at) = pack4<D>(act_residual<D, ACT>(a, row, row + 1, col, v));
 }
 
 // ONCE: a weight tile feeds one row tile, so it is copied non-temporally (512
@@ -247,16 +258,18 @@ __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(Lin
         t1_mainloop<D, false, false, TM, lin_stages<TM>(), ONCE>(oa, ob, a.K, acc, ring);
     }
     AccPos<TM, TN> pos;
-#pragma unroll
-    for (int mb = 0; mb < TM / 32; ++mb) {
-        const int row = lo + pos.m(mb);
-        if (row >= hi) continue;
+    if (a.bias) {
 #pragma unroll
         for (int nb = 0; nb < TN / 32; ++nb) {
-            const int col = n0 + pos.n(nb);
-            if (col < a.N) lin_out<D, ACT>(a, e, row, col, acc[mb][nb]);
+            const f32x4 v = bias4<D>(a, e, n0 + pos.n(nb));
+#pragma unroll
+            for (int mb = 0; mb < TM / 32; ++mb) acc[mb][nb] += v;
         }
     }
+    if (a.z) t1_put<TM>(ring, a.z, lo, hi, n0, a.N, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    t1_put<TM>(ring, a.y, lo, hi, n0, a.N, [&](int mb, int nb) {
+        return pack4<D>(act_residual<D, ACT>(a, lo + pos.m(mb), hi, n0 + pos.n(nb), acc[mb][nb]));
+    });
 }
 
 // ================================================================ split reductions
@@ -300,7 +313,7 @@ __global__ __launch_bounds__(256) void k_linear_sum(LinFwdArgs a) {
     const int col = (int)(i - row * n4) * 4;
     f32x4 v = *(const f32x4*)(a.part + row * a.N + col);
     for (int q = 1; q < a.ksplit; ++q) v += *(const f32x4*)(a.part + ((int64_t)q * a.t.rows + row) * a.N + col);
-    lin_out<D, ACT>(a, 0, row, col, v);
+    lin_out<D, ACT>(a, 0, (int)row, col, v);
 }
 
 // ================================================================ few rows
@@ -405,19 +418,7 @@ __device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1
         const TileOperand<true, TN, 1, kT1Threads, ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
         t1_mainloop<D, false, true, TM, lin_stages<TM>(), ONCE>(oa, ob, a.N, acc, ring);
     }
-    AccPos<TM, TN> pos;
-#pragma unroll
-    for (int mb = 0; mb < TM / 32; ++mb) {
-        const int row = lo + pos.m(mb);
-        if (row >= hi) continue;
-#pragma unroll
-        for (int nb = 0; nb < TN / 32; ++nb) {
-            const int col = n0 + pos.n(nb);
-            const f32x4 v = acc[mb][nb];
-            if (col < a.K)
-                *(uint2*)(a.dx + (int64_t)row * a.K + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
-        }
-    }
+    t1_put<TM>(ring, a.dx, lo, hi, n0, a.K, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
 }
 
 template <class D, int TM, bool ONCE>
@@ -439,20 +440,8 @@ __device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1
         const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
         t1_mainloop<D, true, true, TM, lin_stages<TM>()>(oa, ob, n, acc, ring);
     }
-    AccPos<TM, TN> pos;
-    uint16_t* out = a.dw + (int64_t)e * a.N * a.K;
-#pragma unroll
-    for (int mb = 0; mb < TM / 32; ++mb) {
-        const int row = m0 + pos.m(mb);
-        if (row >= a.N) continue;
-#pragma unroll
-        for (int nb = 0; nb < TN / 32; ++nb) {
-            const int col = n0 + pos.n(nb);
-            const f32x4 v = acc[mb][nb];
-            if (col < a.K)
-                *(uint2*)(out + (int64_t)row * a.K + col) = make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
-        }
-    }
+    t1_put<TM>(ring, a.dw + (int64_t)e * a.N * a.K, m0, a.N, n0, a.K,
+               [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
 }
 
 template <class D>
@@ -577,41 +566,26 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
         for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
-                const int col = nt * 256 + t2_col(hb, nb);
-                const uint2 b = col < a.N ? *(const uint2*)(a.bias + (int64_t)e * a.N + col) : make_uint2(0, 0);
-                const f32x4 v{D::lo(b.x), D::hi(b.x), D::lo(b.y), D::hi(b.y)};
+                const f32x4 v = bias4<D>(a, e, nt * 256 + t2_col(hb, nb));
 #pragma unroll
                 for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
                     for (int mb = 0; mb < 4; ++mb) acc[ha][hb][mb][nb] += v;
             }
     }
-    auto pack = [](const f32x4& v) { return make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3])); };
     if (a.z)
         t2_put(lds, a.z, lo, hi, nt * 256, a.N,
-               [&](int ha, int hb, int mb, int nb) { return pack(acc[ha][hb][mb][nb]); });
+               [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
     t2_put(lds, a.y, lo, hi, nt * 256, a.N, [&](int ha, int hb, int mb, int nb) {
-        f32x4 v = acc[ha][hb][mb][nb];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = act<ACT>(v[r]);
-        if (a.residual) {
-            const int row = lo + t2_row(ha, mb), col = nt * 256 + t2_col(hb, nb);
-            if (row < hi && col < a.N) {
-                const uint2 b = *(const uint2*)(a.residual + (int64_t)row * a.N + col);
-                v += f32x4{D::lo(b.x), D::hi(b.x), D::lo(b.y), D::hi(b.y)};
-            }
-        }
-        return pack(v);
+        return pack4<D>(
+            act_residual<D, ACT>(a, lo + t2_row(ha, mb), hi, nt * 256 + t2_col(hb, nb), acc[ha][hb][mb][nb]));
     });
 }
 
 template <class D>
 __device__ __forceinline__ void t2_store(const T2Lds& lds, uint16_t* out, int r0, int r1, int c0, int ncol,
                                          const T2Acc& acc) {
-    t2_put(lds, out, r0, r1, c0, ncol, [&](int ha, int hb, int mb, int nb) {
-        const f32x4 v = acc[ha][hb][mb][nb];
-        return make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
-    });
+    t2_put(lds, out, r0, r1, c0, ncol, [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
 }
 
 template <class D>

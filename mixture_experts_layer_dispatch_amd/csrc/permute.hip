@@ -46,13 +46,12 @@ __device__ __forceinline__ float lane_value(float v, int j) {
 
 // ---------------------------------------------------------------- non-temporal accesses
 // The expert rows are read once: non-temporal loads (16384 tokens x 10 x 4096
-// bf16: unpermute 312 -> 259 us, permute backward 287 -> 253; 2048 tokens:
-// 38 -> 34, 35 -> 33, unpermute backward 79 -> 63).  Expert rows that are
-// written stay in the 256 MB last-level cache if they fit, and are written
-// past it if they do not (NT): 16384 tokens, 1.3 GB: permute 289 -> 257 us,
-// unpermute backward 582 -> 535; 2048 tokens, 168 MB: permute 28 -> 33 with NT,
-// unpermute backward 63 -> 73.
-constexpr int64_t kCacheBytes = 256ll << 20;
+// bf16: unpermute 312 -> 291 us, permute backward 287 -> 256; 2048 tokens:
+// 38 -> 34, 35 -> 33).  Expert rows that are written are too many to be found
+// in a cache later and go past it (NT) once they are more than the 32 MB of the
+// L2s: 8192 tokens x 8 x 1024 (134 MB) permute 27.3 -> 24.2 us, unpermute
+// backward 56 -> 52; 16384 x 10 x 4096 (1.3 GB) 292 -> 298 and 585 -> 564.
+constexpr int64_t kCacheBytes = 32ll << 20;
 
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {

@@ -304,7 +304,9 @@ __device__ __forceinline__ int t2_col(int hb, int nb) {
 // The tile to out [., ncol] at row r0, column c0 (rows below r1): f(ha, hb, mb,
 // nb) gives four consecutive values of a row, packed.  It goes out through the
 // stages' LDS (32 rows to an array, 16-byte chunk c of row r at slot c ^ (r &
-// 31)) as 512-byte row pieces, 16 bytes per lane: @MEASURED@
+// 31)) as 512-byte row pieces, 16 bytes per lane (stored straight from the
+// fragments, 16 rows by 32 bytes an instruction, the same bytes took 32 us
+// instead of 22 for 134 MB).
 template <class F>
 __device__ __forceinline__ void t2_put(const T2Lds& lds, uint16_t* out, int r0, int r1, int c0, int ncol, const F& f) {
     const int wr = wave_id() >> 2, t = threadIdx.x;
@@ -465,6 +467,40 @@ __device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Thr
         b.copy_tail(0, nk, left, b0);
         __syncthreads();
         l.product(a0, b0);
+    }
+}
+
+// The tile to out [., ncol] at row r0, column c0 (rows below r1): f(mb, nb) gives
+// four consecutive values of a row, packed.  Through the ring's LDS (64 rows to
+// an array, 16-byte chunk c of row r at slot c ^ (r & 15)) as 256-byte row
+// pieces: stored straight from the fragments (16 rows by 32 bytes an
+// instruction) z next to y cost 512 experts of 40 rows 66 us, 42 MB.
+template <int TM, class F>
+__device__ __forceinline__ void t1_put(const T1Ring& ring, uint16_t* out, int r0, int r1, int c0, int ncol,
+                                       const F& f) {
+    const int wm = wave_id() & 1, wn = 64 * (wave_id() >> 1), t = threadIdx.x, lane = lane_id();
+    __syncthreads();                           // the LDS is no longer read
+    uint16_t* h = TM == 128 && wm ? ring.b1 : ring.b0;
+#pragma unroll
+    for (int mb = 0; mb < TM / 32; ++mb) {
+        const int r = (TM == 64 ? 32 * wm : 0) + 16 * mb + (lane & 15);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) {
+            const int c = wn + 16 * nb + 4 * (lane >> 4);
+            *(uint2*)(h + r * 128 + (((c >> 3) ^ (r & 15)) << 3) + (c & 7)) = f(mb, nb);
+        }
+    }
+    __syncthreads();
+    const int c = t & 15;
+    if (c0 + 8 * c < ncol) {
+        uint16_t* p = out + (int64_t)r0 * ncol + c0 + 8 * c;
+#pragma unroll
+        for (int q = 0; q < TM / 16; ++q) {
+            const int r = 16 * q + (t >> 4);
+            if (r0 + r < r1)
+                *(uint4*)(p + (int64_t)r * ncol) =
+                    *(const uint4*)((q < 4 ? ring.b0 : ring.b1) + (r & 63) * 128 + ((c ^ (r & 15)) << 3));
+        }
     }
 }
 
