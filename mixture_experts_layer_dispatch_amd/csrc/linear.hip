@@ -266,8 +266,9 @@ __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(Lin
             for (int mb = 0; mb < TM / 32; ++mb) acc[mb][nb] += v;
         }
     }
-    if (a.z) t1_put<TM>(ring, a.z, lo, hi, n0, a.N, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
-    t1_put<TM>(ring, a.y, lo, hi, n0, a.N, [&](int mb, int nb) {
+    const bool nt_out = many((int64_t)a.t.rows * a.N);
+    if (a.z) t1_put<TM>(ring, nt_out, a.z, lo, hi, n0, a.N, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    t1_put<TM>(ring, nt_out, a.y, lo, hi, n0, a.N, [&](int mb, int nb) {
         return pack4<D>(act_residual<D, ACT>(a, lo + pos.m(mb), hi, n0 + pos.n(nb), acc[mb][nb]));
     });
 }
@@ -418,13 +419,17 @@ __device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1
         const TileOperand<true, TN, 1, kT1Threads, ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
         t1_mainloop<D, false, true, TM, lin_stages<TM>(), ONCE>(oa, ob, a.N, acc, ring);
     }
-    t1_put<TM>(ring, a.dx, lo, hi, n0, a.K, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    t1_put<TM>(ring, many((int64_t)a.t.rows * a.K), a.dx, lo, hi, n0, a.K, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
 }
 
 template <class D, int TM, bool ONCE>
 __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
     T1_RING(ring, TM, lin_stages<TM>());
     dx_tile<D, TM, ONCE>(a, blockIdx.x, ring);
+}
+
+__device__ __forceinline__ int64_t dw_elements(const LinBwdArgs& a) {
+    return (int64_t)(a.t.offsets ? a.t.E : 1) * a.N * a.K;
 }
 
 // dW = dz^T x over a group's rows: both operands with the row as the memory row
@@ -440,7 +445,7 @@ __device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1
         const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
         t1_mainloop<D, true, true, TM, lin_stages<TM>()>(oa, ob, n, acc, ring);
     }
-    t1_put<TM>(ring, a.dw + (int64_t)e * a.N * a.K, m0, a.N, n0, a.K,
+    t1_put<TM>(ring, many(dw_elements(a)), a.dw + (int64_t)e * a.N * a.K, m0, a.N, n0, a.K,
                [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
 }
 
@@ -500,11 +505,12 @@ __global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
     __syncthreads();
     const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
     if (n0 + 8 * c >= a.K) return;
+    const bool past = many(dw_elements(a));
     uint16_t* out = a.dw + ((int64_t)e * a.N + m0) * a.K + n0 + 8 * c;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         const int r = r0 + 16 * q;
-        if (m0 + r < a.N) *(uint4*)(out + (int64_t)r * a.K) = *(const uint4*)(sm + r * TN + ((c ^ (r & 15)) << 3));
+        if (m0 + r < a.N) st_out(past, out + (int64_t)r * a.K, sm + r * TN + ((c ^ (r & 15)) << 3));
     }
 }
 
@@ -573,19 +579,20 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
                     for (int mb = 0; mb < 4; ++mb) acc[ha][hb][mb][nb] += v;
             }
     }
+    const bool nt_out = many((int64_t)a.t.rows * a.N);
     if (a.z)
-        t2_put(lds, a.z, lo, hi, nt * 256, a.N,
+        t2_put(lds, nt_out, a.z, lo, hi, nt * 256, a.N,
                [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
-    t2_put(lds, a.y, lo, hi, nt * 256, a.N, [&](int ha, int hb, int mb, int nb) {
+    t2_put(lds, nt_out, a.y, lo, hi, nt * 256, a.N, [&](int ha, int hb, int mb, int nb) {
         return pack4<D>(
             act_residual<D, ACT>(a, lo + t2_row(ha, mb), hi, nt * 256 + t2_col(hb, nb), acc[ha][hb][mb][nb]));
     });
 }
 
 template <class D>
-__device__ __forceinline__ void t2_store(const T2Lds& lds, uint16_t* out, int r0, int r1, int c0, int ncol,
+__device__ __forceinline__ void t2_store(const T2Lds& lds, bool nt, uint16_t* out, int r0, int r1, int c0, int ncol,
                                          const T2Acc& acc) {
-    t2_put(lds, out, r0, r1, c0, ncol, [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
+    t2_put(lds, nt, out, r0, r1, c0, ncol, [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
 }
 
 template <class D>
@@ -599,7 +606,7 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
         const T2Operand<true> ob(a.w + (int64_t)e * a.N * a.K, a.K, nt * 256, a.K);
         t2_mainloop<D, false, true>(oa, ob, a.N, acc, lds);
     }
-    t2_store<D>(lds, a.dx, lo, hi, nt * 256, a.K, acc);
+    t2_store<D>(lds, many((int64_t)a.t.rows * a.K), a.dx, lo, hi, nt * 256, a.K, acc);
 }
 
 template <class D>
@@ -613,7 +620,7 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
         const T2Operand<true> ob(a.x + (int64_t)lo * a.K, a.K, nt * 256, a.K);
         t2_mainloop<D, true, true>(oa, ob, n, acc, lds);
     }
-    t2_store<D>(lds, a.dw + (int64_t)e * a.N * a.K, mt * 256, a.N, nt * 256, a.K, acc);
+    t2_store<D>(lds, many(dw_elements(a)), a.dw + (int64_t)e * a.N * a.K, mt * 256, a.N, nt * 256, a.K, acc);
 }
 
 // ================================================================ dz and db

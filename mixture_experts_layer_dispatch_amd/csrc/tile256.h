@@ -135,6 +135,22 @@ __device__ __forceinline__ uint4 t2_frag(const uint16_t* half, int r, int ks) {
     }
 }
 
+// 16 bytes of an output: past the caches if it is too large to be found there
+// by whoever reads it next (many: more elements than the 32 MB of the L2s
+// hold).  512 experts of 40 rows (y and z of 42 MB each next to 4.3 GB of
+// weights) 786 -> 719 us, dx of the same 858 -> 815; 16384 x 4096 x 4096 429 -> 421.
+__device__ __forceinline__ bool many(int64_t elements) { return elements > (16 << 20); }
+__device__ __forceinline__ void st_out(bool nt, uint16_t* p, const uint16_t* v) {
+    if (nt) {
+        // (the markers keep the compiler from merging the two stores into a plain one)
+        asm volatile("; non-temporal");
+        __builtin_nontemporal_store(*(const u32x4*)v, (u32x4*)p);
+        asm volatile("; non-temporal");
+    } else {
+        *(u32x4*)p = *(const u32x4*)v;
+    }
+}
+
 // A wave's four quarters: acc[ha][hb][mb][nb] is rows 128 ha + 64 (w >> 2) + 16 mb + (lane & 15),
 // columns 128 hb + 32 (w & 3) + 16 nb + 4 (lane >> 4) + 0 .. 3.
 typedef f32x4 T2Acc[2][2][4][2];
@@ -308,7 +324,8 @@ __device__ __forceinline__ int t2_col(int hb, int nb) {
 // fragments, 16 rows by 32 bytes an instruction, the same bytes took 32 us
 // instead of 22 for 134 MB).
 template <class F>
-__device__ __forceinline__ void t2_put(const T2Lds& lds, uint16_t* out, int r0, int r1, int c0, int ncol, const F& f) {
+__device__ __forceinline__ void t2_put(const T2Lds& lds, bool nt, uint16_t* out, int r0, int r1, int c0, int ncol,
+                                       const F& f) {
     const int wr = wave_id() >> 2, t = threadIdx.x;
     __syncthreads();                           // the LDS is no longer read
 #pragma unroll
@@ -333,7 +350,7 @@ __device__ __forceinline__ void t2_put(const T2Lds& lds, uint16_t* out, int r0, 
         for (int q = 0; q < 16; ++q) {
             const int r = 16 * q + (t >> 5);
             if (r0 + r < r1)
-                *(uint4*)(p + (int64_t)r * ncol) = *(const uint4*)(lds.h[q >> 1] + (r & 31) * 256 + ((c ^ (r & 31)) << 3));
+                st_out(nt, p + (int64_t)r * ncol, lds.h[q >> 1] + (r & 31) * 256 + ((c ^ (r & 31)) << 3));
         }
     }
 }
@@ -476,8 +493,8 @@ __device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Thr
 // pieces: stored straight from the fragments (16 rows by 32 bytes an
 // instruction) z next to y cost 512 experts of 40 rows 66 us, 42 MB.
 template <int TM, class F>
-__device__ __forceinline__ void t1_put(const T1Ring& ring, uint16_t* out, int r0, int r1, int c0, int ncol,
-                                       const F& f) {
+__device__ __forceinline__ void t1_put(const T1Ring& ring, bool nt, uint16_t* out, int r0, int r1, int c0,
+                                       int ncol, const F& f) {
     const int wm = wave_id() & 1, wn = 64 * (wave_id() >> 1), t = threadIdx.x, lane = lane_id();
     __syncthreads();                           // the LDS is no longer read
     uint16_t* h = TM == 128 && wm ? ring.b1 : ring.b0;
@@ -498,8 +515,8 @@ __device__ __forceinline__ void t1_put(const T1Ring& ring, uint16_t* out, int r0
         for (int q = 0; q < TM / 16; ++q) {
             const int r = 16 * q + (t >> 4);
             if (r0 + r < r1)
-                *(uint4*)(p + (int64_t)r * ncol) =
-                    *(const uint4*)((q < 4 ? ring.b0 : ring.b1) + (r & 63) * 128 + ((c ^ (r & 15)) << 3));
+                st_out(nt, p + (int64_t)r * ncol,
+                       (q < 4 ? ring.b0 : ring.b1) + (r & 63) * 128 + ((c ^ (r & 15)) << 3));
         }
     }
 }
