@@ -355,16 +355,19 @@ __global__ __launch_bounds__(64 * W) void k_linear_stream(LinFwdArgs a) {
 #pragma unroll
                 for (int m = 0; m < MB; ++m) u.x[m][s] = *(const uint4*)(xp[m] + k0 + 32 * s);
             }
-        } else {                                           // the last unit: zeros behind the row
+        } else {                                           // the last unit: zeros behind the row (masked, as above)
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                const bool in = k0 + 32 * s + kg < a.K;
+                const int k = k0 + 32 * s + kg < a.K ? k0 + 32 * s : a.K - 8 - kg;
+                const uint32_t in = k0 + 32 * s + kg < a.K ? ~0u : 0u;
+                auto masked = [&](const uint16_t* p) {
+                    const uint4 v = *(const uint4*)(p + k);
+                    return make_uint4(v.x & in, v.y & in, v.z & in, v.w & in);
+                };
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    u.w[n][s] = in ? *(const uint4*)(wp[n] + k0 + 32 * s) : make_uint4(0, 0, 0, 0);
+                for (int n = 0; n < NB; ++n) u.w[n][s] = masked(wp[n]);
 #pragma unroll
-                for (int m = 0; m < MB; ++m)
-                    u.x[m][s] = in ? *(const uint4*)(xp[m] + k0 + 32 * s) : make_uint4(0, 0, 0, 0);
+                for (int m = 0; m < MB; ++m) u.x[m][s] = masked(xp[m]);
             }
         }
     };
@@ -457,9 +460,13 @@ __global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
 
 // Groups of few rows: dW's write is all the work.  Blocks of 32 KB of LDS,
 // four to a CU, so that some wait for their operands while others store: one
-// stage, no ring; the tile goes out through LDS as whole 256-byte row pieces.
-// (The ring form, a block to a CU, took 3160 us where 512 experts of 40 rows
-// write 4.3 GB, register-staged tiles stored from their fragments 1540 us.)
+// stage, no ring; the tile goes out through LDS as whole 256-byte row pieces,
+// past the caches.  Where 512 experts of 40 rows write 4.3 GB: 869 us (4.9 TB/s;
+// 10 rows each: 644, 6.7 TB/s; the ring form, a block to a CU, 3160 us;
+// register-staged tiles stored from their fragments 1540).  Blocks that walk
+// eight tiles, dz^T in fragments and the next x loaded ahead (64 KB, two to a
+// CU): 807 us, but 774 for 10 rows each and 162 instead of 139 us for 64
+// experts of 128 rows.
 template <class D>
 __global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
     constexpr int TM = 128, TN = 128;

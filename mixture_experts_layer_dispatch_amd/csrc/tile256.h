@@ -103,13 +103,20 @@ struct TileOperand {
                                              (lds_void_t*)(dst + (q * THR + wave_id() * 64) * 8), 16, 0, NT ? 2 : 0);
         }
     }
-    // the last, partial step through registers: `left` reduction indices, zeros behind them
+    // the last, partial step through registers: `left` reduction indices, zeros
+    // behind them.  Chunks behind them load the last one instead and are masked:
+    // loads under a lane's condition are waited for one by one (512 experts of
+    // 40 rows, all partial steps: dW 1087 -> 869 us).
     __device__ __forceinline__ void copy_tail(int h, int kt, int left, uint16_t* dst) const {
         const char* b = base + kt * step;
+        const int last = KS ? left - 1 : left - 8, unit = KS ? (int)(step / kTK) : 2;
+        uint4 v[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) v[q] = *(const uint4*)(b + off[h][q] - (uint32_t)(max(kpos[q] - last, 0) * unit));
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
-            const uint4 v = kpos[q] < left ? *(const uint4*)(b + off[h][q]) : make_uint4(0, 0, 0, 0);
-            *(uint4*)(dst + (q * THR + threadIdx.x) * 8) = v;
+            const uint32_t m = kpos[q] < left ? ~0u : 0u;
+            *(uint4*)(dst + (q * THR + threadIdx.x) * 8) = make_uint4(v[q].x & m, v[q].y & m, v[q].z & m, v[q].w & m);
         }
     }
 };
