@@ -182,7 +182,7 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     LinPlan p = linear_plan(c->M, c->E, c->N, c->K, true);
-    LinTiles rows32{nullptr, nullptr, c->E, c->M, kLinDzRows, 0, INT32_MAX, nullptr};
+    LinTiles rows32{nullptr, nullptr, c->E, c->M, kLinDzRows, nullptr};
     if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->K, 128}, {&p.big, c->K, 256}, {&rows32, c->N, 512}}, st))
         return MOE_ERR_HIP;
     uint16_t* dz = (uint16_t*)(ws + L.dz);
@@ -191,7 +191,7 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     if ((db || !none) && launch_linear_dz(d, st)) return MOE_ERR_HIP;
     const LinBwdArgs b{p.small, rows32, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x,
                        (const uint16_t*)w, (uint16_t*)dx, (uint16_t*)dw, (uint16_t*)db, part,
-                       (float*)(ws + L.sums), 0, 0};
+                       (float*)(ws + L.sums), 0, 0, 0};
     if (launch_linear_bwd(p, b, st)) return MOE_ERR_HIP;
     return MOE_OK;
 }

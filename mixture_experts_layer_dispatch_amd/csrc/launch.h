@@ -388,18 +388,17 @@ int launch_unpermute_bwd(const RowsArgs& a, const void* o, const void* dy, const
 enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4, LIN_ACTS = 5 };
 constexpr int kLinDzRows = 32;       // rows of a k_linear_dz tile
 
-// Row tiles of tm rows (0: none) over the groups of lo <= n < hi rows, or over
-// one dense group of `rows` rows (offsets null).
+// Row tiles of tm rows (0: none) over the groups, or over one dense group of
+// `rows` rows (offsets null).
 struct LinTiles {
     const int32_t* offsets;   // [E+1]
     const int32_t* list;      // [E+1] tiles before each group (k_linear_prefix), or null: each block counts (E <= 64)
     int E, rows;              // rows of the whole matrix
-    int tm, lo, hi;
+    int tm;
     int32_t* err;
 };
 
-// Tiles of one product: the groups of many rows (or the dense group) in 256 x
-// 256 tiles, the others in small ones.
+// Tiles of one product: 256 x 256 (big) or small ones.
 struct LinPlan {
     LinTiles small, big;
     bool stream;              // small: k_linear_stream, 16 or 32 rows
@@ -448,6 +447,7 @@ struct LinBwdArgs {
     const float* part;        // k_linear_dz's column sums
     float* sums;              // dx's parts, if its plan splits the reduction
     int ndw, ndx;             // (k_linear_bwd: blocks of dW and of dx)
+    int ndb;                  // (k_linear_dx256: blocks of db in front of dx's)
 };
 
 // linear.hip

@@ -91,9 +91,7 @@ __device__ __forceinline__ int group_rows(const LinTiles& t, int e, int& lo, boo
     return b - a;
 }
 
-__device__ __forceinline__ int group_tiles(const LinTiles& t, int n) {
-    return n >= t.lo && n < t.hi ? (n + t.tm - 1) / t.tm : 0;
-}
+__device__ __forceinline__ int group_tiles(const LinTiles& t, int n) { return (n + t.tm - 1) / t.tm; }
 
 // One block: for each of up to three sets of tiles, list[e] = the tiles of the
 // groups before e, list[E] their number.
@@ -604,9 +602,13 @@ __device__ __forceinline__ void t2_store(const T2Lds& lds, bool nt, uint16_t* ou
 
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
-    int e, lo, hi, nt, mt;
-    if (!lin_tile<256, 4>(a.t, (a.K + 255) / 256, blockIdx.x, e, lo, hi, nt, mt)) return;
     T2_LDS(lds);
+    if ((int)blockIdx.x < a.ndb) {                 // db's columns first (a launch less)
+        db_columns<D>(a.part, a.rows32, a.N, blockIdx.x, kT2Threads / 64, (float*)lds.h[0], a.db);
+        return;
+    }
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<256, 4>(a.t, (a.K + 255) / 256, blockIdx.x - a.ndb, e, lo, hi, nt, mt)) return;
     T2Acc acc;
     {
         const T2Operand<false> oa(a.dz, a.N, lo, hi);
@@ -688,8 +690,8 @@ static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
 static int64_t max_tiles(const LinTiles& t) {
     if (t.tm == 0) return 0;
     if (!t.offsets) return ((int64_t)t.rows + t.tm - 1) / t.tm;
-    // groups of n >= lo rows take ceil(n / tm) tiles: at most rows / tm + groups, groups <= rows / lo
-    const int64_t groups = t.lo > 1 && t.rows / t.lo < t.E ? t.rows / t.lo : t.rows < t.E ? t.rows : t.E;
+    // ceil(n / tm) <= (n + tm - 1) / tm for each of at most min(rows, E) groups with rows
+    const int64_t groups = t.rows < t.E ? t.rows : t.E;
     return ((int64_t)t.rows + groups * (t.tm - 1)) / t.tm;
 }
 
@@ -698,9 +700,15 @@ static int64_t max_tiles(const LinTiles& t) {
 LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
     LinPlan p{};
     p.ksplit = 1;
-    p.small = {nullptr, nullptr, E, M, 0, 0, INT32_MAX, nullptr};
+    p.small = {nullptr, nullptr, E, M, 0, nullptr};
     p.big = p.small;
     if (E > 0) {
+        // (a group below 256 rows then takes a tile of its own: 128-row tiles
+        // for those groups, a launch more, gained nothing)
+        if (M >= 192LL * E) {
+            p.big.tm = 256;
+            return p;
+        }
         p.small.tm = M >= 128LL * E ? 128 : 64;
         // few rows and few tiles: latency, which the streaming form splits over eight waves
         if (!dx && M <= 8LL * E && max_tiles(p.small) * ((C + 127) / 128) < 2048) {
@@ -709,11 +717,6 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
             return p;
         }
         p.once = M <= 64LL * E;
-        if (M >= 192LL * E) {
-            p.small.hi = 256;
-            p.big.tm = 256;
-            p.big.lo = 256;
-        }
         return p;
     }
     if (!dx && M <= 32) {
@@ -738,7 +741,7 @@ size_t linear_part_floats(const LinPlan& p, int M, int C) {
 
 // Whether the blocks of a product find their tiles themselves (LinTiles.list null)
 bool linear_inline_tiles(const LinTiles& t, int C, int tn) {
-    return t.E <= 64 && max_tiles(t) * ((C + tn - 1) / tn) <= 1024;
+    return t.E <= 64 && max_tiles(t) * ((C + tn - 1) / tn) <= 2048;
 }
 
 int launch_linear_prefix(const LinPrefix& p, hipStream_t st) {
@@ -785,9 +788,8 @@ static int fwd_(const LinPlan& p, LinFwdArgs a, hipStream_t st) {
     return with_act(a.act, [&](auto A) {
         if (p.big.tm) {
             a.t = p.big;
-            if (go(k_linear_fwd256<D, A()>, max_tiles(a.t) * ((a.N + 255) / 256), kT2Threads, a, st)) return -1;
+            return go(k_linear_fwd256<D, A()>, max_tiles(a.t) * ((a.N + 255) / 256), kT2Threads, a, st);
         }
-        if (!p.small.tm) return 0;
         a.t = p.small;
         const int64_t tiles = max_tiles(a.t);
         if (p.stream) {
@@ -831,9 +833,8 @@ static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
     }
     if (p.big.tm) {
         a.t = p.big;
-        if (go(k_linear_dx256<D>, max_tiles(a.t) * ((a.K + 255) / 256), kT2Threads, a, st)) return -1;
+        return go(k_linear_dx256<D>, a.ndb + max_tiles(a.t) * ((a.K + 255) / 256), kT2Threads, a, st);
     }
-    if (!p.small.tm) return 0;
     a.t = p.small;
     const int64_t grid = max_tiles(a.t) * ((a.K + 127) / 128);
     if (a.t.tm == 128) return go(k_linear_dx<D, 128, false>, grid, kT1Threads, a, st);
@@ -867,7 +868,9 @@ static int bwd_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
         a.ndx = (int)ndx;
         return go(k_linear_bwd<D>, ndw + ndx + ndb, kT1Threads, a, st);
     }
-    if (a.db) {
+    if (a.db && a.dx && p.big.tm) {
+        a.ndb = (int)ndb;                          // with dx, below
+    } else if (a.db) {
         ProfScope prof_(st, "linear_db");
         if (go(k_linear_db<D>, ndb, 1024, a, st)) return -1;
     }
