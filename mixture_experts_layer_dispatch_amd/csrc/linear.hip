@@ -208,6 +208,8 @@ __device__ __forceinline__ bool lin_wtile(const LinTiles& t, int nMt, int nNt, i
 // stages of the ring: two blocks of 64-row tiles share a CU
 template <int TM>
 constexpr int lin_stages() { return TM == 64 ? 3 : 4; }
+template <int TM>
+constexpr int lin_waves() { return TM == 64 ? 4 : 8; }
 
 // Four consecutive output columns from col, values packed: the bias of expert
 // e, the activation with the residual of a row (both zero past the last column).
@@ -243,30 +245,30 @@ __device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int row, int
 // experts of 40 rows, 4.3 GB of weights: 801 -> 698 us, 6.45 TB/s; where two
 // row tiles read it: 39 -> 46 us).
 template <class D, int ACT, int TM, bool ONCE>
-__global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
+__global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
     constexpr int TN = 128;
     int e, lo, hi, nt, mt;
     if (!lin_tile<TM, 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
     const int n0 = nt * TN;
     T1_RING(ring, TM, lin_stages<TM>());
-    T1Acc<TM> acc;
+    T1Acc<TM, lin_waves<TM>()> acc;
     {
-        const TileOperand<false, TM, 1, kT1Threads> oa(a.x, a.K, lo, hi);
-        const TileOperand<false, TN, 1, kT1Threads, ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N);
-        t1_mainloop<D, false, false, TM, lin_stages<TM>(), ONCE>(oa, ob, a.K, acc, ring);
+        const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.x, a.K, lo, hi);
+        const TileOperand<false, TN, 1, 64 * lin_waves<TM>(), ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.N);
+        t1_mainloop<D, false, false, TM, lin_stages<TM>(), lin_waves<TM>(), ONCE>(oa, ob, a.K, acc, ring);
     }
-    AccPos<TM, TN> pos;
+    T1Pos<TM, lin_waves<TM>()> pos;
     if (a.bias) {
 #pragma unroll
-        for (int nb = 0; nb < TN / 32; ++nb) {
+        for (int nb = 0; nb < t1_nb<lin_waves<TM>()>(); ++nb) {
             const f32x4 v = bias4<D>(a, e, n0 + pos.n(nb));
 #pragma unroll
             for (int mb = 0; mb < TM / 32; ++mb) acc[mb][nb] += v;
         }
     }
     const bool nt_out = many((int64_t)a.t.rows * a.N);
-    if (a.z) t1_put<TM>(ring, nt_out, a.z, lo, hi, n0, a.N, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
-    t1_put<TM>(ring, nt_out, a.y, lo, hi, n0, a.N, [&](int mb, int nb) {
+    if (a.z) t1_put<TM, lin_waves<TM>()>(ring, nt_out, a.z, lo, hi, n0, a.N, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    t1_put<TM, lin_waves<TM>()>(ring, nt_out, a.y, lo, hi, n0, a.N, [&](int mb, int nb) {
         return pack4<D>(act_residual<D, ACT>(a, lo + pos.m(mb), hi, n0 + pos.n(nb), acc[mb][nb]));
     });
 }
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_fwd(Lin
 // k_linear_sum adds in order (128 x 4096 x 4096: @SPLIT@).  N: output columns,
 // K: reduction length, w: [N, K], or (BKS) [K, N].
 template <class D, bool BKS, int TM>
-__global__ __launch_bounds__(kT1Threads, 1) void k_linear_part(LinFwdArgs a) {
+__global__ __launch_bounds__(64 * lin_waves<TM>(), 1) void k_linear_part(LinFwdArgs a) {
     constexpr int TN = 128;
     const int part = blockIdx.x % a.ksplit;
     int e, lo, hi, nt, mt;
@@ -285,19 +287,19 @@ __global__ __launch_bounds__(kT1Threads, 1) void k_linear_part(LinFwdArgs a) {
     const int steps = (a.K + kTK - 1) / kTK, k0 = steps * part / a.ksplit * kTK;
     const int k1 = min(steps * (part + 1) / a.ksplit * kTK, a.K), n0 = nt * TN;
     T1_RING(ring, TM, 4);
-    T1Acc<TM> acc;
+    T1Acc<TM, lin_waves<TM>()> acc;
     {
-        const TileOperand<false, TM, 1, kT1Threads> oa(a.x + k0, a.K, lo, hi);
-        const TileOperand<BKS, TN, 1, kT1Threads> ob(BKS ? a.w + (int64_t)k0 * a.N : a.w + k0, BKS ? a.N : a.K, n0, a.N);
-        t1_mainloop<D, false, BKS, TM, 4>(oa, ob, k1 - k0, acc, ring);
+        const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.x + k0, a.K, lo, hi);
+        const TileOperand<BKS, TN, 1, 64 * lin_waves<TM>()> ob(BKS ? a.w + (int64_t)k0 * a.N : a.w + k0, BKS ? a.N : a.K, n0, a.N);
+        t1_mainloop<D, false, BKS, TM, 4, lin_waves<TM>()>(oa, ob, k1 - k0, acc, ring);
     }
-    AccPos<TM, TN> pos;
+    T1Pos<TM, lin_waves<TM>()> pos;
 #pragma unroll
     for (int mb = 0; mb < TM / 32; ++mb) {
         const int row = lo + pos.m(mb);
         if (row >= hi) continue;
 #pragma unroll
-        for (int nb = 0; nb < TN / 32; ++nb) {
+        for (int nb = 0; nb < t1_nb<lin_waves<TM>()>(); ++nb) {
             const int col = n0 + pos.n(nb);
             if (col < a.N) *(f32x4*)(a.part + ((int64_t)part * a.t.rows + row) * a.N + col) = acc[mb][nb];
         }
@@ -414,17 +416,17 @@ __device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1
     int e, lo, hi, nt, mt;
     if (!lin_tile<TM, 1>(a.t, (a.K + TN - 1) / TN, block, e, lo, hi, nt, mt)) return;
     const int n0 = nt * TN;
-    T1Acc<TM> acc;
+    T1Acc<TM, lin_waves<TM>()> acc;
     {
-        const TileOperand<false, TM, 1, kT1Threads> oa(a.dz, a.N, lo, hi);
-        const TileOperand<true, TN, 1, kT1Threads, ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
-        t1_mainloop<D, false, true, TM, lin_stages<TM>(), ONCE>(oa, ob, a.N, acc, ring);
+        const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.dz, a.N, lo, hi);
+        const TileOperand<true, TN, 1, 64 * lin_waves<TM>(), ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
+        t1_mainloop<D, false, true, TM, lin_stages<TM>(), lin_waves<TM>(), ONCE>(oa, ob, a.N, acc, ring);
     }
-    t1_put<TM>(ring, many((int64_t)a.t.rows * a.K), a.dx, lo, hi, n0, a.K, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    t1_put<TM, lin_waves<TM>()>(ring, many((int64_t)a.t.rows * a.K), a.dx, lo, hi, n0, a.K, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
 }
 
 template <class D, int TM, bool ONCE>
-__global__ __launch_bounds__(kT1Threads, TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
+__global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
     T1_RING(ring, TM, lin_stages<TM>());
     dx_tile<D, TM, ONCE>(a, blockIdx.x, ring);
 }
@@ -440,18 +442,18 @@ __device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1
     int e, mt, nt, lo, n;
     if (!lin_wtile(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
-    T1Acc<TM> acc;
+    T1Acc<TM, lin_waves<TM>()> acc;
     {
-        const TileOperand<true, TM, 1, kT1Threads> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
-        const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
-        t1_mainloop<D, true, true, TM, lin_stages<TM>()>(oa, ob, n, acc, ring);
+        const TileOperand<true, TM, 1, 64 * lin_waves<TM>()> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
+        const TileOperand<true, TN, 1, 64 * lin_waves<TM>()> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
+        t1_mainloop<D, true, true, TM, lin_stages<TM>(), lin_waves<TM>()>(oa, ob, n, acc, ring);
     }
-    t1_put<TM>(ring, many(dw_elements(a)), a.dw + (int64_t)e * a.N * a.K, m0, a.N, n0, a.K,
+    t1_put<TM, lin_waves<TM>()>(ring, many(dw_elements(a)), a.dw + (int64_t)e * a.N * a.K, m0, a.N, n0, a.K,
                [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
 }
 
 template <class D>
-__global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
+__global__ __launch_bounds__(64 * lin_waves<128>(), 1) void k_linear_dw(LinBwdArgs a) {
     T1_RING(ring, 128, 4);
     dw_tile<D>(a, blockIdx.x, ring);
 }
@@ -466,7 +468,7 @@ __global__ __launch_bounds__(kT1Threads, 1) void k_linear_dw(LinBwdArgs a) {
 // CU): 807 us, but 774 for 10 rows each and 162 instead of 139 us for 64
 // experts of 128 rows.
 template <class D>
-__global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
+__global__ __launch_bounds__(256, 4) void k_linear_dw_few(LinBwdArgs a) {
     constexpr int TM = 128, TN = 128;
     __shared__ __attribute__((aligned(16))) uint16_t sm[TM * TN];
     static_assert(TM * TN == 2 * kT2Half, "the operands' stage and the tile take the same LDS");
@@ -474,11 +476,11 @@ __global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
     if (!lin_wtile(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
     uint16_t *const sa = sm, *const sb = sm + kT2Half;
-    T1Acc<TM> acc;
+    T1Acc<TM, 4> acc;
     {
-        const TileOperand<true, TM, 1, kT1Threads> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
-        const TileOperand<true, TN, 1, kT1Threads> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
-        T1Loop<D, true, true, TM, 3> l(oa, ob, acc);
+        const TileOperand<true, TM, 1, 256> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
+        const TileOperand<true, TN, 1, 256> ob(a.x + (int64_t)lo * a.K, a.K, n0, a.K);
+        T1Loop<D, true, true, TM, 3, 4> l(oa, ob, acc);
         const int nk = n / kTK, left = n % kTK;
         for (int kt = 0; kt < nk; ++kt) {
             oa.copy(0, kt, sa);
@@ -497,7 +499,7 @@ __global__ __launch_bounds__(kT1Threads, 4) void k_linear_dw_few(LinBwdArgs a) {
         }
     }
     // 16-byte chunk c of row r at slot c ^ (r & 15)
-    AccPos<TM, TN> pos;
+    T1Pos<TM, 4> pos;
 #pragma unroll
     for (int mb = 0; mb < TM / 32; ++mb)
 #pragma unroll
@@ -548,7 +550,7 @@ __device__ __forceinline__ void db_columns(const float* part, const LinTiles& t,
 // All that follows dz in one launch, for products whose tiles leave CUs idle:
 // blocks of dW's tiles, dx's tiles and db's columns.
 template <class D>
-__global__ __launch_bounds__(kT1Threads, 1) void k_linear_bwd(LinBwdArgs a) {
+__global__ __launch_bounds__(64 * lin_waves<128>(), 1) void k_linear_bwd(LinBwdArgs a) {
     T1_RING(ring, 128, 4);
     int b = blockIdx.x;
     if (b < a.ndw) {
@@ -557,7 +559,7 @@ __global__ __launch_bounds__(kT1Threads, 1) void k_linear_bwd(LinBwdArgs a) {
     }
     b -= a.ndw;
     if (b < a.ndx) dx_tile<D, 128, false>(a, b, ring);
-    else db_columns<D>(a.part, a.rows32, a.N, b - a.ndx, kT1Threads / 64, (float*)ring.a0, a.db);
+    else db_columns<D>(a.part, a.rows32, a.N, b - a.ndx, lin_waves<128>(), (float*)ring.a0, a.db);
 }
 
 // ================================================================ 256 x 256 tiles
@@ -780,8 +782,8 @@ static int fwd_(const LinPlan& p, LinFwdArgs a, hipStream_t st) {
         a.t = p.small;
         a.ksplit = p.ksplit;
         const int64_t grid = max_tiles(a.t) * ((a.N + 127) / 128) * a.ksplit;
-        if (a.t.tm == 128 ? go(k_linear_part<D, false, 128>, grid, kT1Threads, a, st)
-                          : go(k_linear_part<D, false, 64>, grid, kT1Threads, a, st))
+        if (a.t.tm == 128 ? go(k_linear_part<D, false, 128>, grid, 64 * lin_waves<128>(), a, st)
+                          : go(k_linear_part<D, false, 64>, grid, 64 * lin_waves<64>(), a, st))
             return -1;
         return sum_parts<D>(a, st);
     }
@@ -799,9 +801,9 @@ static int fwd_(const LinPlan& p, LinFwdArgs a, hipStream_t st) {
             return go(k_linear_stream<D, A(), 2, 1, 4, 8>, tiles * n16, 512, a, st);
         }
         const int64_t grid = tiles * ((a.N + 127) / 128);
-        if (a.t.tm == 128) return go(k_linear_fwd<D, A(), 128, false>, grid, kT1Threads, a, st);
-        if (p.once) return go(k_linear_fwd<D, A(), 64, true>, grid, kT1Threads, a, st);
-        return go(k_linear_fwd<D, A(), 64, false>, grid, kT1Threads, a, st);
+        if (a.t.tm == 128) return go(k_linear_fwd<D, A(), 128, false>, grid, 64 * lin_waves<128>(), a, st);
+        if (p.once) return go(k_linear_fwd<D, A(), 64, true>, grid, 64 * lin_waves<64>(), a, st);
+        return go(k_linear_fwd<D, A(), 64, false>, grid, 64 * lin_waves<64>(), a, st);
     });
 }
 
@@ -826,8 +828,8 @@ static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
     if (p.ksplit > 1) {                        // dz W as the sum of its parts
         LinFwdArgs f{p.small, a.dtype, LIN_NONE, a.K, a.N, a.dz, a.w, nullptr, nullptr, a.dx, nullptr, p.ksplit, a.sums};
         const int64_t grid = max_tiles(f.t) * ((a.K + 127) / 128) * p.ksplit;
-        if (p.small.tm == 128 ? go(k_linear_part<D, true, 128>, grid, kT1Threads, f, st)
-                              : go(k_linear_part<D, true, 64>, grid, kT1Threads, f, st))
+        if (p.small.tm == 128 ? go(k_linear_part<D, true, 128>, grid, 64 * lin_waves<128>(), f, st)
+                              : go(k_linear_part<D, true, 64>, grid, 64 * lin_waves<64>(), f, st))
             return -1;
         return sum_parts<D>(f, st);
     }
@@ -837,9 +839,9 @@ static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
     }
     a.t = p.small;
     const int64_t grid = max_tiles(a.t) * ((a.K + 127) / 128);
-    if (a.t.tm == 128) return go(k_linear_dx<D, 128, false>, grid, kT1Threads, a, st);
-    if (p.once) return go(k_linear_dx<D, 64, true>, grid, kT1Threads, a, st);
-    return go(k_linear_dx<D, 64, false>, grid, kT1Threads, a, st);
+    if (a.t.tm == 128) return go(k_linear_dx<D, 128, false>, grid, 64 * lin_waves<128>(), a, st);
+    if (p.once) return go(k_linear_dx<D, 64, true>, grid, 64 * lin_waves<64>(), a, st);
+    return go(k_linear_dx<D, 64, false>, grid, 64 * lin_waves<64>(), a, st);
 }
 
 // dW: 256 x 256 tiles, the ring of 128 x 128 tiles, or the form of few rows.
@@ -848,9 +850,9 @@ static int dw_(const LinBwdArgs& a, hipStream_t st) {
     const int64_t groups = a.t.offsets ? a.t.E : 1, M = a.t.rows;
     const int64_t t256 = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
     const int64_t t128 = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-    if (M < 256 * groups) return go(k_linear_dw_few<D>, t128, kT1Threads, a, st);
+    if (M < 256 * groups) return go(k_linear_dw_few<D>, t128, 256, a, st);
     if (t256 >= 128) return go(k_linear_dw256<D>, t256, kT2Threads, a, st);
-    return go(k_linear_dw<D>, t128, kT1Threads, a, st);
+    return go(k_linear_dw<D>, t128, 64 * lin_waves<128>(), a, st);
 }
 
 template <class D>
@@ -866,7 +868,7 @@ static int bwd_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
         a.t = p.small;
         a.ndw = (int)ndw;
         a.ndx = (int)ndx;
-        return go(k_linear_bwd<D>, ndw + ndx + ndb, kT1Threads, a, st);
+        return go(k_linear_bwd<D>, ndw + ndx + ndb, 64 * lin_waves<128>(), a, st);
     }
     if (a.db && a.dx && p.big.tm) {
         a.ndb = (int)ndb;                          // with dx, below

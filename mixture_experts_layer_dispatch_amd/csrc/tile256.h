@@ -370,40 +370,53 @@ __device__ __forceinline__ void t2_put(const T2Lds& lds, bool nt, uint16_t* out,
 // on a CU then has up to 96 KB of copies in flight: with one step in flight
 // (register-staged) such a product took about 1 us a step, the latency of a
 // load from HBM.
-constexpr int kT1Threads = 256;
+// NW waves in two rows; a wave's columns are NB blocks of 16.
+template <int NW>
+constexpr int t1_nb() { return 16 / NW; }
+template <int TM, int NW>
+using T1Acc = f32x4[TM / 32][t1_nb<NW>()];
 
-template <int TM>
-using T1Acc = f32x4[TM / 32][4];
+// row and first column in the tile of accumulator (mb, nb): rows 16 apart, four columns each
+template <int TM, int NW>
+struct T1Pos {
+    int m_, n_;
+    __device__ __forceinline__ T1Pos()
+        : m_((TM / 2) * (wave_id() & 1) + (lane_id() & 15)),
+          n_(16 * t1_nb<NW>() * (wave_id() >> 1) + 4 * (lane_id() >> 4)) {}
+    __device__ __forceinline__ int m(int mb) const { return m_ + 16 * mb; }
+    __device__ __forceinline__ int n(int nb) const { return n_ + 16 * nb; }
+};
 
-template <class D, bool AKS, bool BKS, int TM, int NST, bool NT = false>
+template <class D, bool AKS, bool BKS, int TM, int NST, int NW, bool NT = false>
 struct T1Loop {
-    using OpA = TileOperand<AKS, TM, 1, kT1Threads>;
-    using OpB = TileOperand<BKS, 128, 1, kT1Threads, NT>;
+    static constexpr int NB = t1_nb<NW>();
+    using OpA = TileOperand<AKS, TM, 1, 64 * NW>;
+    using OpB = TileOperand<BKS, 128, 1, 64 * NW, NT>;
     static constexpr int PER = OpA::PER + OpB::PER;      // copies per thread and step
     const OpA& a;
     const OpB& b;
-    T1Acc<TM>& acc;
+    T1Acc<TM, NW>& acc;
     int wm, wn;
 
-    __device__ __forceinline__ T1Loop(const OpA& a_, const OpB& b_, T1Acc<TM>& acc_)
-        : a(a_), b(b_), acc(acc_), wm((TM / 2) * (wave_id() & 1)), wn(64 * (wave_id() >> 1)) {
+    __device__ __forceinline__ T1Loop(const OpA& a_, const OpB& b_, T1Acc<TM, NW>& acc_)
+        : a(a_), b(b_), acc(acc_), wm((TM / 2) * (wave_id() & 1)), wn(16 * NB * (wave_id() >> 1)) {
 #pragma unroll
         for (int mb = 0; mb < TM / 32; ++mb)
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __device__ __forceinline__ void product(const uint16_t* sa, const uint16_t* sb) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            uint4 fa[TM / 32], fb[4];
+            uint4 fa[TM / 32], fb[NB];
 #pragma unroll
             for (int mb = 0; mb < TM / 32; ++mb) fa[mb] = t2_frag<AKS>(sa, wm + 16 * mb, 32 * s);
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) fb[nb] = t2_frag<BKS>(sb, wn + 16 * nb, 32 * s);
+            for (int nb = 0; nb < NB; ++nb) fb[nb] = t2_frag<BKS>(sb, wn + 16 * nb, 32 * s);
 #pragma unroll
             for (int mb = 0; mb < TM / 32; ++mb)
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = D::mfma(fb[nb], fa[mb], acc[mb][nb]);
+                for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = D::mfma(fb[nb], fa[mb], acc[mb][nb]);
         }
     }
     // step kt on (sa, sb) while step kt + NST - 1 is copied to (na, nb)
@@ -437,14 +450,14 @@ struct T1Ring {
     const T1Ring NAME{NAME##a0, NAME##a1, NAME##a2, NAME##a3, NAME##b0, NAME##b1, NAME##b2, NAME##b3}
 
 // acc = A (x) B over `len` reduction indices
-template <class D, bool AKS, bool BKS, int TM, int NST, bool NT = false>
-__device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Threads>& a,
-                                            const TileOperand<BKS, 128, 1, kT1Threads, NT>& b, int len,
-                                            T1Acc<TM>& acc, const T1Ring& r) {
+template <class D, bool AKS, bool BKS, int TM, int NST, int NW, bool NT = false>
+__device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, 64 * NW>& a,
+                                            const TileOperand<BKS, 128, 1, 64 * NW, NT>& b, int len,
+                                            T1Acc<TM, NW>& acc, const T1Ring& r) {
     static_assert(NST == 3 || NST == 4, "");
     uint16_t *const a0 = r.a0, *const a1 = r.a1, *const a2 = r.a2, *const a3 = r.a3;
     uint16_t *const b0 = r.b0, *const b1 = r.b1, *const b2 = r.b2, *const b3 = r.b3;
-    T1Loop<D, AKS, BKS, TM, NST, NT> l(a, b, acc);
+    T1Loop<D, AKS, BKS, TM, NST, NW, NT> l(a, b, acc);
     const int nk = len / kTK, left = len % kTK;
     if (nk > 0) {
         // steps 0 .. NST - 2; what is past the last one is the last one again,
@@ -499,17 +512,18 @@ __device__ __forceinline__ void t1_mainloop(const TileOperand<AKS, TM, 1, kT1Thr
 // an array, 16-byte chunk c of row r at slot c ^ (r & 15)) as 256-byte row
 // pieces: stored straight from the fragments (16 rows by 32 bytes an
 // instruction) z next to y cost 512 experts of 40 rows 66 us, 42 MB.
-template <int TM, class F>
+template <int TM, int NW, class F>
 __device__ __forceinline__ void t1_put(const T1Ring& ring, bool nt, uint16_t* out, int r0, int r1, int c0,
                                        int ncol, const F& f) {
-    const int wm = wave_id() & 1, wn = 64 * (wave_id() >> 1), t = threadIdx.x, lane = lane_id();
+    constexpr int NB = t1_nb<NW>(), RP = 4 * NW;           // rows of a pass
+    const int wm = wave_id() & 1, wn = 16 * NB * (wave_id() >> 1), t = threadIdx.x, lane = lane_id();
     __syncthreads();                           // the LDS is no longer read
     uint16_t* h = TM == 128 && wm ? ring.b1 : ring.b0;
 #pragma unroll
     for (int mb = 0; mb < TM / 32; ++mb) {
         const int r = (TM == 64 ? 32 * wm : 0) + 16 * mb + (lane & 15);
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
+        for (int nb = 0; nb < NB; ++nb) {
             const int c = wn + 16 * nb + 4 * (lane >> 4);
             *(uint2*)(h + r * 128 + (((c >> 3) ^ (r & 15)) << 3) + (c & 7)) = f(mb, nb);
         }
@@ -519,11 +533,11 @@ __device__ __forceinline__ void t1_put(const T1Ring& ring, bool nt, uint16_t* ou
     if (c0 + 8 * c < ncol) {
         uint16_t* p = out + (int64_t)r0 * ncol + c0 + 8 * c;
 #pragma unroll
-        for (int q = 0; q < TM / 16; ++q) {
-            const int r = 16 * q + (t >> 4);
+        for (int q = 0; q < TM / RP; ++q) {
+            const int r = RP * q + (t >> 4);
             if (r0 + r < r1)
                 st_out(nt, p + (int64_t)r * ncol,
-                       (q < 4 ? ring.b0 : ring.b1) + (r & 63) * 128 + ((c ^ (r & 15)) << 3));
+                       (RP * q < 64 ? ring.b0 : ring.b1) + (r & 63) * 128 + ((c ^ (r & 15)) << 3));
         }
     }
 }
