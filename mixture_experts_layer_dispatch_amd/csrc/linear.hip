@@ -143,8 +143,9 @@ __device__ __forceinline__ WaveTiles wave_tiles(const LinTiles& t, bool tell) {
 
 // Block b's tile: expert e, rows lo .. hi - 1, column tile nt, and its number
 // mt among the row tiles.  An XCD's consecutive tiles are BAND row tiles by the
-// column tiles one after the other: with 256 x 256 tiles and BAND 4, 4 by 8
-// for its 32 CUs, so that its L2 holds 12 operand strips for 32 tiles.
+// column tiles one after the other: with BAND 4, 4 by 8 for its 32 CUs, so that
+// its L2 holds 12 operand strips for 32 tiles (1024 x 4096 x 4096 in 128 x 128
+// tiles, 1 by 32: 45 -> 38 us; dW's 256 x 256 tiles 386 -> 377).
 template <int TM, int BAND>
 __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int& e, int& lo, int& hi, int& nt,
                                          int& mt) {
@@ -158,9 +159,11 @@ __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int&
     }
     if (b >= ntiles * nNt) return false;
     const int L = xcd_remap(b, ntiles * nNt);
-    const int band = L / (BAND * nNt), r = L - band * BAND * nNt, rows = min(BAND, ntiles - BAND * band);
+    // (small groups share weights within a group only: no bands)
+    const int B = TM < 256 && t.offsets ? 1 : BAND;
+    const int band = L / (B * nNt), r = L - band * B * nNt, rows = min(B, ntiles - B * band);
     nt = r / rows;
-    mt = BAND * band + (r - nt * rows);
+    mt = B * band + (r - nt * rows);
     if (!t.offsets) {
         e = 0;
         lo = mt * TM;
@@ -189,15 +192,18 @@ __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int&
     return true;
 }
 
-// dW: block b's expert e, tile (mt, nt) of nMt by nNt, and the expert's rows lo, n.
+// dW: block b's expert e, tile (mt, nt) of nMt by nNt, and the expert's rows lo,
+// n; tiles in bands of BAND row tiles, as above.
+template <int BAND>
 __device__ __forceinline__ bool lin_wtile(const LinTiles& t, int nMt, int nNt, int b, int& e, int& mt, int& nt,
                                           int& lo, int& n) {
     const int per = nMt * nNt, total = (t.offsets ? t.E : 1) * per;
     if (b >= total) return false;
     const int L = xcd_remap(b, total), rem = L % per;
     e = L / per;
-    mt = rem / nNt;
-    nt = rem - mt * nNt;
+    const int band = rem / (BAND * nNt), r = rem - band * BAND * nNt, rows = min(BAND, nMt - BAND * band);
+    nt = r / rows;
+    mt = BAND * band + (r - nt * rows);
     lo = 0;
     n = t.rows;
     if (t.offsets) n = group_rows(t, e, lo, true);
@@ -248,7 +254,7 @@ template <class D, int ACT, int TM, bool ONCE>
 __global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
     constexpr int TN = 128;
     int e, lo, hi, nt, mt;
-    if (!lin_tile<TM, 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
+    if (!lin_tile<TM, TM == 128 ? 4 : 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
     const int n0 = nt * TN;
     T1_RING(ring, TM, lin_stages<TM>());
     T1Acc<TM, lin_waves<TM>()> acc;
@@ -276,7 +282,7 @@ __global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_line
 // ================================================================ split reductions
 // Too few tiles for the chip (dense): each tile's reduction is split into
 // ksplit ascending parts of whole 64-deep steps, a block each, whose fp32 sums
-// k_linear_sum adds in order (128 x 4096 x 4096: @SPLIT@).  N: output columns,
+// k_linear_sum adds in order (128 x 4096 x 4096: 39 -> 17 us).  N: output columns,
 // K: reduction length, w: [N, K], or (BKS) [K, N].
 template <class D, bool BKS, int TM>
 __global__ __launch_bounds__(64 * lin_waves<TM>(), 1) void k_linear_part(LinFwdArgs a) {
@@ -414,7 +420,7 @@ template <class D, int TM, bool ONCE>
 __device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
     constexpr int TN = 128;
     int e, lo, hi, nt, mt;
-    if (!lin_tile<TM, 1>(a.t, (a.K + TN - 1) / TN, block, e, lo, hi, nt, mt)) return;
+    if (!lin_tile<TM, TM == 128 ? 4 : 1>(a.t, (a.K + TN - 1) / TN, block, e, lo, hi, nt, mt)) return;
     const int n0 = nt * TN;
     T1Acc<TM, lin_waves<TM>()> acc;
     {
@@ -440,7 +446,7 @@ template <class D>
 __device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
     constexpr int TM = 128, TN = 128;
     int e, mt, nt, lo, n;
-    if (!lin_wtile(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
+    if (!lin_wtile<4>(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
     T1Acc<TM, lin_waves<TM>()> acc;
     {
@@ -473,7 +479,7 @@ __global__ __launch_bounds__(256, 4) void k_linear_dw_few(LinBwdArgs a) {
     __shared__ __attribute__((aligned(16))) uint16_t sm[TM * TN];
     static_assert(TM * TN == 2 * kT2Half, "the operands' stage and the tile take the same LDS");
     int e, mt, nt, lo, n;
-    if (!lin_wtile(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
+    if (!lin_wtile<1>(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, blockIdx.x, e, mt, nt, lo, n)) return;
     const int m0 = mt * TM, n0 = nt * TN;
     uint16_t *const sa = sm, *const sb = sm + kT2Half;
     T1Acc<TM, 4> acc;
@@ -623,7 +629,7 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
     int e, mt, nt, lo, n;
-    if (!lin_wtile(a.t, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
+    if (!lin_wtile<4>(a.t, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
     T2_LDS(lds);
     T2Acc acc;
     {
@@ -726,14 +732,17 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
         p.small.tm = M <= 16 ? 16 : 32;
         return p;
     }
-    if (((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 128) {
+    if (((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 144) {
         p.big.tm = 256;
         return p;
     }
     p.small.tm = M <= 64 ? 64 : 128;
     const int64_t tiles = max_tiles(p.small) * ((C + 127) / 128);
+    // (reductions below 24 steps: the second launch and the parts' traffic cost
+    // more than they save, 1024 x 1024 x 1024 18 instead of 12 us; 128 x 1000 x
+    // 1544 gains, 15.7 -> 11.3)
     const int64_t ks = 256 / tiles < R / 256 ? 256 / tiles : R / 256;
-    p.ksplit = ks < 2 ? 1 : ks < 16 ? (int)ks : 16;
+    p.ksplit = ks < 2 || R < 24 * kTK ? 1 : ks < 16 ? (int)ks : 16;
     return p;
 }
 
