@@ -389,7 +389,7 @@ MOE_API moe_status moe_unpermute_forward(const moe_config* cfg, const moe_sched*
  *   dw [T, k] fp32 (written): <o[row(t,j)], dy[t]>;
  *   d_logits [T, E] fp32 (written; may be NULL): through the softmax over the
  *   chosen logits, zero for experts a token did not choose.
- * d_o must not overlap o.  Reads sched's row_of_slot, topk_w and (for d_logits)
+ * d_o must not overlap o or dy.  Reads sched's row_of_slot, topk_w and (for d_logits)
  * topk_idx; workspace as in moe_permute_forward. */
 MOE_API moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
                                           const void* o, const void* dy, void* d_o, float* dw, float* d_logits,
@@ -428,7 +428,8 @@ MOE_API moe_status moe_linear_workspace_size(const moe_linear_config* cfg, size_
  *   Rows in no group are neither read nor written.  A group that is not inside
  *   [0, M] or not ascending is skipped and sets MOE_DEVERR_BAD_OFFSETS.
  *   fp32 accumulation; the sum, bias, activation and residual in fp32, y and z
- *   rounded once each.  Apart from residual = y, outputs overlap no input. */
+ *   rounded once each.  Apart from residual = y, outputs overlap no input
+ *   and each other (the same pointer twice is refused). */
 MOE_API moe_status moe_linear_forward(const moe_linear_config* cfg, const int32_t* offsets, const void* x,
                                       const void* w, const void* bias, const void* residual, void* y, void* z,
                                       void* workspace, size_t workspace_bytes, void* stream);
@@ -440,7 +441,7 @@ MOE_API moe_status moe_linear_forward(const moe_linear_config* cfg, const int32_
  *   z: as moe_linear_forward wrote it (not read if act is MOE_ACT_NONE); x is
  *   read for dw, w for dx (else they may be NULL).
  *   dz is rounded to cfg->dtype once as the products' operand (db sums it
- *   unrounded); outputs are overwritten.  A group without rows gets dw = 0 and
+ *   unrounded); outputs are overwritten and overlap nothing else.  A group without rows gets dw = 0 and
  *   db = 0; rows of dx in no group are left as they were. */
 MOE_API moe_status moe_linear_backward(const moe_linear_config* cfg, const int32_t* offsets, const void* x,
                                        const void* w, const void* z, const void* dy, void* dx, void* dw, void* db,

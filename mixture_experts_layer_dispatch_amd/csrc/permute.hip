@@ -65,7 +65,9 @@ __device__ __forceinline__ void st_row(uint4* p, const uint4& v) {
 
 // ================================================================ permute
 // A wave takes one 1 KB segment (64 chunks of 16 bytes) of a token's row and
-// writes it k times.
+// writes it k times.  (A wave per expert row, reading its token's row, writes in
+// order but reads every row k times: 16384 tokens x 10 x 4096 366 us instead of
+// 297; four segments to a wave 301.)
 template <bool NT>
 __global__ __launch_bounds__(256) void k_permute(const uint4* __restrict__ x, int C, int nseg,
                                                  const int32_t* __restrict__ row_of_slot, int T, int k, int S,

@@ -40,24 +40,29 @@ def test_linear_workspace_size_needs_its_arguments():
     assert B.lib().moe_linear_workspace_size(_lc(), None) == B.MOE_ERR_INVALID_ARG
 
 
-def _fwd(c=None, off=None, x=FAKE, w=FAKE, bias=None, res=None, y=FAKE, z=None, ws=FAKE, n=BIG):
+X, W, Y, Z, DY, DX, DW, DB = (FAKE + (i << 20) for i in range(1, 9))    # buffers of their own
+
+
+def _fwd(c=None, off=None, x=X, w=W, bias=None, res=None, y=Y, z=None, ws=FAKE, n=BIG):
     return B.lib().moe_linear_forward(c or _lc(), off, x, w, bias, res, y, z, ws, n, None)
 
 
-def _bwd(c=None, off=None, x=FAKE, w=FAKE, z=FAKE, dy=FAKE, dx=FAKE, dw=FAKE, db=FAKE, ws=FAKE, n=BIG):
+def _bwd(c=None, off=None, x=X, w=W, z=Z, dy=DY, dx=DX, dw=DW, db=DB, ws=FAKE, n=BIG):
     return B.lib().moe_linear_backward(c or _lc(act=1), off, x, w, z, dy, dx, dw, db, ws, n, None)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(w=None), dict(y=None), dict(x=FAKE + 8), dict(w=FAKE + 2),
                                 dict(y=FAKE + 4), dict(bias=FAKE + 8), dict(res=FAKE + 8), dict(z=FAKE + 8),
-                                dict(off=FAKE), dict(c=_lc(E=4)), dict(c=_lc(E=4), off=FAKE + 2), dict(c=_lc(N=12))])
+                                dict(off=FAKE), dict(c=_lc(E=4)), dict(c=_lc(E=4), off=FAKE + 2), dict(c=_lc(N=12)),
+                                dict(y=X), dict(y=W), dict(z=Y), dict(z=X), dict(z=Z, res=Z), dict(bias=Y)])
 def test_linear_forward_refuses(kw):
     assert _fwd(**kw) == B.MOE_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("kw", [dict(dy=None), dict(z=None), dict(z=FAKE + 8), dict(dx=None, dw=None, db=None),
                                 dict(w=None), dict(x=None), dict(dx=FAKE + 8), dict(dw=FAKE + 2), dict(db=FAKE + 8),
-                                dict(dy=FAKE + 8), dict(off=FAKE), dict(c=_lc(E=2, act=1))])
+                                dict(dy=FAKE + 8), dict(off=FAKE), dict(c=_lc(E=2, act=1)),
+                                dict(dx=X), dict(dx=DY), dict(dw=W), dict(dw=DX), dict(db=DY), dict(db=DW)])
 def test_linear_backward_refuses(kw):
     assert _bwd(**kw) == B.MOE_ERR_INVALID_ARG
 
@@ -89,8 +94,12 @@ def test_permute_and_unpermute_refuse():
     assert L.moe_unpermute_forward(cfg, rows_only, 0, FAKE, None, FAKE, FAKE, 256, None) == bad
     assert L.moe_unpermute_forward(cfg, s, 0, FAKE, FAKE + 8, FAKE, FAKE, 256, None) == bad
     assert L.moe_unpermute_forward(cfg, s, 0, FAKE, None, None, FAKE, 256, None) == bad
+    for p in ([X, DY, X, DW], [X, DY, DY, DW]):            # d_o is o, or dy
+        assert L.moe_unpermute_backward(cfg, s, 0, *p, FAKE, FAKE, 256, None) == bad
+    assert L.moe_permute_forward(cfg, s, 0, X, X, FAKE, 256, None) == bad
+    assert L.moe_unpermute_forward(cfg, s, 0, X, None, X, FAKE, 256, None) == bad
     for i in range(4):                                    # o, dy, d_o, dw
-        p = [FAKE] * 4
+        p = [X, DY, Y, DW]
         p[i] = None
         assert L.moe_unpermute_backward(cfg, s, 0, *p, FAKE, FAKE, 256, None) == bad
     part = B.moe_sched(row_of_slot=FAKE, topk_w=FAKE)     # d_logits needs topk_idx

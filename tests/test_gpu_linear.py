@@ -94,7 +94,7 @@ def check_products(out, x, w, zs, dy, lc, off, n):
         assert_within(name, got, want, tol)
 
 
-DENSE = [(1, 8, 8), (1, 4096, 1024), (3, 264, 136), (16, 128, 64), (17, 1000, 520), (64, 72, 8), (65, 136, 200),
+DENSE = [(1, 8, 8), (1, 4096, 1024), (3, 264, 136), (48, 200, 2056), (64, 1544, 72), (130, 1608, 2104), (16, 128, 64), (17, 1000, 520), (64, 72, 8), (65, 136, 200),
          (129, 384, 328), (300, 1032, 256), (777, 520, 1544), (1024, 512, 768), (1300, 2056, 264)]
 
 
@@ -118,7 +118,7 @@ def test_activations_biases_residuals(M, act, bias, residual, dtype):
     c.check(out)
 
 
-COUNTS = [[0, 0, 0], [1], [0, 1, 0, 5, 64], [65, 0, 63, 128, 1], [300, 7, 0, 520], [3] * 70, [40] * 33,
+COUNTS = [[150, 130, 170, 0, 200], [100, 90, 70], [0, 0, 0], [1], [0, 1, 0, 5, 64], [65, 0, 63, 128, 1], [300, 7, 0, 520], [3] * 70, [40] * 33,
           [1000, 0, 0, 2], [257, 256, 255, 511, 513]]
 
 
@@ -179,6 +179,44 @@ def test_large_groups(counts):
     out = c.outputs()
     c.run(out)
     c.check(out)
+
+
+def test_outputs_stored_past_the_caches():
+    """Outputs of more than 32 MB, and lists of tiles for few groups."""
+    c = Lin(59, 4100, 4104, 72, BF, "relu")
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+    c = Lin(60, 4100, 72, 4104, FP, "silu")               # dx, with db in front of its tiles
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+    rng = np.random.default_rng(6)
+    c = Lin(61, 17000, 1032, 64, BF, "silu", list(np.bincount(rng.integers(0, 110, 16990), minlength=110)))
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+    c = Lin(62, 20000, 2048, 64, BF, "relu", [9000, 0, 3001, 7990])
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+
+
+def test_groups_may_start_behind_the_first_row():
+    c = Lin(63, 300, 136, 72, BF, "gelu", [100, 0, 150])
+    out = c.outputs()
+    c.run(out)
+    pad = torch.full_like(c.x[:7], float("nan"))
+    for name, fill in (("x", pad), ("res", c.res[:7]), ("dy", c.dy[:7] * float("nan"))):
+        setattr(c, name, torch.cat([fill, getattr(c, name)])[:300].contiguous())
+    c.off = c.off + 7
+    got = c.outputs()
+    c.run(got)
+    for n in ("y", "z", "dx"):
+        assert torch.equal(got[n][7:257], out[n][:250]), n
+        assert (got[n][:7] == -77).all() and (got[n][257:] == -77).all(), n
+    for n in ("dw", "db"):
+        assert torch.equal(got[n], out[n]), n
 
 
 def test_residual_may_be_the_output():
