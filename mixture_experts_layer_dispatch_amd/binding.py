@@ -607,23 +607,33 @@ def alloc_error_word(device="cuda") -> torch.Tensor:
     return torch.zeros(256, dtype=torch.uint8, device=device)
 
 
-def _check_tensors(specs):
-    """_validate for the building blocks: tensors (name, tensor, shape, dtype;
-    a None tensor is an optional one that was not given), which have to be
-    on the current device, where the call's work is enqueued."""
-    at = -1
-    for name, t, shape, dtype in specs:
+def _check_tensors(required, optional=()):
+    """_validate for the building blocks: (name, tensor, shape, dtype) of the
+    tensors a call needs and of those it may be given, which have to be on
+    the current device, where the call's work is enqueued."""
+    at = None
+    same = True
+    for name, t, shape, dtype in required:
+        if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+            _refuse(name, t, shape, dtype)
+        d = t.get_device()
+        if d != at:
+            same = same and at is None
+            at = d
+    for name, t, shape, dtype in optional:
         if t is None:
             continue
-        if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
+        if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
             _refuse(name, t, shape, dtype)
-        if at < 0:
-            at = t.get_device()
-    if at < 0 or at != torch.cuda.current_device() or any(t is not None and t.get_device() != at for _, t, _, _ in specs):
-        _refuse_device(specs)
+        if t.get_device() != at:
+            same = False
+    if not same or at < 0 or at != torch.cuda.current_device():
+        _refuse_device([s for s in (*required, *optional) if s[1] is not None])
 
 
 def _refuse(name, t, shape, dtype):
+    if t is None:
+        raise ValueError(f"{name}: missing")
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.shape != shape:
@@ -635,124 +645,107 @@ def _refuse(name, t, shape, dtype):
 
 def _refuse_device(specs):
     for name, t, _, _ in specs:
-        if t is not None and not t.is_cuda:
+        if not t.is_cuda:
             raise ValueError(f"{name}: must be on the GPU, found on {t.device}")
     here = torch.cuda.current_device()
     for name, t, _, _ in specs:
-        if t is not None and t.get_device() != here:
+        if t.get_device() != here:
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
-
-
-def _required(**tensors):
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{name}: missing")
-
-
-def _rows_checks(cfg: Config, sched: dict, ws, first: str, data, names):
-    """Checks what every permute / unpermute call takes; returns the tensors' dtype code."""
-    if not isinstance(data, torch.Tensor) or data.dtype not in DTYPES:
-        raise ValueError(f"{first}: expected a bf16, fp16 or fp32 tensor")
-    if ws is None:
-        raise ValueError("workspace: missing")
-    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
-    if 0 <= n < 256:
-        raise ValueError(f"workspace: {n} bytes, at least 256 are needed")
-    specs = [("workspace", ws, (n,), torch.uint8)]
-    for name in names:
-        if sched.get(name) is None:
-            raise ValueError(f"sched[{name!r}]: missing")
-        if name == "row_of_slot":
-            specs.append(("sched['row_of_slot']", sched[name], (cfg.S,), torch.int32))
-        elif name == "topk_w":
-            specs.append(("sched['topk_w']", sched[name], (cfg.T, cfg.k), torch.float32))
-        else:
-            specs.append(("sched['topk_idx']", sched[name], (cfg.T, cfg.k), torch.int32))
-    return DTYPES[data.dtype], specs
-
-
-def _some_sched(sched: dict, names) -> moe_sched:
-    st = moe_sched()
-    for name in names:
-        setattr(st, name, sched[name].data_ptr())
-    return st
-
-
-def moe_permute_forward(cfg: Config, sched: dict, x: torch.Tensor, xs: torch.Tensor, ws: torch.Tensor, stream=None):
-    """xs[row_of_slot[t, j]] = x[t]: token rows [T, H] to their experts' rows [S, H] (bf16, fp16 or fp32)."""
-    _required(x=x, xs=xs)
-    names = ("row_of_slot",)
-    dt, specs = _rows_checks(cfg, sched, ws, "x", x, names)
-    _check_tensors(specs + [("x", x, (cfg.T, cfg.H), x.dtype), ("xs", xs, (cfg.S, cfg.H), x.dtype)])
-    _check(lib().moe_permute_forward(cfg.c(), _some_sched(sched, names), dt, x.data_ptr(), xs.data_ptr(),
-                                     ws.data_ptr(), ws.numel(), _stream(stream)), "moe_permute_forward")
-
-
-def moe_permute_backward(cfg: Config, sched: dict, dxs: torch.Tensor, dx: torch.Tensor, ws: torch.Tensor, stream=None):
-    """dx[t] = sum_j dxs[row_of_slot[t, j]]."""
-    _required(dxs=dxs, dx=dx)
-    names = ("row_of_slot",)
-    dt, specs = _rows_checks(cfg, sched, ws, "dxs", dxs, names)
-    _check_tensors(specs + [("dxs", dxs, (cfg.S, cfg.H), dxs.dtype), ("dx", dx, (cfg.T, cfg.H), dxs.dtype)])
-    _check(lib().moe_permute_backward(cfg.c(), _some_sched(sched, names), dt, dxs.data_ptr(), dx.data_ptr(),
-                                      ws.data_ptr(), ws.numel(), _stream(stream)), "moe_permute_backward")
-
-
-def moe_unpermute_forward(cfg: Config, sched: dict, o: torch.Tensor, y: torch.Tensor, ws: torch.Tensor, residual=None,
-                          stream=None):
-    """y[t] = sum_j topk_w[t, j] o[row_of_slot[t, j]] (+ residual[t], which may be y itself)."""
-    _required(o=o, y=y)
-    names = ("row_of_slot", "topk_w")
-    dt, specs = _rows_checks(cfg, sched, ws, "o", o, names)
-    _check_tensors(specs + [("o", o, (cfg.S, cfg.H), o.dtype), ("y", y, (cfg.T, cfg.H), o.dtype),
-                            ("residual", residual, (cfg.T, cfg.H), o.dtype)])
-    _check(lib().moe_unpermute_forward(cfg.c(), _some_sched(sched, names), dt, o.data_ptr(), _ptr(residual),
-                                       y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
-           "moe_unpermute_forward")
-
-
-def moe_unpermute_backward(cfg: Config, sched: dict, o: torch.Tensor, dy: torch.Tensor, do: torch.Tensor,
-                           dw: torch.Tensor, ws: torch.Tensor, d_logits=None, stream=None):
-    """do[row(t, j)] = topk_w[t, j] dy[t]; dw[t, j] = <o[row(t, j)], dy[t]>; d_logits [T, E] through the
-    softmax over the chosen logits.  The residual's gradient is dy itself."""
-    _required(o=o, dy=dy, do=do, dw=dw)
-    names = ("row_of_slot", "topk_w") if d_logits is None else ("row_of_slot", "topk_w", "topk_idx")
-    dt, specs = _rows_checks(cfg, sched, ws, "o", o, names)
-    f32_ = torch.float32
-    _check_tensors(specs + [("o", o, (cfg.S, cfg.H), o.dtype), ("dy", dy, (cfg.T, cfg.H), o.dtype),
-                            ("do", do, (cfg.S, cfg.H), o.dtype), ("dw", dw, (cfg.T, cfg.k), f32_),
-                            ("d_logits", d_logits, (cfg.T, cfg.E), f32_)])
-    _check(lib().moe_unpermute_backward(cfg.c(), _some_sched(sched, names), dt, o.data_ptr(), dy.data_ptr(),
-                                        do.data_ptr(), dw.data_ptr(), _ptr(d_logits), ws.data_ptr(), ws.numel(),
-                                        _stream(stream)), "moe_unpermute_backward")
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_SCHED_ROWS, _SCHED_WEIGHTS = ("row_of_slot",), ("row_of_slot", "topk_w")
+
+
+def _rows_checks(cfg: Config, sched: dict, ws, first: str, data, names):
+    """What every permute / unpermute call takes: (dtype code of the data, moe_sched of the named
+    arrays, specs of those and the workspace)."""
+    if not isinstance(data, torch.Tensor) or data.dtype not in DTYPES:
+        raise ValueError(f"{first}: {'missing' if data is None else 'expected a bf16, fp16 or fp32 tensor'}")
+    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
+    if 0 <= n < 256:
+        raise ValueError(f"workspace: {n} bytes, at least 256 are needed")
+    specs = [("workspace", ws, (n,), torch.uint8)]
+    st = moe_sched()
+    for name in names:
+        t = sched.get(name)
+        shape = (cfg.T * cfg.k,) if name == "row_of_slot" else (cfg.T, cfg.k)
+        specs.append((name, t, shape, torch.float32 if name == "topk_w" else torch.int32))
+        if isinstance(t, torch.Tensor):
+            setattr(st, name, t.data_ptr())
+    return DTYPES[data.dtype], st, specs
+
+
+def moe_permute_forward(cfg: Config, sched: dict, x: torch.Tensor, xs: torch.Tensor, ws: torch.Tensor, stream=None):
+    """xs[row_of_slot[t, j]] = x[t]: token rows [T, H] to their experts' rows [S, H] (bf16, fp16 or fp32)."""
+    dt, st, specs = _rows_checks(cfg, sched, ws, "x", x, _SCHED_ROWS)
+    specs += [("x", x, (cfg.T, cfg.H), x.dtype), ("xs", xs, (cfg.T * cfg.k, cfg.H), x.dtype)]
+    _check_tensors(specs)
+    _check(lib().moe_permute_forward(cfg.c(), st, dt, x.data_ptr(), xs.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     _stream(stream)), "moe_permute_forward")
+
+
+def moe_permute_backward(cfg: Config, sched: dict, dxs: torch.Tensor, dx: torch.Tensor, ws: torch.Tensor, stream=None):
+    """dx[t] = sum_j dxs[row_of_slot[t, j]]."""
+    dt, st, specs = _rows_checks(cfg, sched, ws, "dxs", dxs, _SCHED_ROWS)
+    specs += [("dxs", dxs, (cfg.T * cfg.k, cfg.H), dxs.dtype), ("dx", dx, (cfg.T, cfg.H), dxs.dtype)]
+    _check_tensors(specs)
+    _check(lib().moe_permute_backward(cfg.c(), st, dt, dxs.data_ptr(), dx.data_ptr(), ws.data_ptr(), ws.numel(),
+                                      _stream(stream)), "moe_permute_backward")
+
+
+def moe_unpermute_forward(cfg: Config, sched: dict, o: torch.Tensor, y: torch.Tensor, ws: torch.Tensor, residual=None,
+                          stream=None):
+    """y[t] = sum_j topk_w[t, j] o[row_of_slot[t, j]] (+ residual[t], which may be y itself)."""
+    dt, st, specs = _rows_checks(cfg, sched, ws, "o", o, _SCHED_WEIGHTS)
+    specs += [("o", o, (cfg.T * cfg.k, cfg.H), o.dtype), ("y", y, (cfg.T, cfg.H), o.dtype)]
+    _check_tensors(specs, (("residual", residual, (cfg.T, cfg.H), o.dtype),))
+    _check(lib().moe_unpermute_forward(cfg.c(), st, dt, o.data_ptr(), _ptr(residual), y.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), _stream(stream)), "moe_unpermute_forward")
+
+
+def moe_unpermute_backward(cfg: Config, sched: dict, o: torch.Tensor, dy: torch.Tensor, do: torch.Tensor,
+                           dw: torch.Tensor, ws: torch.Tensor, d_logits=None, stream=None):
+    """do[row(t, j)] = topk_w[t, j] dy[t]; dw[t, j] = <o[row(t, j)], dy[t]>; d_logits [T, E] through the
+    softmax over the chosen logits.  The residual's gradient is dy itself."""
+    names = _SCHED_WEIGHTS if d_logits is None else (*_SCHED_WEIGHTS, "topk_idx")
+    dt, st, specs = _rows_checks(cfg, sched, ws, "o", o, names)
+    rows, f32_ = (cfg.T * cfg.k, cfg.H), torch.float32
+    specs += [("o", o, rows, o.dtype), ("dy", dy, (cfg.T, cfg.H), o.dtype), ("do", do, rows, o.dtype),
+              ("dw", dw, (cfg.T, cfg.k), f32_)]
+    _check_tensors(specs, (("d_logits", d_logits, (cfg.T, cfg.E), f32_),))
+    _check(lib().moe_unpermute_backward(cfg.c(), st, dt, o.data_ptr(), dy.data_ptr(), do.data_ptr(), dw.data_ptr(),
+                                        _ptr(d_logits), ws.data_ptr(), ws.numel(), _stream(stream)),
+           "moe_unpermute_backward")
+
+
 def _linear_checks(lc: LinearConfig, ws, offsets):
-    """(moe_linear_config, specs of the workspace and offsets, leading shape of w and bias)."""
+    """(moe_linear_config, specs of the workspace and the offsets, leading shape of w and bias)."""
     c, need = lc.checked
-    _required(workspace=ws)
     n = ws.numel() if isinstance(ws, torch.Tensor) else -1
     if 0 <= n < need:
         raise ValueError(f"workspace: {n} bytes, the config needs {need}")
-    if (offsets is None) != (lc.E == 0):
+    E = lc.E
+    if (offsets is None) != (E == 0):
         raise ValueError("offsets: given if and only if E > 0")
-    return c, [("workspace", ws, (n,), torch.uint8), ("offsets", offsets, (lc.E + 1,), torch.int32)], \
-        ((lc.E,) if lc.E else ())
+    specs = [("workspace", ws, (n,), torch.uint8)]
+    if E == 0:
+        return c, specs, ()
+    specs.append(("offsets", offsets, (E + 1,), torch.int32))
+    return c, specs, (E,)
 
 
 def moe_linear_forward(lc: LinearConfig, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, ws: torch.Tensor,
                        bias=None, residual=None, z=None, offsets=None, stream=None):
     """y = act(x w^T + bias) + residual; z, if given, keeps x w^T + bias for the backward.  With E > 0
     rows offsets[e] .. offsets[e + 1] take w[e], bias[e].  residual may be y itself."""
-    _required(x=x, w=w, y=y)
     c, specs, lead = _linear_checks(lc, ws, offsets)
     dt, mn = lc.dtype, (lc.M, lc.N)
-    _check_tensors(specs + [("x", x, (lc.M, lc.K), dt), ("w", w, (*lead, lc.N, lc.K), dt), ("y", y, mn, dt),
-                            ("bias", bias, (*lead, lc.N), dt), ("residual", residual, mn, dt), ("z", z, mn, dt)])
+    specs += [("x", x, (lc.M, lc.K), dt), ("w", w, (*lead, lc.N, lc.K), dt), ("y", y, mn, dt)]
+    _check_tensors(specs, (("bias", bias, (*lead, lc.N), dt), ("residual", residual, mn, dt), ("z", z, mn, dt)))
     _check(lib().moe_linear_forward(c, _ptr(offsets), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
                                     y.data_ptr(), _ptr(z), ws.data_ptr(), ws.numel(), _stream(stream)),
            "moe_linear_forward")
@@ -763,19 +756,16 @@ def moe_linear_backward(lc: LinearConfig, x, w, z, dy: torch.Tensor, ws: torch.T
     """The gradients whose output is given: dx = dz w, dw = dz^T x, db = sum of dz, with dz = dy act'(z)
     (z as moe_linear_forward kept it; not read if act is "none").  x is needed for dw, w for dx.  The
     residual's gradient is dy itself."""
-    _required(dy=dy)
-    if lc.act != "none":
-        _required(z=z)
-    if dx is not None:
-        _required(w=w)
-    if dw is not None:
-        _required(x=x)
     if dx is None and dw is None and db is None:
         raise ValueError("dx, dw, db: at least one is needed")
     c, specs, lead = _linear_checks(lc, ws, offsets)
     dt, mn, mk, nk = lc.dtype, (lc.M, lc.N), (lc.M, lc.K), (*lead, lc.N, lc.K)
-    _check_tensors(specs + [("x", x, mk, dt), ("w", w, nk, dt), ("z", z, mn, dt), ("dy", dy, mn, dt),
-                            ("dx", dx, mk, dt), ("dw", dw, nk, dt), ("db", db, (*lead, lc.N), dt)])
+    specs.append(("dy", dy, mn, dt))
+    optional = [("dx", dx, mk, dt), ("dw", dw, nk, dt), ("db", db, (*lead, lc.N), dt)]
+    (specs if lc.act != "none" else optional).append(("z", z, mn, dt))
+    (specs if dx is not None else optional).append(("w", w, nk, dt))
+    (specs if dw is not None else optional).append(("x", x, mk, dt))
+    _check_tensors(specs, optional)
     _check(lib().moe_linear_backward(c, _ptr(offsets), _ptr(x), _ptr(w), _ptr(z), dy.data_ptr(), _ptr(dx), _ptr(dw),
                                      _ptr(db), ws.data_ptr(), ws.numel(), _stream(stream)), "moe_linear_backward")
 
