@@ -171,15 +171,18 @@ __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int&
         return true;
     }
     if (t.list) {
-        int a = 0, z = t.E;
-        while (z - a > 1) {
-            const int mid = (a + z) >> 1;
-            if (t.list[mid] <= mt) a = mid;
-            else z = mid;
-        }
-        e = a;
+        // the last group whose tiles start at or before mt, in two loads: 64
+        // groups apart, then those between (a binary search is ten loads that
+        // wait for each other, 0.5 us each: @SEARCH@)
+        const int per = (t.E + 63) >> 6, lane = lane_id();
+        const bool far = lane * per < t.E && t.list[min(lane * per, t.E)] <= mt;
+        const int e0 = per * (63 - __builtin_clzll(__ballot(far)));
+        const bool near = lane < per && e0 + lane < t.E;
+        const int pre = t.list[min(e0 + lane, t.E)];
+        const int i = 63 - __builtin_clzll(__ballot(near && pre <= mt));
+        e = e0 + i;
         const int a0 = t.offsets[e];
-        lo = a0 + (mt - t.list[e]) * TM;
+        lo = a0 + (mt - __builtin_amdgcn_readlane(pre, i)) * TM;
         hi = min(lo + TM, t.offsets[e + 1]);
     } else {
         // the last group whose tiles start at or before mt (one without tiles starts where the next one does)
