@@ -71,8 +71,9 @@ __device__ __forceinline__ float act_grad(float z) {
     if constexpr (ACT == LIN_RELU) return z > 0.f ? 1.f : 0.f;
     else if constexpr (ACT == LIN_GELU) return normal_cdf(z) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
     else if constexpr (ACT == LIN_GELU_TANH) {
-        const float p = sigm(2.0f * kTanhC * (z + kTanhA * z * z * z));
-        return p + z * p * (1.0f - p) * 2.0f * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
+        const float p = sigm(2.0f * kTanhC * (z + kTanhA * z * z * z)), d = p * (1.0f - p);
+        // (where the sigmoid is 0 or 1, z^2 may be infinite)
+        return d == 0.f ? p : p + z * d * 2.0f * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
     } else if constexpr (ACT == LIN_SILU) {
         const float p = sigm(z);
         return p * (1.0f + z * (1.0f - p));
@@ -173,7 +174,8 @@ __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int&
     if (t.list) {
         // the last group whose tiles start at or before mt, in two loads: 64
         // groups apart, then those between (a binary search is ten loads that
-        // wait for each other, 0.5 us each: @SEARCH@)
+        // wait for each other, 0.5 us each: 1518 x 1520 x 944 at
+        // 425 experts 289 instead of 253 us)
         const int per = (t.E + 63) >> 6, lane = lane_id();
         const bool far = lane * per < t.E && t.list[min(lane * per, t.E)] <= mt;
         const int e0 = per * (63 - __builtin_clzll(__ballot(far)));
@@ -252,7 +254,9 @@ __device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int row, int
 
 // ONCE: a weight tile feeds one row tile, so it is copied non-temporally (512
 // experts of 40 rows, 4.3 GB of weights: 801 -> 698 us, 6.45 TB/s; where two
-// row tiles read it: 39 -> 46 us).
+// row tiles read it: 39 -> 46 us).  Weight rows have to be whole 128-byte lines
+// for that: pieces of a line that two steps read come twice (K = 4072: 1122
+// non-temporally, 916 plainly).
 template <class D, int ACT, int TM, bool ONCE>
 __global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
     constexpr int TN = 128;
@@ -727,7 +731,7 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
             p.small.tm = 16;
             return p;
         }
-        p.once = M <= 64LL * E;
+        p.once = M <= 64LL * E && (dx ? C : R) % 64 == 0;
         return p;
     }
     if (!dx && M <= 32) {

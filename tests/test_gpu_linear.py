@@ -181,6 +181,26 @@ def test_large_groups(counts):
     c.check(out)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("act", list(B.ACTS))
+def test_activations_at_the_ends_of_the_type(act, dtype):
+    """Pre-activations up to the type's largest and lowest values (a mask's fill, an outlier)."""
+    f = torch.finfo(dtype)
+    z = torch.tensor([f.min, f.min / 2, -1e4, -30, -8, -6.1, -5.9, -1e-3, 0.0, 1e-3, 5.9, 6.1, 8, 30, 1e4, f.max],
+                     dtype=torch.float64).to(dtype).cuda()
+    lc = B.LinearConfig(M=8, N=16, K=8, dtype=dtype, act=act)
+    x, w = torch.zeros(8, 8, dtype=dtype, device="cuda"), torch.zeros(16, 8, dtype=dtype, device="cuda")
+    out = {"y": torch.empty(8, 16, dtype=dtype, device="cuda"), "z": torch.empty(8, 16, dtype=dtype, device="cuda")}
+    ws = B.alloc_linear_workspace(lc)
+    B.moe_linear_forward(lc, x, w, out["y"], ws, bias=z, z=out["z"])
+    dy = torch.ones(8, 16, dtype=dtype, device="cuda")
+    out.update(dx=torch.empty_like(x), dw=torch.empty_like(w), db=torch.empty_like(z))
+    B.moe_linear_backward(lc, x, w, out["z"], dy, ws, dx=out["dx"], dw=out["dw"], db=out["db"])
+    assert torch.equal(out["z"], z.expand(8, 16))
+    with np.errstate(over="ignore"):
+        check_linear(out, x, w, z, None, dy, lc, None, 8)
+
+
 def test_outputs_stored_past_the_caches():
     """Outputs of more than 32 MB, and lists of tiles for few groups."""
     c = Lin(59, 4100, 4104, 72, BF, "relu")
