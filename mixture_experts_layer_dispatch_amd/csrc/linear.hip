@@ -710,6 +710,26 @@ static int64_t max_tiles(const LinTiles& t) {
     return ((int64_t)t.rows + groups * (t.tm - 1)) / t.tm;
 }
 
+// Whether a product of M rows (of E groups, E = 0: dense) and C output columns
+// takes 256 x 256 tiles rather than 128 x 128 ones.  A CU works on one of the
+// large tiles at a time and on two or three small ones, so each begun round of
+// 256 large tiles costs what two rounds of 256 small tiles do, full or not:
+//   4096 -> 1024, 8 groups of 768 rows   87 us, 128 x 128:  82
+//                            1024 rows   88                111
+//   1536 -> 768, 64 groups of 256 rows  106                 85  (two rounds, the second nearly empty)
+//                             512 rows  108                142
+//   1024 -> 1024, 16 groups of 384 rows  33                 29
+//                              512 rows  34                 41
+//   4096 x 4096, dense, 2560 rows        82                109
+// (groups of fewer than 128 rows leave half of a large tile empty: 64 of 96,
+// 4096 -> 1024: 150 us, 128 x 128: 136)
+static bool takes_256(int64_t M, int64_t E, int64_t C) {
+    auto tiles = [&](int64_t t) {                  // a group's last tile is half full on average
+        return (E > 0 ? M + E * (t / 2) : M + t - 1) / t * ((C + t - 1) / t);
+    };
+    return (tiles(256) + 255) / 256 * 512 < tiles(128);
+}
+
 // The tiles of a product with C output columns and R reduction indices: x W^T,
 // or (dx) dz W.
 LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
@@ -718,20 +738,20 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
     p.small = {nullptr, nullptr, E, M, 0, nullptr};
     p.big = p.small;
     if (E > 0) {
-        // (a group below 256 rows then takes a tile of its own: 128-row tiles
-        // for those groups, a launch more, gained nothing)
-        if (M >= 192LL * E) {
+        if (M >= 128LL * E && takes_256(M, E, C)) {
             p.big.tm = 256;
             return p;
         }
-        p.small.tm = M >= 128LL * E ? 128 : 64;
+        // (64 experts of 40 and 64 rows, 4096 -> 1024: 64-row tiles 99 and 148 us,
+        // 128-row tiles 105 and 130)
+        p.small.tm = M > 48LL * E ? 128 : 64;
         // few rows and few tiles: latency, which the streaming form splits over eight waves
         if (!dx && M <= 8LL * E && max_tiles(p.small) * ((C + 127) / 128) < 2048) {
             p.stream = true;
             p.small.tm = 16;
             return p;
         }
-        p.once = M <= 64LL * E && (dx ? C : R) % 64 == 0;
+        p.once = p.small.tm == 64 && (dx ? C : R) % 64 == 0;
         return p;
     }
     if (!dx && M <= 32) {
@@ -739,7 +759,7 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
         p.small.tm = M <= 16 ? 16 : 32;
         return p;
     }
-    if (((int64_t)(M + 255) / 256) * ((C + 255) / 256) >= 144) {
+    if (takes_256(M, 0, C)) {
         p.big.tm = 256;
         return p;
     }
@@ -860,13 +880,16 @@ static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
     return go(k_linear_dx<D, 64, false>, grid, 64 * lin_waves<64>(), a, st);
 }
 
-// dW: 256 x 256 tiles, the ring of 128 x 128 tiles, or the form of few rows.
+// dW: 256 x 256 tiles, the ring of 128 x 128 tiles, or the form of few rows,
+// whose several blocks to a CU hide the stores of tiles with few steps (64
+// experts, 1024 x 4096: of 384 rows 285 us, 256 x 256 tiles 320; of 512 347 and
+// 364; of 768 500 and 451).
 template <class D>
 static int dw_(const LinBwdArgs& a, hipStream_t st) {
     const int64_t groups = a.t.offsets ? a.t.E : 1, M = a.t.rows;
     const int64_t t256 = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
     const int64_t t128 = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-    if (M < 256 * groups) return go(k_linear_dw_few<D>, t128, 256, a, st);
+    if (M < 512 * groups) return go(k_linear_dw_few<D>, t128, 256, a, st);
     if (t256 >= 128) return go(k_linear_dw256<D>, t256, kT2Threads, a, st);
     return go(k_linear_dw<D>, t128, 64 * lin_waves<128>(), a, st);
 }
