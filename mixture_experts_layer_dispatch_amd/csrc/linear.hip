@@ -287,8 +287,8 @@ __global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_line
 }
 
 // ================================================================ split reductions
-// Too few tiles for the chip (dense): each tile's reduction is split into
-// ksplit ascending parts of whole 64-deep steps, a block each, whose fp32 sums
+// Too few tiles for the chip: each tile's reduction is split into ksplit
+// ascending parts of whole 64-deep steps, a block each, whose fp32 sums
 // k_linear_sum adds in order (128 x 4096 x 4096: 39 -> 17 us).  N: output columns,
 // K: reduction length, w: [N, K], or (BKS) [K, N].
 template <class D, bool BKS, int TM>
@@ -303,7 +303,8 @@ __global__ __launch_bounds__(64 * lin_waves<TM>(), 1) void k_linear_part(LinFwdA
     T1Acc<TM, lin_waves<TM>()> acc;
     {
         const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.x + k0, a.K, lo, hi);
-        const TileOperand<BKS, TN, 1, 64 * lin_waves<TM>()> ob(BKS ? a.w + (int64_t)k0 * a.N : a.w + k0, BKS ? a.N : a.K, n0, a.N);
+        const uint16_t* w = a.w + (int64_t)e * a.N * a.K;
+        const TileOperand<BKS, TN, 1, 64 * lin_waves<TM>()> ob(BKS ? w + (int64_t)k0 * a.N : w + k0, BKS ? a.N : a.K, n0, a.N);
         t1_mainloop<D, false, BKS, TM, 4, lin_waves<TM>()>(oa, ob, k1 - k0, acc, ring);
     }
     T1Pos<TM, lin_waves<TM>()> pos;
@@ -319,15 +320,17 @@ __global__ __launch_bounds__(64 * lin_waves<TM>(), 1) void k_linear_part(LinFwdA
     }
 }
 
-template <class D, int ACT>
+// Eight rows of a tile, 128 columns.
+template <class D, int ACT, int TM>
 __global__ __launch_bounds__(256) void k_linear_sum(LinFwdArgs a) {
-    const int n4 = a.N / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / n4;
-    if (row >= a.t.rows) return;
-    const int col = (int)(i - row * n4) * 4;
-    f32x4 v = *(const f32x4*)(a.part + row * a.N + col);
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, 1>(a.t, (a.N + 127) / 128, blockIdx.x / (TM / 8), e, lo, hi, nt, mt)) return;
+    const int row = lo + blockIdx.x % (TM / 8) * 8 + (threadIdx.x >> 5), col = nt * 128 + (threadIdx.x & 31) * 4;
+    if (row >= hi || col >= a.N) return;
+    f32x4 v = *(const f32x4*)(a.part + (int64_t)row * a.N + col);
+#pragma unroll 4
     for (int q = 1; q < a.ksplit; ++q) v += *(const f32x4*)(a.part + ((int64_t)q * a.t.rows + row) * a.N + col);
-    lin_out<D, ACT>(a, 0, (int)row, col, v);
+    lin_out<D, ACT>(a, e, row, col, v);
 }
 
 // ================================================================ few rows
@@ -704,7 +707,7 @@ static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
 // upper bound of the tiles of a set
 static int64_t max_tiles(const LinTiles& t) {
     if (t.tm == 0) return 0;
-    if (!t.offsets) return ((int64_t)t.rows + t.tm - 1) / t.tm;
+    if (t.E == 0) return ((int64_t)t.rows + t.tm - 1) / t.tm;
     // ceil(n / tm) <= (n + tm - 1) / tm for each of at most min(rows, E) groups with rows
     const int64_t groups = t.rows < t.E ? t.rows : t.E;
     return ((int64_t)t.rows + groups * (t.tm - 1)) / t.tm;
@@ -730,6 +733,29 @@ static bool takes_256(int64_t M, int64_t E, int64_t C) {
     return (tiles(256) + 255) / 256 * 512 < tiles(128);
 }
 
+// The parts of a reduction over R that its few tiles are best split into.  A
+// step of a lone block takes about 0.45 us; the sum's launch 6 us, and a part
+// of a million outputs, written and read, 1.5 us.
+//   128 x 4096 x 4096                    39 us, in parts 17
+//   8 groups of 16 rows, 4096 -> 1024    34              18
+//               64 rows                  31              22
+//   1024 x 1024 x 1024                   12              18
+//   8 groups of 128 rows, 2048 -> 2048   21              36
+static int parts(const LinTiles& t, int R, int C) {
+    const int64_t tiles = max_tiles(t) * ((C + 127) / 128);
+    const int steps = (R + kTK - 1) / kTK;
+    int best = 1;
+    float least = 0.45f * steps;
+    for (int64_t ks = 2; ks <= 16 && ks * tiles <= 256 && ks * 4 <= steps; ++ks) {
+        const float us = 0.45f * steps / ks + 6 + 1.5e-6f * ks * t.rows * C;
+        if (us < least) {
+            least = us;
+            best = (int)ks;
+        }
+    }
+    return best;
+}
+
 // The tiles of a product with C output columns and R reduction indices: x W^T,
 // or (dx) dz W.
 LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
@@ -746,12 +772,13 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
         // 128-row tiles 105 and 130)
         p.small.tm = M > 48LL * E ? 128 : 64;
         // few rows and few tiles: latency, which the streaming form splits over eight waves
-        if (!dx && M <= 8LL * E && max_tiles(p.small) * ((C + 127) / 128) < 2048) {
+        if (!dx && M <= 8LL * E && (M + 63LL) / 64 * ((C + 127) / 128) < 2048) {
             p.stream = true;
             p.small.tm = 16;
             return p;
         }
         p.once = p.small.tm == 64 && (dx ? C : R) % 64 == 0;
+        p.ksplit = parts(p.small, R, C);
         return p;
     }
     if (!dx && M <= 32) {
@@ -764,12 +791,7 @@ LinPlan linear_plan(int M, int E, int R, int C, bool dx) {
         return p;
     }
     p.small.tm = M <= 64 ? 64 : 128;
-    const int64_t tiles = max_tiles(p.small) * ((C + 127) / 128);
-    // (reductions below 24 steps: the second launch and the parts' traffic cost
-    // more than they save, 1024 x 1024 x 1024 18 instead of 12 us; 128 x 1000 x
-    // 1544 gains, 15.7 -> 11.3)
-    const int64_t ks = 256 / tiles < R / 256 ? 256 / tiles : R / 256;
-    p.ksplit = ks < 2 || R < 24 * kTK ? 1 : ks < 16 ? (int)ks : 16;
+    p.ksplit = parts(p.small, R, C);
     return p;
 }
 
@@ -806,10 +828,16 @@ static int go(K kern, int64_t grid, int threads, const A& a, hipStream_t st) {
     return ok();
 }
 
-template <class D>
-static int sum_parts(const LinFwdArgs& a, hipStream_t st) {
-    const int64_t grid = ((int64_t)a.t.rows * (a.N / 4) + 255) / 256;
-    return with_act(a.act, [&](auto A) { return go(k_linear_sum<D, A()>, grid, 256, a, st); });
+// the parts of a split product, or of dz W (BKS), and their sum
+template <class D, bool BKS>
+static int split_(const LinFwdArgs& a, hipStream_t st) {
+    const int64_t tiles = max_tiles(a.t) * ((a.N + 127) / 128);
+    if (a.t.tm == 128) {
+        if (go(k_linear_part<D, BKS, 128>, tiles * a.ksplit, 64 * lin_waves<128>(), a, st)) return -1;
+        return with_act(a.act, [&](auto A) { return go(k_linear_sum<D, A(), 128>, tiles * 16, 256, a, st); });
+    }
+    if (go(k_linear_part<D, BKS, 64>, tiles * a.ksplit, 64 * lin_waves<64>(), a, st)) return -1;
+    return with_act(a.act, [&](auto A) { return go(k_linear_sum<D, A(), 64>, tiles * 8, 256, a, st); });
 }
 
 template <class D>
@@ -817,11 +845,7 @@ static int fwd_(const LinPlan& p, LinFwdArgs a, hipStream_t st) {
     if (p.ksplit > 1) {
         a.t = p.small;
         a.ksplit = p.ksplit;
-        const int64_t grid = max_tiles(a.t) * ((a.N + 127) / 128) * a.ksplit;
-        if (a.t.tm == 128 ? go(k_linear_part<D, false, 128>, grid, 64 * lin_waves<128>(), a, st)
-                          : go(k_linear_part<D, false, 64>, grid, 64 * lin_waves<64>(), a, st))
-            return -1;
-        return sum_parts<D>(a, st);
+        return split_<D, false>(a, st);
     }
     return with_act(a.act, [&](auto A) {
         if (p.big.tm) {
@@ -863,11 +887,7 @@ template <class D>
 static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
     if (p.ksplit > 1) {                        // dz W as the sum of its parts
         LinFwdArgs f{p.small, a.dtype, LIN_NONE, a.K, a.N, a.dz, a.w, nullptr, nullptr, a.dx, nullptr, p.ksplit, a.sums};
-        const int64_t grid = max_tiles(f.t) * ((a.K + 127) / 128) * p.ksplit;
-        if (p.small.tm == 128 ? go(k_linear_part<D, true, 128>, grid, 64 * lin_waves<128>(), f, st)
-                              : go(k_linear_part<D, true, 64>, grid, 64 * lin_waves<64>(), f, st))
-            return -1;
-        return sum_parts<D>(f, st);
+        return split_<D, true>(f, st);
     }
     if (p.big.tm) {
         a.t = p.big;

@@ -201,6 +201,39 @@ def test_activations_at_the_ends_of_the_type(act, dtype):
         check_linear(out, x, w, z, None, dy, lc, None, 8)
 
 
+# groups whose products have enough 256 x 256 tiles: of x W^T, then of dz W and dW
+@pytest.mark.parametrize("counts", [[900, 0, 1100, 600], [1257, 1256, 255, 1, 513], [1300, 1, 64, 0, 1700]])
+@pytest.mark.parametrize("N,K", [(4104, 328), (328, 4104)])
+def test_large_groups_of_many_tiles(N, K, counts):
+    c = Lin(69, sum(counts) + 3, N, K, FP, "relu", counts)
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+
+
+@pytest.mark.parametrize("M", [512, 520, 575, 577, 639, 704])
+def test_large_dense_weight_gradient_of_more_rows(M):
+    c = Lin(79, M, 2056, 4104, FP if M % 2 else BF, "relu")
+    dw = torch.full_like(c.w, -77.0)
+    z = randn(gen(5), (M, 2056), c.lc.dtype)
+    B.moe_linear_backward(c.lc, c.x, None, z, c.dy, c.ws, dw=dw)
+    check_products({"dw": dw}, c.x, c.w, z, c.dy, c.lc, None, M)
+
+
+# few tiles and long reductions: several parts each, forward and (N long) for dx
+@pytest.mark.parametrize("counts", [[60, 0, 140], [0, 0, 1], [33, 5, 0, 64, 1], [200, 129, 300], [16] * 3])
+@pytest.mark.parametrize("N,K", [(264, 2056), (1800, 136), (1640, 1544)])
+def test_split_reductions_of_groups(N, K, counts):
+    c = Lin(89, sum(counts) + 5, N, K, BF if N == 264 else FP, "gelu", counts)
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+    again = c.outputs()
+    c.run(again)
+    for n in out:
+        assert torch.equal(out[n], again[n]), n
+
+
 def test_outputs_stored_past_the_caches():
     """Outputs of more than 32 MB, and lists of tiles for few groups."""
     c = Lin(59, 4100, 4104, 72, BF, "relu")
