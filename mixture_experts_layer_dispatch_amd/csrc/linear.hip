@@ -94,6 +94,17 @@ __device__ __forceinline__ int group_rows(const LinTiles& t, int e, int& lo, boo
 
 __device__ __forceinline__ int group_tiles(const LinTiles& t, int n) { return (n + t.tm - 1) / t.tm; }
 
+// Upper bound of the tiles of a set: ceil(n / tm) <= (n + tm - 1) / tm for each
+// of at most min(rows, E) groups with rows.  Grids and workspaces are made for
+// it, so numbers of tiles are cut to it: offsets that descend somewhere
+// (refused there) can make the other groups overlap.
+__host__ __device__ static inline int64_t max_tiles(const LinTiles& t) {
+    if (t.tm == 0) return 0;
+    if (t.E == 0) return ((int64_t)t.rows + t.tm - 1) / t.tm;
+    const int64_t groups = t.rows < t.E ? t.rows : t.E;
+    return (t.rows + groups * (t.tm - 1)) / t.tm;
+}
+
 // One block: for each of up to three sets of tiles, list[e] = the tiles of the
 // groups before e, list[E] their number.
 __global__ __launch_bounds__(1024) void k_linear_prefix(LinPrefix p) {
@@ -114,8 +125,9 @@ __global__ __launch_bounds__(1024) void k_linear_prefix(LinPrefix p) {
         int pre = incl - n;
         for (int v = 0; v < wv; ++v) pre += wsum[v];
         int32_t* out = const_cast<int32_t*>(p.t[q].list);
-        if (e < E) out[e] = pre;
-        if (e == E - 1) out[E] = pre + n;
+        const int most = (int)max_tiles(p.t[q]);
+        if (e < E) out[e] = min(pre, most);
+        if (e == E - 1) out[E] = min(pre + n, most);
         __syncthreads();
     }
 }
@@ -137,8 +149,9 @@ __device__ __forceinline__ WaveTiles wave_tiles(const LinTiles& t, bool tell) {
         const int o = __shfl_up(incl, off);
         if (lane >= off) incl += o;
     }
-    w.pre = incl - n;
-    w.total = __builtin_amdgcn_readlane(incl, 63);
+    const int most = (int)max_tiles(t);
+    w.pre = min(incl - n, most);
+    w.total = min(__builtin_amdgcn_readlane(incl, 63), most);
     return w;
 }
 
@@ -551,7 +564,7 @@ __device__ __forceinline__ void db_columns(const float* part, const LinTiles& t,
     } else if (t.offsets) {
         const WaveTiles w = wave_tiles(t, false);
         t0 = __builtin_amdgcn_readlane(w.pre, e);
-        t1 = t0 + group_tiles(t, __builtin_amdgcn_readlane(w.n, e));
+        t1 = min(t0 + group_tiles(t, __builtin_amdgcn_readlane(w.n, e)), w.total);
     }
     float s = 0.f;
     if (col < N)
@@ -703,15 +716,6 @@ __global__ __launch_bounds__(1024) void k_linear_db(LinBwdArgs a) {
 
 // ================================================================ launchers
 static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
-
-// upper bound of the tiles of a set
-static int64_t max_tiles(const LinTiles& t) {
-    if (t.tm == 0) return 0;
-    if (t.E == 0) return ((int64_t)t.rows + t.tm - 1) / t.tm;
-    // ceil(n / tm) <= (n + tm - 1) / tm for each of at most min(rows, E) groups with rows
-    const int64_t groups = t.rows < t.E ? t.rows : t.E;
-    return ((int64_t)t.rows + groups * (t.tm - 1)) / t.tm;
-}
 
 // Whether a product of M rows (of E groups, E = 0: dense) and C output columns
 // takes 256 x 256 tiles rather than 128 x 128 ones.  A CU works on one of the

@@ -321,6 +321,21 @@ def test_rows_and_experts_do_not_mix():
     assert (got["y"][100:] == -77).all() and (got["dx"][100:] == -77).all()
 
 
+@pytest.mark.parametrize("E", [7, 90])
+def test_overlapping_groups_stay_inside_the_workspace(E):
+    """Offsets that go back and forth: more tiles than any valid offsets have."""
+    M, N, K = 200, 136, 72
+    c = Lin(24, M, N, K, BF, "silu", [M] + [0] * (E - 1))
+    c.off = torch.tensor([0, M] * ((E + 1) // 2) + [0] * ((E + 1) % 2), dtype=torch.int32, device="cuda")
+    need = c.ws.numel()
+    buf = torch.full((need + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    buf[:256].zero_()
+    c.ws = buf[:need]
+    c.run(c.outputs())
+    assert B.moe_check_device_error(c.ws) != 0
+    assert (buf[need:] == 0x5A).all()
+
+
 def test_ragged_edges_do_not_read_their_neighbours():
     """K and N that end inside a tile, with NaN right behind every operand."""
     M, N, K = 70, 72, 200
