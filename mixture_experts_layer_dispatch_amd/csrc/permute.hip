@@ -27,6 +27,13 @@
 
 namespace moe {
 
+// Launches of more than 2^32 threads take a second grid dimension.
+constexpr int64_t kGridX = 1 << 22;
+static dim3 rows_grid(int64_t blocks) {
+    return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Lane j < k of the wave holds the row of the token's slot j (-1: bad).
 __device__ __forceinline__ int slot_row(const int32_t* __restrict__ row_of_slot, int t, int k, int S, int lane,
                                         int32_t* err) {
@@ -72,9 +79,9 @@ template <bool NT>
 __global__ __launch_bounds__(256) void k_permute(const uint4* __restrict__ x, int C, int nseg,
                                                  const int32_t* __restrict__ row_of_slot, int T, int k, int S,
                                                  uint4* __restrict__ xs, int32_t* __restrict__ err) {
-    const int64_t L = (int64_t)blockIdx.x * 4 + wave_id();
+    const int64_t L = block_number() * 4 + wave_id();
+    if (L >= (int64_t)T * nseg) return;
     const int t = (int)(L / nseg);
-    if (t >= T) return;
     const int lane = lane_id(), c = (int)(L % nseg) * 64 + lane;
     const int myrow = slot_row(row_of_slot, t, k, S, lane, err);
     if (c >= C) return;
@@ -94,9 +101,9 @@ __global__ __launch_bounds__(256) void k_unpermute(const uint4* __restrict__ o, 
                                                    const float* __restrict__ w, int T, int k, int S,
                                                    const uint4* residual, uint4* y,
                                                    int32_t* __restrict__ err) {
-    const int64_t L = (int64_t)blockIdx.x * 4 + wave_id();
+    const int64_t L = block_number() * 4 + wave_id();
+    if (L >= (int64_t)T * nseg) return;
     const int t = (int)(L / nseg);
-    if (t >= T) return;
     const int lane = lane_id(), c = (int)(L % nseg) * 64 + lane;
     const int myrow = slot_row(row_of_slot, t, k, S, lane, err);
     float myw = 1.f;
@@ -178,8 +185,9 @@ __global__ __launch_bounds__(256) void k_unpermute_bwd(const uint4* __restrict__
     __shared__ float s_dl[TPB][kMaxTopK];
     __shared__ int32_t s_idx[TPB][kMaxTopK];
     const int wv = wave_id(), sub = wv % WPT, tt = wv / WPT, lane = lane_id();
-    const int t = blockIdx.x * TPB + tt;
-    const bool live = t < T;
+    const int64_t t64 = block_number() * TPB + tt;
+    const bool live = t64 < T;
+    const int t = live ? (int)t64 : 0;
     const int myrow = live ? slot_row(row_of_slot, t, k, S, lane, err) : -1;
     const float myw = live && lane < k ? w[(int64_t)t * k + lane] : 0.f;
     float mydw = 0.f;                                     // lane j: dw of slot j
@@ -256,7 +264,7 @@ template <class D, bool WEIGHT>
 static int unpermute_(const RowsArgs& a, const void* o, const float* w, const void* residual, void* y,
                       hipStream_t st) {
     const int C = a.H / D::PER16, nseg = (C + 63) / 64;
-    const unsigned grid = (unsigned)(((int64_t)a.T * nseg + 3) / 4);
+    const dim3 grid = rows_grid(((int64_t)a.T * nseg + 3) / 4);
     auto go = [&](auto kern) {
         kern<<<grid, 256, 0, st>>>((const uint4*)o, C, nseg, a.row_of_slot, w, a.T, a.k, a.S,
                                    (const uint4*)residual, (uint4*)y, a.err);
@@ -277,7 +285,7 @@ static int unpermute_any(const RowsArgs& a, const void* o, const float* w, const
 int launch_permute(const RowsArgs& a, const void* x, void* xs, hipStream_t st) {
     ProfScope prof_(st, "permute");
     const int C = a.H * (a.dtype == 2 ? 4 : 2) / 16, nseg = (C + 63) / 64;
-    const unsigned grid = (unsigned)(((int64_t)a.T * nseg + 3) / 4);
+    const dim3 grid = rows_grid(((int64_t)a.T * nseg + 3) / 4);
     auto go = [&](auto kern) {
         kern<<<grid, 256, 0, st>>>((const uint4*)x, C, nseg, a.row_of_slot, a.T, a.k, a.S, (uint4*)xs, a.err);
         return hipGetLastError() == hipSuccess ? 0 : -1;
@@ -301,7 +309,7 @@ static int unpermute_bwd_(const RowsArgs& a, const void* o, const void* dy, cons
                           int E, void* d_o, float* dw, float* d_logits, hipStream_t st) {
     const int C = a.H / D::PER16, nseg = (C + 63) / 64;
     auto go = [&](auto kern, int tpb) {
-        kern<<<(a.T + tpb - 1) / tpb, 256, 0, st>>>((const uint4*)o, (const uint4*)dy, C, nseg, a.row_of_slot, idx,
+        kern<<<rows_grid(((int64_t)a.T + tpb - 1) / tpb), 256, 0, st>>>((const uint4*)o, (const uint4*)dy, C, nseg, a.row_of_slot, idx,
                                                     w, a.T, a.k, E, a.S, (uint4*)d_o, dw, d_logits, a.err);
     };
     const bool nt = (int64_t)a.S * C * 16 > kCacheBytes;

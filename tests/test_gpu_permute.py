@@ -201,3 +201,42 @@ def test_on_another_stream_and_replayed_from_a_graph():
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(out[n], want[n]), n
+
+
+def test_more_tokens_than_one_grid_dimension_takes():
+    """k = 1, 2^24 + 5 tokens of 640: more than 2^32 threads in every launch."""
+    T, H, step = (1 << 24) + 5, 640, 1 << 21
+    cfg, ws = B.Config(T=T, H=H, I=128, E=4, k=1), B.alloc_error_word()
+    row = (T - 1 - torch.arange(T, device="cuda")).to(torch.int32)          # row(t) = T - 1 - t
+    sched = {"row_of_slot": row, "topk_w": (torch.arange(T, device="cuda") % 7 - 3).float().view(T, 1)}
+    marks = (torch.arange(T, device="cuda") % 251).to(BF).view(T, 1)        # exact in bf16, also times -3 .. 3
+    col = torch.arange(H, device="cuda") % 2 == 0
+    a, b = torch.empty(T, H, dtype=BF, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda")
+    for i in range(0, T, step):
+        a[i:i + step] = torch.where(col, marks[i:i + step], 1)
+
+    def check(out, want):
+        for i in range(0, T, step):
+            assert torch.equal(out[i:i + step], want(torch.arange(i, min(i + step, T), device="cuda"))), i
+
+    def rows(t):
+        return torch.where(col, marks[t], 1).to(BF)
+
+    def weighted(t):
+        return (rows(t).float() * sched["topk_w"][t]).to(BF)
+
+    B.moe_permute_forward(cfg, sched, a, b, ws)
+    check(b, lambda r: rows(T - 1 - r))
+    a.fill_(-77)
+    B.moe_permute_backward(cfg, sched, b, a, ws)
+    check(a, rows)
+    a.fill_(-77)
+    B.moe_unpermute_forward(cfg, sched, b, a, ws)
+    check(a, weighted)
+    for i in range(0, T, step):
+        a[i:i + step] = 1                                                    # dy: the weights' gradient counts the row
+    c, dw = torch.empty_like(a), torch.empty(T, 1, device="cuda")
+    B.moe_unpermute_backward(cfg, sched, b, a, c, dw, ws)
+    check(c, lambda r: sched["topk_w"][T - 1 - r].to(BF).expand(-1, H))
+    assert torch.equal(dw, marks.float() * 320 + 320)
+    assert B.moe_check_device_error(ws) == 0
