@@ -155,6 +155,31 @@ __device__ __forceinline__ WaveTiles wave_tiles(const LinTiles& t, bool tell) {
     return w;
 }
 
+// 256 x 256 tiles behind the last whole round of 256 that are computed as four
+// 128 x 128 tiles each: up to 64 make one round of those, up to 128 two, which
+// take 0.4 and 0.8 of the time of a round of the large tiles (4096 -> 4096, 5120
+// rows: 320 tiles, 178 -> 138 us; 5632 rows, 352 tiles, 179 -> 168; 6144, 384,
+// 181 -> 174).
+constexpr int kRest256 = 128;
+
+// The tile L of block b of `total`; with `quarter`, the quarter of it for a tile
+// that is computed in quarters, else -1.
+__device__ __forceinline__ bool rest_tile(int total, int b, int* quarter, int& L) {
+    const int rest = total & 255, whole = total - rest;
+    const bool split = quarter && rest <= kRest256;
+    if (split && b >= whole) {
+        if (b >= whole + 4 * rest) return false;
+        const int s = xcd_remap(b - whole, 4 * rest);
+        L = whole + (s >> 2);
+        *quarter = s & 3;
+        return true;
+    }
+    if (b >= total) return false;
+    L = xcd_remap(b, split ? whole : total);
+    if (quarter) *quarter = -1;
+    return true;
+}
+
 // Block b's tile: expert e, rows lo .. hi - 1, column tile nt, and its number
 // mt among the row tiles.  An XCD's consecutive tiles are BAND row tiles by the
 // column tiles one after the other: with BAND 4, 4 by 8 for its 32 CUs, so that
@@ -162,7 +187,7 @@ __device__ __forceinline__ WaveTiles wave_tiles(const LinTiles& t, bool tell) {
 // tiles, 1 by 32: 45 -> 38 us; dW's 256 x 256 tiles 386 -> 377).
 template <int TM, int BAND>
 __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int& e, int& lo, int& hi, int& nt,
-                                         int& mt) {
+                                         int& mt, int* quarter = nullptr) {
     WaveTiles w;
     int ntiles;
     if (!t.offsets) ntiles = (t.rows + TM - 1) / TM;
@@ -171,8 +196,8 @@ __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int&
         w = wave_tiles(t, b == 0);
         ntiles = w.total;
     }
-    if (b >= ntiles * nNt) return false;
-    const int L = xcd_remap(b, ntiles * nNt);
+    int L;
+    if (!rest_tile(ntiles * nNt, b, quarter, L)) return false;
     // (small groups share weights within a group only: no bands)
     const int B = TM < 256 && t.offsets ? 1 : BAND;
     const int band = L / (B * nNt), r = L - band * B * nNt, rows = min(B, ntiles - B * band);
@@ -214,10 +239,11 @@ __device__ __forceinline__ bool lin_tile(const LinTiles& t, int nNt, int b, int&
 // n; tiles in bands of BAND row tiles, as above.
 template <int BAND>
 __device__ __forceinline__ bool lin_wtile(const LinTiles& t, int nMt, int nNt, int b, int& e, int& mt, int& nt,
-                                          int& lo, int& n) {
+                                          int& lo, int& n, int* quarter = nullptr) {
     const int per = nMt * nNt, total = (t.offsets ? t.E : 1) * per;
-    if (b >= total) return false;
-    const int L = xcd_remap(b, total), rem = L % per;
+    int L;
+    if (!rest_tile(total, b, quarter, L)) return false;
+    const int rem = L % per;
     e = L / per;
     const int band = rem / (BAND * nNt), r = rem - band * BAND * nNt, rows = min(BAND, nMt - BAND * band);
     nt = r / rows;
@@ -271,12 +297,8 @@ __device__ __forceinline__ void lin_out(const LinFwdArgs& a, int e, int row, int
 // for that: pieces of a line that two steps read come twice (K = 4072: 1122
 // non-temporally, 916 plainly).
 template <class D, int ACT, int TM, bool ONCE>
-__global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
+__device__ __forceinline__ void fwd_tile(const LinFwdArgs& a, int e, int lo, int hi, int n0, const T1Ring& ring) {
     constexpr int TN = 128;
-    int e, lo, hi, nt, mt;
-    if (!lin_tile<TM, TM == 128 ? 4 : 1>(a.t, (a.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
-    const int n0 = nt * TN;
-    T1_RING(ring, TM, lin_stages<TM>());
     T1Acc<TM, lin_waves<TM>()> acc;
     {
         const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.x, a.K, lo, hi);
@@ -293,10 +315,19 @@ __global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_line
         }
     }
     const bool nt_out = many((int64_t)a.t.rows * a.N);
-    if (a.z) t1_put<TM, lin_waves<TM>()>(ring, nt_out, a.z, lo, hi, n0, a.N, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    if (a.z)
+        t1_put<TM, lin_waves<TM>()>(ring, nt_out, a.z, lo, hi, n0, a.N,
+                                    [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
     t1_put<TM, lin_waves<TM>()>(ring, nt_out, a.y, lo, hi, n0, a.N, [&](int mb, int nb) {
         return pack4<D>(act_residual<D, ACT>(a, lo + pos.m(mb), hi, n0 + pos.n(nb), acc[mb][nb]));
     });
+}
+template <class D, int ACT, int TM, bool ONCE>
+__global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_fwd(LinFwdArgs a) {
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, TM == 128 ? 4 : 1>(a.t, (a.N + 127) / 128, blockIdx.x, e, lo, hi, nt, mt)) return;
+    T1_RING(ring, TM, lin_stages<TM>());
+    fwd_tile<D, ACT, TM, ONCE>(a, e, lo, hi, nt * 128, ring);
 }
 
 // ================================================================ split reductions
@@ -317,7 +348,8 @@ __global__ __launch_bounds__(64 * lin_waves<TM>(), 1) void k_linear_part(LinFwdA
     {
         const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.x + k0, a.K, lo, hi);
         const uint16_t* w = a.w + (int64_t)e * a.N * a.K;
-        const TileOperand<BKS, TN, 1, 64 * lin_waves<TM>()> ob(BKS ? w + (int64_t)k0 * a.N : w + k0, BKS ? a.N : a.K, n0, a.N);
+        const TileOperand<BKS, TN, 1, 64 * lin_waves<TM>()> ob(BKS ? w + (int64_t)k0 * a.N : w + k0,
+                                                               BKS ? a.N : a.K, n0, a.N);
         t1_mainloop<D, false, BKS, TM, 4, lin_waves<TM>()>(oa, ob, k1 - k0, acc, ring);
     }
     T1Pos<TM, lin_waves<TM>()> pos;
@@ -440,24 +472,28 @@ __global__ __launch_bounds__(64 * W) void k_linear_stream(LinFwdArgs a) {
 // ================================================================ backward, small tiles
 // dx = dz W: W read with its row (the reduction index n) as the memory row
 template <class D, int TM, bool ONCE>
-__device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
+__device__ __forceinline__ void dx_tile(const LinBwdArgs& a, int e, int lo, int hi, int n0, const T1Ring& ring) {
     constexpr int TN = 128;
-    int e, lo, hi, nt, mt;
-    if (!lin_tile<TM, TM == 128 ? 4 : 1>(a.t, (a.K + TN - 1) / TN, block, e, lo, hi, nt, mt)) return;
-    const int n0 = nt * TN;
     T1Acc<TM, lin_waves<TM>()> acc;
     {
         const TileOperand<false, TM, 1, 64 * lin_waves<TM>()> oa(a.dz, a.N, lo, hi);
         const TileOperand<true, TN, 1, 64 * lin_waves<TM>(), ONCE> ob(a.w + (int64_t)e * a.N * a.K, a.K, n0, a.K);
         t1_mainloop<D, false, true, TM, lin_stages<TM>(), lin_waves<TM>(), ONCE>(oa, ob, a.N, acc, ring);
     }
-    t1_put<TM, lin_waves<TM>()>(ring, many((int64_t)a.t.rows * a.K), a.dx, lo, hi, n0, a.K, [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+    t1_put<TM, lin_waves<TM>()>(ring, many((int64_t)a.t.rows * a.K), a.dx, lo, hi, n0, a.K,
+                                [&](int mb, int nb) { return pack4<D>(acc[mb][nb]); });
+}
+template <class D, int TM, bool ONCE>
+__device__ __forceinline__ void dx_block(const LinBwdArgs& a, int block, const T1Ring& ring) {
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, TM == 128 ? 4 : 1>(a.t, (a.K + 127) / 128, block, e, lo, hi, nt, mt)) return;
+    dx_tile<D, TM, ONCE>(a, e, lo, hi, nt * 128, ring);
 }
 
 template <class D, int TM, bool ONCE>
 __global__ __launch_bounds__(64 * lin_waves<TM>(), TM == 64 ? 2 : 1) void k_linear_dx(LinBwdArgs a) {
     T1_RING(ring, TM, lin_stages<TM>());
-    dx_tile<D, TM, ONCE>(a, blockIdx.x, ring);
+    dx_block<D, TM, ONCE>(a, blockIdx.x, ring);
 }
 
 __device__ __forceinline__ int64_t dw_elements(const LinBwdArgs& a) {
@@ -466,11 +502,8 @@ __device__ __forceinline__ int64_t dw_elements(const LinBwdArgs& a) {
 
 // dW = dz^T x over a group's rows: both operands with the row as the memory row
 template <class D>
-__device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1Ring& ring) {
+__device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int e, int lo, int n, int m0, int n0, const T1Ring& ring) {
     constexpr int TM = 128, TN = 128;
-    int e, mt, nt, lo, n;
-    if (!lin_wtile<4>(a.t, (a.N + TM - 1) / TM, (a.K + TN - 1) / TN, block, e, mt, nt, lo, n)) return;
-    const int m0 = mt * TM, n0 = nt * TN;
     T1Acc<TM, lin_waves<TM>()> acc;
     {
         const TileOperand<true, TM, 1, 64 * lin_waves<TM>()> oa(a.dz + (int64_t)lo * a.N, a.N, m0, a.N);
@@ -482,9 +515,16 @@ __device__ __forceinline__ void dw_tile(const LinBwdArgs& a, int block, const T1
 }
 
 template <class D>
+__device__ __forceinline__ void dw_block(const LinBwdArgs& a, int block, const T1Ring& ring) {
+    int e, mt, nt, lo, n;
+    if (!lin_wtile<4>(a.t, (a.N + 127) / 128, (a.K + 127) / 128, block, e, mt, nt, lo, n)) return;
+    dw_tile<D>(a, e, lo, n, mt * 128, nt * 128, ring);
+}
+
+template <class D>
 __global__ __launch_bounds__(64 * lin_waves<128>(), 1) void k_linear_dw(LinBwdArgs a) {
     T1_RING(ring, 128, 4);
-    dw_tile<D>(a, blockIdx.x, ring);
+    dw_block<D>(a, blockIdx.x, ring);
 }
 
 // Groups of few rows: dW's write is all the work.  Blocks of 32 KB of LDS,
@@ -534,9 +574,7 @@ __global__ __launch_bounds__(256, 4) void k_linear_dw_few(LinBwdArgs a) {
 #pragma unroll
         for (int nb = 0; nb < TN / 32; ++nb) {
             const int r = pos.m(mb), c = pos.n(nb);
-            const f32x4 v = acc[mb][nb];
-            *(uint2*)(sm + r * TN + (((c >> 3) ^ (r & 15)) << 3) + (c & 7)) =
-                make_uint2(D::pack2(v[0], v[1]), D::pack2(v[2], v[3]));
+            *(uint2*)(sm + r * TN + (((c >> 3) ^ (r & 15)) << 3) + (c & 7)) = pack4<D>(acc[mb][nb]);
         }
     __syncthreads();
     const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
@@ -583,20 +621,29 @@ __global__ __launch_bounds__(64 * lin_waves<128>(), 1) void k_linear_bwd(LinBwdA
     T1_RING(ring, 128, 4);
     int b = blockIdx.x;
     if (b < a.ndw) {
-        dw_tile<D>(a, b, ring);
+        dw_block<D>(a, b, ring);
         return;
     }
     b -= a.ndw;
-    if (b < a.ndx) dx_tile<D, 128, false>(a, b, ring);
+    if (b < a.ndx) dx_block<D, 128, false>(a, b, ring);
     else db_columns<D>(a.part, a.rows32, a.N, b - a.ndx, lin_waves<128>(), (float*)ring.a0, a.db);
 }
 
 // ================================================================ 256 x 256 tiles
+__device__ __forceinline__ T1Ring t1_ring(const T2Lds& l) {
+    return T1Ring{l.h[0], l.h[1], l.h[2], l.h[3], l.h[4], l.h[5], l.h[6], l.h[7]};
+}
+
 template <class D, int ACT>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
-    int e, lo, hi, nt, mt;
-    if (!lin_tile<256, 4>(a.t, (a.N + 255) / 256, blockIdx.x, e, lo, hi, nt, mt)) return;
+    int e, lo, hi, nt, mt, q;
+    if (!lin_tile<256, 4>(a.t, (a.N + 255) / 256, blockIdx.x, e, lo, hi, nt, mt, &q)) return;
     T2_LDS(lds);
+    if (q >= 0) {
+        const int r0 = lo + 128 * (q >> 1), n0 = nt * 256 + 128 * (q & 1);
+        if (r0 < hi && n0 < a.N) fwd_tile<D, ACT, 128, false>(a, e, r0, min(r0 + 128, hi), n0, t1_ring(lds));
+        return;
+    }
     T2Acc acc;
     {
         const T2Operand<false> oa(a.x, a.K, lo, hi);
@@ -638,8 +685,13 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
         db_columns<D>(a.part, a.rows32, a.N, blockIdx.x, kT2Threads / 64, (float*)lds.h[0], a.db);
         return;
     }
-    int e, lo, hi, nt, mt;
-    if (!lin_tile<256, 4>(a.t, (a.K + 255) / 256, blockIdx.x - a.ndb, e, lo, hi, nt, mt)) return;
+    int e, lo, hi, nt, mt, q;
+    if (!lin_tile<256, 4>(a.t, (a.K + 255) / 256, blockIdx.x - a.ndb, e, lo, hi, nt, mt, &q)) return;
+    if (q >= 0) {
+        const int r0 = lo + 128 * (q >> 1), n0 = nt * 256 + 128 * (q & 1);
+        if (r0 < hi && n0 < a.K) dx_tile<D, 128, false>(a, e, r0, min(r0 + 128, hi), n0, t1_ring(lds));
+        return;
+    }
     T2Acc acc;
     {
         const T2Operand<false> oa(a.dz, a.N, lo, hi);
@@ -651,9 +703,14 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
 
 template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
-    int e, mt, nt, lo, n;
-    if (!lin_wtile<4>(a.t, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n)) return;
+    int e, mt, nt, lo, n, q;
+    if (!lin_wtile<4>(a.t, (a.N + 255) / 256, (a.K + 255) / 256, blockIdx.x, e, mt, nt, lo, n, &q)) return;
     T2_LDS(lds);
+    if (q >= 0) {
+        const int m0 = mt * 256 + 128 * (q >> 1), n0 = nt * 256 + 128 * (q & 1);
+        if (m0 < a.N && n0 < a.K) dw_tile<D>(a, e, lo, n, m0, n0, t1_ring(lds));
+        return;
+    }
     T2Acc acc;
     {
         const T2Operand<true> oa(a.dz + (int64_t)lo * a.N, a.N, mt * 256, a.N);
@@ -667,7 +724,7 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
 // A block takes a tile of TR rows by 512 columns (8 per lane, rows round
 // robin over four waves): dz = dy act'(z) (rounded once, to the type the
 // products read), and the column sums of the unrounded dz, in fp32, one
-// partial row per tile.
+// partial row per tile.  Bound by HBM: 20480 x 1024 bf16, 126 MB in 27 us.
 template <class D, int ACT, int TR>
 __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
     __shared__ float sums[3][64][8];
@@ -717,13 +774,18 @@ __global__ __launch_bounds__(1024) void k_linear_db(LinBwdArgs a) {
 // ================================================================ launchers
 static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
 
+// blocks of a product with C output columns in 256 x 256 tiles, the last ones in quarters
+static int64_t blocks256(const LinTiles& t, int C) {
+    return max_tiles(t) * ((C + 255) / 256) + 3 * kRest256;
+}
+
 // Whether a product of M rows (of E groups, E = 0: dense) and C output columns
 // takes 256 x 256 tiles rather than 128 x 128 ones.  A CU works on one of the
-// large tiles at a time and on two or three small ones, so each begun round of
-// 256 large tiles costs what two rounds of 256 small tiles do, full or not:
+// large tiles at a time; a round of 256 of them takes what two rounds of 256
+// small tiles do, full or not, and 64 left over go as one round of small ones:
 //   4096 -> 1024, 8 groups of 768 rows   87 us, 128 x 128:  82
 //                            1024 rows   88                111
-//   1536 -> 768, 64 groups of 256 rows  106                 85  (two rounds, the second nearly empty)
+//   1536 -> 768, 64 groups of 128 rows   56                 65
 //                             512 rows  108                142
 //   1024 -> 1024, 16 groups of 384 rows  33                 29
 //                              512 rows  34                 41
@@ -734,7 +796,8 @@ static bool takes_256(int64_t M, int64_t E, int64_t C) {
     auto tiles = [&](int64_t t) {                  // a group's last tile is half full on average
         return (E > 0 ? M + E * (t / 2) : M + t - 1) / t * ((C + t - 1) / t);
     };
-    return (tiles(256) + 255) / 256 * 512 < tiles(128);
+    const int64_t whole = tiles(256) / 256, rest = tiles(256) % 256;
+    return whole * 512 + (rest == 0 ? 0 : rest <= 64 ? 256 : 512) < tiles(128);
 }
 
 // The parts of a reduction over R that its few tiles are best split into.  A
@@ -854,13 +917,14 @@ static int fwd_(const LinPlan& p, LinFwdArgs a, hipStream_t st) {
     return with_act(a.act, [&](auto A) {
         if (p.big.tm) {
             a.t = p.big;
-            return go(k_linear_fwd256<D, A()>, max_tiles(a.t) * ((a.N + 255) / 256), kT2Threads, a, st);
+            return go(k_linear_fwd256<D, A()>, blocks256(a.t, a.N), kT2Threads, a, st);
         }
         a.t = p.small;
         const int64_t tiles = max_tiles(a.t);
         if (p.stream) {
             const int n16 = (a.N + 15) / 16;
-            if (a.t.tm == 16 && a.t.offsets) return go(k_linear_stream<D, A(), 1, 2, 4, 8>, tiles * ((n16 + 1) / 2), 512, a, st);
+            if (a.t.tm == 16 && a.t.offsets)
+                return go(k_linear_stream<D, A(), 1, 2, 4, 8>, tiles * ((n16 + 1) / 2), 512, a, st);
             if (a.t.tm == 16) return go(k_linear_stream<D, A(), 1, 1, 4, 8>, tiles * n16, 512, a, st);
             return go(k_linear_stream<D, A(), 2, 1, 4, 8>, tiles * n16, 512, a, st);
         }
@@ -895,7 +959,7 @@ static int dx_(const LinPlan& p, LinBwdArgs a, hipStream_t st) {
     }
     if (p.big.tm) {
         a.t = p.big;
-        return go(k_linear_dx256<D>, a.ndb + max_tiles(a.t) * ((a.K + 255) / 256), kT2Threads, a, st);
+        return go(k_linear_dx256<D>, a.ndb + blocks256(a.t, a.K), kT2Threads, a, st);
     }
     a.t = p.small;
     const int64_t grid = max_tiles(a.t) * ((a.K + 127) / 128);
@@ -914,7 +978,7 @@ static int dw_(const LinBwdArgs& a, hipStream_t st) {
     const int64_t t256 = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
     const int64_t t128 = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
     if (M < 512 * groups) return go(k_linear_dw_few<D>, t128, 256, a, st);
-    if (t256 >= 128) return go(k_linear_dw256<D>, t256, kT2Threads, a, st);
+    if (t256 >= 128) return go(k_linear_dw256<D>, t256 + 3 * kRest256, kT2Threads, a, st);
     return go(k_linear_dw<D>, t128, 64 * lin_waves<128>(), a, st);
 }
 

@@ -309,8 +309,9 @@ static int unpermute_bwd_(const RowsArgs& a, const void* o, const void* dy, cons
                           int E, void* d_o, float* dw, float* d_logits, hipStream_t st) {
     const int C = a.H / D::PER16, nseg = (C + 63) / 64;
     auto go = [&](auto kern, int tpb) {
-        kern<<<rows_grid(((int64_t)a.T + tpb - 1) / tpb), 256, 0, st>>>((const uint4*)o, (const uint4*)dy, C, nseg, a.row_of_slot, idx,
-                                                    w, a.T, a.k, E, a.S, (uint4*)d_o, dw, d_logits, a.err);
+        kern<<<rows_grid(((int64_t)a.T + tpb - 1) / tpb), 256, 0, st>>>(
+            (const uint4*)o, (const uint4*)dy, C, nseg, a.row_of_slot, idx, w, a.T, a.k, E, a.S, (uint4*)d_o, dw,
+            d_logits, a.err);
     };
     const bool nt = (int64_t)a.S * C * 16 > kCacheBytes;
     auto pick = [&](auto NT) {

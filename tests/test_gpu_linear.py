@@ -220,6 +220,26 @@ def test_large_dense_weight_gradient_of_more_rows(M):
     check_products({"dw": dw}, c.x, c.w, z, c.dy, c.lc, None, M)
 
 
+# one round of 256 x 256 tiles and some left over, of x W^T, then of dz W; of dW
+@pytest.mark.parametrize("M,counts", [(4200, None), (4700, None), (3700, [1700, 1, 64, 0, 1900]),
+                                      (4500, [300, 2000, 130, 2000, 5, 60])])
+@pytest.mark.parametrize("N,K,dtype", [(4232, 136, BF), (136, 4232, FP)])
+def test_tiles_behind_the_last_whole_round(M, counts, N, K, dtype):
+    c = Lin(99, M, N, K, dtype, "gelu", counts)
+    out = c.outputs()
+    c.run(out)
+    c.check(out)
+
+
+@pytest.mark.parametrize("M,counts", [(600, None), (1300, [513, 787])])
+def test_weight_tiles_behind_the_last_whole_round(M, counts):
+    c = Lin(109, M, 2184, 8200 if counts is None else 4232, BF, "silu", counts)
+    dw = torch.full_like(c.w, -77.0)
+    z = randn(gen(5), (M, 2184), c.lc.dtype)
+    B.moe_linear_backward(c.lc, c.x, None, z, c.dy, c.ws, dw=dw, offsets=c.off)
+    check_products({"dw": dw}, c.x, c.w, z, c.dy, c.lc, c.off_list, M)
+
+
 # few tiles and long reductions: several parts each, forward and (N long) for dx
 @pytest.mark.parametrize("counts", [[60, 0, 140], [0, 0, 1], [33, 5, 0, 64, 1], [200, 129, 300], [16] * 3])
 @pytest.mark.parametrize("N,K", [(264, 2056), (1800, 136), (1640, 1544)])
