@@ -403,7 +403,7 @@ struct LinPlan {
     LinTiles small, big;
     bool stream;              // small: k_linear_stream, 16 or 32 rows
     bool once;                // small: each weight tile feeds one row tile
-    int ksplit;               // parts the reduction is split into (dense)
+    int ksplit;               // parts the reduction is split into (small)
 };
 
 struct LinPrefix {

@@ -675,7 +675,8 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_fwd256(LinFwdArgs a) {
 template <class D>
 __device__ __forceinline__ void t2_store(const T2Lds& lds, bool nt, uint16_t* out, int r0, int r1, int c0, int ncol,
                                          const T2Acc& acc) {
-    t2_put(lds, nt, out, r0, r1, c0, ncol, [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
+    t2_put(lds, nt, out, r0, r1, c0, ncol,
+           [&](int ha, int hb, int mb, int nb) { return pack4<D>(acc[ha][hb][mb][nb]); });
 }
 
 template <class D>

@@ -30,7 +30,8 @@ namespace moe {
 // Launches of more than 2^32 threads take a second grid dimension.
 constexpr int64_t kGridX = 1 << 22;
 static dim3 rows_grid(int64_t blocks) {
-    return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+    if (blocks <= kGridX) return dim3((unsigned)blocks);
+    return dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
 }
 __device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 

@@ -19,6 +19,17 @@
 // halves (80 KB) ahead of the reads and are never drained in the loop: each
 // memory part waits only until the half the next phase reads has landed
 // (vmcnt 10, two copies per thread and half).
+//
+// 16384 x 4096 x 4096, bf16: x W^T 417 us (1320 TFLOP/s; with gelu 433), dz W
+// 389 (1413), dz^T x 383 (1436); the library's products there: 436, 501 and 915.
+// MFMA busy 69 percent of the cycles, at 1.94 GHz, what power leaves of the
+// clock; 2 percent of the LDS cycles are bank conflicts.  256 x 256 rather than
+// 128 x 128 halves the bytes that each product reads from LDS and L2; the
+// accumulators then take half of a wave's registers, hence eight waves, one
+// block to a CU and the alternating groups instead of several blocks.
+//
+// Below it, the same operands and layouts for 64 or 128 x 128 tiles over a ring
+// of three or four stages (T1).
 #pragma once
 
 #include "dtype.h"
