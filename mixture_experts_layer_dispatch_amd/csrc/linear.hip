@@ -775,9 +775,15 @@ __global__ __launch_bounds__(1024) void k_linear_db(LinBwdArgs a) {
 // ================================================================ launchers
 static int ok() { return hipGetLastError() == hipSuccess ? 0 : -1; }
 
-// blocks of a product with C output columns in 256 x 256 tiles, the last ones in quarters
+// blocks for `tiles` 256 x 256 tiles, or for at most as many (the device counts
+// groups' tiles), the ones behind the last whole round in quarters
+static int64_t blocks256(int64_t tiles, bool exact) {
+    const int64_t rest = tiles % 256;
+    return tiles + 3 * (!exact ? kRest256 : rest <= kRest256 ? rest : 0);
+}
+
 static int64_t blocks256(const LinTiles& t, int C) {
-    return max_tiles(t) * ((C + 255) / 256) + 3 * kRest256;
+    return blocks256(max_tiles(t) * ((C + 255) / 256), t.E == 0);
 }
 
 // Whether a product of M rows (of E groups, E = 0: dense) and C output columns
@@ -979,7 +985,7 @@ static int dw_(const LinBwdArgs& a, hipStream_t st) {
     const int64_t t256 = groups * ((a.N + 255) / 256) * ((a.K + 255) / 256);
     const int64_t t128 = groups * ((a.N + 127) / 128) * ((a.K + 127) / 128);
     if (M < 512 * groups) return go(k_linear_dw_few<D>, t128, 256, a, st);
-    if (t256 >= 128) return go(k_linear_dw256<D>, t256 + 3 * kRest256, kT2Threads, a, st);
+    if (t256 >= 128) return go(k_linear_dw256<D>, blocks256(t256, true), kT2Threads, a, st);
     return go(k_linear_dw<D>, t128, 64 * lin_waves<128>(), a, st);
 }
 
