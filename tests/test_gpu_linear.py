@@ -341,6 +341,28 @@ def test_rows_and_experts_do_not_mix():
     assert (got["y"][100:] == -77).all() and (got["dx"][100:] == -77).all()
 
 
+@pytest.mark.parametrize("N,K,counts", [(4232, 136, [1700, 1, 64, 0, 1900]), (136, 4232, [1700, 1, 64, 0, 1900]),
+                                        (2184, 4232, [787, 513]), (264, 2056, [60, 0, 140])])
+def test_large_tiles_and_split_reductions_keep_groups_apart(N, K, counts):
+    """NaN in the last group and behind it, in every operand: the groups before it stay as they were."""
+    c = Lin(25, sum(counts) + 21, N, K, BF, "none", counts)
+    out = c.outputs()
+    c.run(out)
+    n, nan = sum(counts[:-1]), float("nan")
+    for name in ("x", "dy", "res"):
+        getattr(c, name)[n:] = nan
+    c.w[-1] = nan
+    c.bias[-1] = nan
+    got = c.outputs()
+    c.run(got)
+    for name in ("y", "z", "dx"):
+        assert torch.equal(got[name][:n], out[name][:n]), name
+        assert (got[name][c.live:] == -77).all(), name
+    for name in ("dw", "db"):
+        assert torch.equal(got[name][:-1], out[name][:-1]), name
+        assert torch.isnan(got[name][-1]).all(), name
+
+
 @pytest.mark.parametrize("E", [7, 90])
 def test_overlapping_groups_stay_inside_the_workspace(E):
     """Offsets that go back and forth: more tiles than any valid offsets have."""
@@ -448,6 +470,12 @@ def test_two_calls_at_once_on_two_streams():
     for w, g in zip(want, got):
         for n in w:
             assert torch.equal(w[n], g[n]), n
+
+
+@pytest.mark.parametrize("M,N,K,counts", [(128, 264, 2056, None), (40, 264, 2056, [30, 10]), (4200, 4232, 136, None),
+                                          (1300, 2184, 4232, [513, 787])])
+def test_large_and_split_products_replayed_from_a_graph(M, N, K, counts):
+    test_replayed_from_a_graph(M, N, K, counts)
 
 
 @pytest.mark.parametrize("M,N,K,counts", [(4, 512, 1024, None), (200, 264, 520, None), (600, 512, 256, [300, 0, 290]),
