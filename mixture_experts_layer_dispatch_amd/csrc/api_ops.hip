@@ -51,7 +51,8 @@ LinLayout lin_layout(const moe_linear_config& c) {
     };
     for (size_t& l : L.lists) l = take((size_t)(c.E + 1) * 4);
     L.dz = take(c.act == MOE_ACT_NONE ? 0 : (size_t)c.M * c.N * 2);
-    L.part = take(((size_t)(c.M + kLinDzRows - 1) / kLinDzRows + c.E) * c.N * 4);
+    const int rows = linear_dz_rows(c.M, c.E, c.N);
+    L.part = take((((size_t)c.M + rows - 1) / rows + c.E) * c.N * 4);
     const size_t f = linear_part_floats(linear_plan(c.M, c.E, c.K, c.N, false), c.M, c.N);
     const size_t b = linear_part_floats(linear_plan(c.M, c.E, c.N, c.K, true), c.M, c.K);
     L.sums = take((f > b ? f : b) * 4);
@@ -192,14 +193,14 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     LinPlan p = linear_plan(c->M, c->E, c->N, c->K, true);
-    LinTiles rows32{nullptr, nullptr, c->E, c->M, kLinDzRows, nullptr};
-    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->K, 128}, {&p.big, c->K, 256}, {&rows32, c->N, 512}}, st))
+    LinTiles strips{nullptr, nullptr, c->E, c->M, linear_dz_rows(c->M, c->E, c->N), nullptr};
+    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->K, 128}, {&p.big, c->K, 256}, {&strips, c->N, 512}}, st))
         return MOE_ERR_HIP;
     uint16_t* dz = (uint16_t*)(ws + L.dz);
     float* part = db ? (float*)(ws + L.part) : nullptr;
-    const LinDzArgs d{rows32, c->dtype, c->act, c->N, (const uint16_t*)dy, (const uint16_t*)z, dz, part};
+    const LinDzArgs d{strips, c->dtype, c->act, c->N, (const uint16_t*)dy, (const uint16_t*)z, dz, part};
     if ((db || !none) && launch_linear_dz(d, st)) return MOE_ERR_HIP;
-    const LinBwdArgs b{p.small, rows32, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x,
+    const LinBwdArgs b{p.small, strips, c->dtype, c->N, c->K, none ? (const uint16_t*)dy : dz, (const uint16_t*)x,
                        (const uint16_t*)w, (uint16_t*)dx, (uint16_t*)dw, (uint16_t*)db, part,
                        (float*)(ws + L.sums), 0, 0, 0};
     if (launch_linear_bwd(p, b, st)) return MOE_ERR_HIP;

@@ -386,7 +386,6 @@ int launch_unpermute_bwd(const RowsArgs& a, const void* o, const void* dy, const
 // ---------------------------------------------------------------- linear
 // moe_act
 enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4, LIN_ACTS = 5 };
-constexpr int kLinDzRows = 32;       // rows of a k_linear_dz tile
 
 // Row tiles of tm rows (0: none) over the groups, or over one dense group of
 // `rows` rows (offsets null).
@@ -425,7 +424,7 @@ struct LinFwdArgs {
 };
 
 struct LinDzArgs {
-    LinTiles t;               // of kLinDzRows rows
+    LinTiles t;               // of linear_dz_rows rows
     int dtype, act, N;
     const uint16_t* dy;
     const uint16_t* z;        // read unless act is LIN_NONE
@@ -436,7 +435,7 @@ struct LinDzArgs {
 // dx, dw, db: null = not wanted
 struct LinBwdArgs {
     LinTiles t;               // dx's row tiles; dW's groups
-    LinTiles rows32;          // the tiles of part (kLinDzRows rows)
+    LinTiles strips;          // the tiles of part (linear_dz_rows rows)
     int dtype, N, K;
     const uint16_t* dz;       // [M, N]
     const uint16_t* x;
@@ -453,6 +452,7 @@ struct LinBwdArgs {
 // linear.hip
 LinPlan linear_plan(int M, int E, int R, int C, bool dx);
 size_t linear_part_floats(const LinPlan& p, int M, int C);
+int linear_dz_rows(int M, int E, int N);     // rows of a k_linear_dz tile
 bool linear_inline_tiles(const LinTiles& t, int C, int tn);
 int launch_linear_prefix(const LinPrefix& p, hipStream_t st);
 int launch_linear_fwd(const LinPlan& p, const LinFwdArgs& a, hipStream_t st);

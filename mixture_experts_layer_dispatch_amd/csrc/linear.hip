@@ -626,7 +626,7 @@ __global__ __launch_bounds__(64 * lin_waves<128>(), 1) void k_linear_bwd(LinBwdA
     }
     b -= a.ndw;
     if (b < a.ndx) dx_block<D, 128, false>(a, b, ring);
-    else db_columns<D>(a.part, a.rows32, a.N, b - a.ndx, lin_waves<128>(), (float*)ring.a0, a.db);
+    else db_columns<D>(a.part, a.strips, a.N, b - a.ndx, lin_waves<128>(), (float*)ring.a0, a.db);
 }
 
 // ================================================================ 256 x 256 tiles
@@ -683,7 +683,7 @@ template <class D>
 __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dx256(LinBwdArgs a) {
     T2_LDS(lds);
     if ((int)blockIdx.x < a.ndb) {                 // db's columns first (a launch less)
-        db_columns<D>(a.part, a.rows32, a.N, blockIdx.x, kT2Threads / 64, (float*)lds.h[0], a.db);
+        db_columns<D>(a.part, a.strips, a.N, blockIdx.x, kT2Threads / 64, (float*)lds.h[0], a.db);
         return;
     }
     int e, lo, hi, nt, mt, q;
@@ -769,7 +769,7 @@ __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
 template <class D>
 __global__ __launch_bounds__(1024) void k_linear_db(LinBwdArgs a) {
     __shared__ float sums[16 * 64];
-    db_columns<D>(a.part, a.rows32, a.N, blockIdx.x, 16, sums, a.db);
+    db_columns<D>(a.part, a.strips, a.N, blockIdx.x, 16, sums, a.db);
 }
 
 // ================================================================ launchers
@@ -873,6 +873,11 @@ size_t linear_part_floats(const LinPlan& p, int M, int C) {
     return p.ksplit > 1 ? (size_t)p.ksplit * M * C : 0;
 }
 
+// 32, or 8 where those are too few for the chip (1111 x 1000: 7.3 -> 4.4 us).
+int linear_dz_rows(int M, int E, int N) {
+    return max_tiles({nullptr, nullptr, E, M, 32, nullptr}) * ((N + 511) / 512) < 256 ? 8 : 32;
+}
+
 // Whether the blocks of a product find their tiles themselves (LinTiles.list null)
 bool linear_inline_tiles(const LinTiles& t, int C, int tn) {
     return t.E <= 64 && max_tiles(t) * ((C + tn - 1) / tn) <= 2048;
@@ -950,7 +955,10 @@ int launch_linear_fwd(const LinPlan& p, const LinFwdArgs& a, hipStream_t st) {
 template <class D>
 static int dz_(const LinDzArgs& a, hipStream_t st) {
     const int64_t grid = max_tiles(a.t) * ((a.N + 511) / 512);
-    return with_act(a.act, [&](auto A) { return go(k_linear_dz<D, A(), kLinDzRows>, grid, 256, a, st); });
+    return with_act(a.act, [&](auto A) {
+        return a.t.tm == 8 ? go(k_linear_dz<D, A(), 8>, grid, 256, a, st)
+                           : go(k_linear_dz<D, A(), 32>, grid, 256, a, st);
+    });
 }
 
 int launch_linear_dz(const LinDzArgs& a, hipStream_t st) {
