@@ -171,7 +171,8 @@ moe_status moe_linear_forward(const moe_linear_config* c, const int32_t* offsets
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     LinPlan p = linear_plan(c->M, c->E, c->K, c->N, false);
-    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->N, p.stream ? 32 : 128}, {&p.big, c->N, 256}}, st)) return MOE_ERR_HIP;
+    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->N, p.stream ? 32 : 128}, {&p.big, c->N, 256}}, st))
+        return MOE_ERR_HIP;
     const LinFwdArgs a{{}, c->dtype, c->act, c->N, c->K, (const uint16_t*)x, (const uint16_t*)w,
                        (const uint16_t*)bias, (const uint16_t*)residual, (uint16_t*)y, (uint16_t*)z, 1,
                        (float*)(ws + L.sums)};
