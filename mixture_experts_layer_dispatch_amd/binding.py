@@ -180,6 +180,13 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _check_field(name, v, bits=32):
+    """Refuses what a signed field of a C struct cannot hold: ctypes keeps its low bits, which can be
+    another, valid size."""
+    if not -1 << bits - 1 <= v < 1 << bits - 1:
+        raise ValueError(f"{name}: {v} does not fit {bits} bits")
+
+
 @dataclass
 class Config:
     T: int
@@ -194,6 +201,10 @@ class Config:
     precision: int = PREC_BF16
     recompute: bool = False
     acc_experts: int = 0
+
+    def __setattr__(self, name, value):       # here rather than in c(), which every call pays for
+        _check_field(name, value, 64 if name == "capacity_rows" else 32)
+        object.__setattr__(self, name, value)
 
     def c(self) -> moe_config:
         return moe_config(self.T, self.H, self.I, self.E, self.k, self.n_shared, self.macrobatch,
@@ -588,6 +599,8 @@ class LinearConfig:
             raise ValueError(f"act: {self.act!r}, expected one of {', '.join(ACTS)}")
         if self.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"dtype: {self.dtype}, expected torch.bfloat16 or torch.float16")
+        for name in ("M", "N", "K", "E"):
+            _check_field(name, getattr(self, name))
         return moe_linear_config(self.M, self.N, self.K, self.E, DTYPES[self.dtype], ACTS[self.act], 0)
 
 
