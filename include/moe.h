@@ -364,7 +364,9 @@ typedef enum moe_dtype {
  *   workspace: the layer's, or any 256 zeroed bytes (256-byte aligned): only the
  *   device error word, its first 4 bytes, is used.  A row outside [0, S) is
  *   skipped and sets MOE_DEVERR_BAD_ROW; rows that no slot names are left as
- *   they were. */
+ *   they were.
+ *   Outputs of this call and the three below overlap nothing else (the same
+ *   pointer twice is refused), apart from moe_unpermute_forward's residual = y. */
 MOE_API moe_status moe_permute_forward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
                                        const void* x, void* xs, void* workspace, size_t workspace_bytes,
                                        void* stream);
@@ -389,8 +391,8 @@ MOE_API moe_status moe_unpermute_forward(const moe_config* cfg, const moe_sched*
  *   dw [T, k] fp32 (written): <o[row(t,j)], dy[t]>;
  *   d_logits [T, E] fp32 (written; may be NULL): through the softmax over the
  *   chosen logits, zero for experts a token did not choose.
- * d_o must not overlap o or dy.  Reads sched's row_of_slot, topk_w and (for d_logits)
- * topk_idx; workspace as in moe_permute_forward. */
+ * Reads sched's row_of_slot, topk_w and (for d_logits) topk_idx; workspace as in
+ * moe_permute_forward. */
 MOE_API moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,
                                           const void* o, const void* dy, void* d_o, float* dw, float* d_logits,
                                           void* workspace, size_t workspace_bytes, void* stream);

@@ -108,7 +108,7 @@ moe_status moe_permute_forward(const moe_config* cfg, const moe_sched* sched, mo
     RowsArgs a;
     const moe_status s = rows_args(cfg, sched, dtype, workspace, workspace_bytes, a);
     if (s != MOE_OK) return s;
-    if (!at(x, 16) || !at(xs, 16) || x == xs) return MOE_ERR_INVALID_ARG;
+    if (!at(x, 16) || !at(xs, 16) || among(xs, {x, sched->row_of_slot})) return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     return launch_permute(a, x, xs, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
 }
@@ -118,7 +118,7 @@ moe_status moe_permute_backward(const moe_config* cfg, const moe_sched* sched, m
     RowsArgs a;
     const moe_status s = rows_args(cfg, sched, dtype, workspace, workspace_bytes, a);
     if (s != MOE_OK) return s;
-    if (!at(dxs, 16) || !at(dx, 16) || dxs == dx) return MOE_ERR_INVALID_ARG;
+    if (!at(dxs, 16) || !at(dx, 16) || among(dx, {dxs, sched->row_of_slot})) return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     return launch_permute_bwd(a, dxs, dx, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
 }
@@ -129,7 +129,8 @@ moe_status moe_unpermute_forward(const moe_config* cfg, const moe_sched* sched, 
     RowsArgs a;
     const moe_status s = rows_args(cfg, sched, dtype, workspace, workspace_bytes, a);
     if (s != MOE_OK) return s;
-    if (!at(o, 16) || !at_or_null(residual) || !at(y, 16) || !at(sched->topk_w, 4) || o == y)
+    if (!at(o, 16) || !at_or_null(residual) || !at(y, 16) || !at(sched->topk_w, 4) ||
+        among(y, {o, sched->row_of_slot, sched->topk_w}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     return launch_unpermute(a, o, sched->topk_w, residual, y, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
@@ -142,7 +143,11 @@ moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched* sched,
     const moe_status s = rows_args(cfg, sched, dtype, workspace, workspace_bytes, a);
     if (s != MOE_OK) return s;
     if (!at(o, 16) || !at(dy, 16) || !at(d_o, 16) || !at(dw, 4) || !at(sched->topk_w, 4) ||
-        (d_logits && (!at(d_logits, 4) || !at(sched->topk_idx, 4))) || among(d_o, {o, dy}))
+        (d_logits && (!at(d_logits, 4) || !at(sched->topk_idx, 4))))
+        return MOE_ERR_INVALID_ARG;
+    const void *row = sched->row_of_slot, *w = sched->topk_w, *idx = d_logits ? sched->topk_idx : nullptr;
+    if (among(d_o, {o, dy, row, w, idx, dw, d_logits}) || among(dw, {o, dy, row, w, idx, d_logits}) ||
+        among(d_logits, {o, dy, row, w, idx}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     return launch_unpermute_bwd(a, o, dy, sched->topk_idx, sched->topk_w, cfg->E, d_o, dw, d_logits,
@@ -165,7 +170,7 @@ moe_status moe_linear_forward(const moe_linear_config* c, const int32_t* offsets
     const moe_status s = lin_common(c, offsets, workspace, workspace_bytes, L);
     if (s != MOE_OK) return s;
     if (!at(x, 16) || !at(w, 16) || !at(y, 16) || !at_or_null(bias) || !at_or_null(residual) || !at_or_null(z) ||
-        among(y, {x, w, bias, z}) || among(z, {x, w, bias, residual}))
+        among(y, {offsets, x, w, bias, z}) || among(z, {offsets, x, w, bias, residual}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
@@ -188,7 +193,8 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     const bool none = c->act == MOE_ACT_NONE;
     if (!at(dy, 16) || (none ? !at_or_null(z) : !at(z, 16)) || (!dx && !dw && !db) || !at_or_null(dx) ||
         !at_or_null(dw) || !at_or_null(db) || (dx ? !at(w, 16) : !at_or_null(w)) || (dw ? !at(x, 16) : !at_or_null(x)) ||
-        among(dx, {x, w, z, dy, dw, db}) || among(dw, {x, w, z, dy, db}) || among(db, {x, w, z, dy}))
+        among(dx, {offsets, x, w, z, dy, dw, db}) || among(dw, {offsets, x, w, z, dy, db}) ||
+        among(db, {offsets, x, w, z, dy}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
