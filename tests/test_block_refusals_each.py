@@ -56,6 +56,36 @@ def test_an_output_is_no_other_buffer(name, out, other):
     assert _call(name, **{out: ADDR[other]}) == B.MOE_ERR_INVALID_ARG
 
 
+
+# one wrong argument each: a missing or misaligned buffer
+REQUIRED = [(c, n) for c, (bufs, reads) in CALLS.items() for n in bufs + reads if n not in ("residual", "d_logits")]
+
+
+@pytest.mark.parametrize("name,arg", REQUIRED)
+def test_a_buffer_that_is_missing(name, arg):
+    assert _call(name, **{arg: None}) == B.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,arg", [(c, n) for c, (bufs, reads) in CALLS.items() for n in bufs + reads])
+def test_a_buffer_that_is_not_aligned(name, arg):
+    by = 2 if arg in (*SCHED, "dw", "d_logits") else 8     # 4 bytes of indices and fp32 values, 16 of rows
+    assert _call(name, **{arg: ADDR[arg] + by}) == B.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_types_configs_schedules_workspaces(name):
+    for dtype in (-1, 3):
+        assert _call(name, dtype=dtype) == B.MOE_ERR_INVALID_ARG
+    assert _call(name, sched=False) == B.MOE_ERR_INVALID_ARG
+    assert _call(name, with_cfg=False) == B.MOE_ERR_INVALID_ARG
+    for change in (dict(H=100), dict(H=0), dict(T=0), dict(k=0), dict(k=5), dict(E=0), dict(E=1025), dict(I=0)):
+        cfg = B.Config(**{**dict(T=8, H=128, I=128, E=4, k=2), **change})
+        assert _call(name, cfg=cfg) == B.MOE_ERR_INVALID_ARG
+    assert _call(name, ws=None) == B.MOE_ERR_WORKSPACE
+    assert _call(name, ws=ADDR["ws"] + 128) == B.MOE_ERR_WORKSPACE
+    assert _call(name, ws_bytes=255) == B.MOE_ERR_WORKSPACE
+
+
 # ------------------------------------------------------------------ linear
 LIN = {n: (i + 32) << 20 for i, n in enumerate(["offsets", "x", "w", "bias", "residual", "y", "z", "dy", "dx", "dw",
                                                 "db", "ws"])}
@@ -79,3 +109,25 @@ def test_an_output_of_linear_is_no_other_buffer(name, out, other):
     assert _linear(name) == PASSES
     assert _linear(name, **{out: LIN[other]}) == B.MOE_ERR_INVALID_ARG
     assert _linear("moe_linear_forward", residual=LIN["y"]) == PASSES
+
+
+@pytest.mark.parametrize("name,arg", [(c, n) for c, args in LIN_CALLS.items() for n in args
+                                      if n not in ("bias", "residual") and (c, n) != ("moe_linear_forward", "z")
+                                      and n not in ("dx", "dw", "db")])
+def test_a_buffer_of_linear_that_is_missing(name, arg):
+    assert _linear(name, **{arg: None}) == B.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,arg", [(c, n) for c, args in LIN_CALLS.items() for n in args])
+def test_a_buffer_of_linear_that_is_not_aligned(name, arg):
+    assert _linear(name, **{arg: LIN[arg] + (2 if arg == "offsets" else 8)}) == B.MOE_ERR_INVALID_ARG
+
+
+def test_what_linear_may_be_given_without():
+    assert _linear("moe_linear_forward", bias=None, residual=None, z=None) == PASSES
+    for gone in (("dx", "w"), ("dw", "x"), ("db",), ("dx", "dw", "w", "x")):
+        assert _linear("moe_linear_backward", **{n: None for n in gone}) == PASSES
+    assert _linear("moe_linear_backward", dx=None, dw=None, db=None) == B.MOE_ERR_INVALID_ARG
+    for name in LIN_CALLS:
+        assert _linear(name, E=0, offsets=None) == PASSES
+        assert _linear(name, E=0) == B.MOE_ERR_INVALID_ARG
