@@ -390,7 +390,8 @@ MOE_API moe_status moe_unpermute_forward(const moe_config* cfg, const moe_sched*
  *   d_o [S, H] of `dtype` (written): d_o[row(t,j)] = topk_w[t,j] * dy[t];
  *   dw [T, k] fp32 (written): <o[row(t,j)], dy[t]>;
  *   d_logits [T, E] fp32 (written; may be NULL): through the softmax over the
- *   chosen logits, zero for experts a token did not choose.
+ *   chosen logits, zero for experts a token did not choose, the sum over its
+ *   slots for an expert that a caller's table names more than once.
  * Reads sched's row_of_slot, topk_w and (for d_logits) topk_idx; workspace as in
  * moe_permute_forward. */
 MOE_API moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,

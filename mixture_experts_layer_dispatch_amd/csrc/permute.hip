@@ -7,7 +7,7 @@
 //   unpermute backward  do[row(t, j)] = w[t, j] dy[t],
 //                       dw[t, j] = <o[row(t, j)], dy[t]>, and through the
 //                       softmax over the chosen logits
-//                       d_logit[t, idx[t, j]] = w_j (dw_j - sum_i w_i dw_i)
+//                       d_logit[t, idx[t, j]] += w_j (dw_j - sum_i w_i dw_i)
 //
 // with row = row_of_slot of one schedule table, as the pages have it
 // (arex-research.com "Cursor 放出 MoK", design section, first decision: one
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(256) void k_unpermute_bwd(const uint4* __restrict__
     for (int e = sub * 64 + lane; e < E; e += 64 * WPT) {
         float v = 0.f;
         for (int j = 0; j < k; ++j)
-            if (s_idx[tt][j] == e) v = s_dl[tt][j];
+            if (s_idx[tt][j] == e) v += s_dl[tt][j];      // (a caller's table may name an expert twice)
         d_logits[(int64_t)t * E + e] = v;
     }
 }

@@ -40,7 +40,8 @@ def unpermute_backward(o, dy, row_of_slot, w, idx, E):
     do[row_of_slot] = (w[:, :, None] * dy[:, None, :]).reshape(T * k, -1)
     dw = np.einsum("tkh,th->tk", rows, dy)
     dl = np.zeros((T, E))
-    np.put_along_axis(dl, np.asarray(idx, np.int64), w * (dw - (w * dw).sum(1, keepdims=True)), axis=1)
+    # added, not put: a caller's table may name an expert twice
+    np.add.at(dl, (np.arange(T)[:, None], np.asarray(idx, np.int64)), w * (dw - (w * dw).sum(1, keepdims=True)))
     return do, dw, dl
 
 
