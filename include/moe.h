@@ -391,7 +391,8 @@ MOE_API moe_status moe_unpermute_forward(const moe_config* cfg, const moe_sched*
  *   dw [T, k] fp32 (written): <o[row(t,j)], dy[t]>;
  *   d_logits [T, E] fp32 (written; may be NULL): through the softmax over the
  *   chosen logits, zero for experts a token did not choose, the sum over its
- *   slots for an expert that a caller's table names more than once.
+ *   slots for an expert that a caller's table names more than once; an expert
+ *   outside [0, E) is skipped and sets MOE_DEVERR_BAD_EXPERT.
  * Reads sched's row_of_slot, topk_w and (for d_logits) topk_idx; workspace as in
  * moe_permute_forward. */
 MOE_API moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched* sched, moe_dtype dtype,

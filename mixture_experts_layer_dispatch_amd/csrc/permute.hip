@@ -248,7 +248,9 @@ __global__ __launch_bounds__(256) void k_unpermute_bwd(const uint4* __restrict__
     for (int j = 0; j < k; ++j) c = fmaf(lane_value(myw, j), lane_value(mydw, j), c);
     if (live && sub == 0 && lane < k) {
         s_dl[tt][lane] = myw * (mydw - c);
-        s_idx[tt][lane] = idx[(int64_t)t * k + lane];
+        const int e = idx[(int64_t)t * k + lane];
+        s_idx[tt][lane] = e;                              // (compared only: one outside matches nothing below)
+        if ((unsigned)e >= (unsigned)E) raise_err(err, ERR_BAD_EXPERT);
     }
     __syncthreads();
     if (!live) return;

@@ -1,4 +1,5 @@
-"""Schedule tables built by the caller: an expert chosen twice by a token."""
+"""Schedule tables built by the caller: an expert chosen twice by a token, and
+experts outside the layer's."""
 import numpy as np
 import pytest
 import torch
@@ -52,3 +53,24 @@ def test_an_expert_chosen_twice_gets_both_gradients(T, E, k, H, dtype):
     np.add.at(tol, (t, idx.cpu().numpy()), serr + 2.0 ** -22 * np.abs(share))
     assert_within("dl", dl, ref, tol)
     assert w.shape == (T, k) and B.moe_check_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("T,E,k,H", SHAPES)
+def test_experts_outside_the_layer_are_skipped_and_reported(T, E, k, H):
+    cfg, sched, ws = schedule(53, T, E, k, H)
+    g = gen(54)
+    o, dy = randn(g, (T * k, H), BF), randn(g, (T, H), BF)
+    plain = _backward(cfg, sched, ws, o, dy)
+    assert B.moe_check_device_error(ws) == 0
+    good = sched["topk_idx"]
+    for bad in (E, -1, 1 << 30):
+        idx = good.clone()
+        idx[3, 2] = bad
+        do, dw, dl = _backward(cfg, {**sched, "topk_idx": idx}, ws, o, dy)
+        assert B.moe_check_device_error(ws) == B.DEVERR_BAD_EXPERT
+        assert B.moe_check_device_error(ws) == 0            # read and cleared
+        want = plain[2].clone()
+        want[3, good[3, 2].long()] = 0
+        assert torch.equal(dl, want) and torch.equal(do, plain[0]) and torch.equal(dw, plain[1])
+        B.moe_unpermute_backward(cfg, {**sched, "topk_idx": idx}, o, dy, do, dw, ws)      # not read
+        assert B.moe_check_device_error(ws) == 0
