@@ -359,8 +359,9 @@ typedef enum moe_dtype {
 
 /* Rows to experts ([AREX] first decision; [ALPHA] 一: dispatch).
  *   x [T, H], xs [S, H] of `dtype` (xs written): xs[row_of_slot[t*k+j]] = x[t].
- *   Of cfg only T, H, E and k matter, of sched only row_of_slot; rows are those
- *   of the whole batch (macrobatch m's are [m*M*k, (m+1)*M*k)).
+ *   Of cfg only T, H, E and k matter (the rest has to be valid), of sched only
+ *   row_of_slot; rows are those of the whole batch (macrobatch m's are
+ *   [m*M*k, (m+1)*M*k)).
  *   workspace: the layer's, or any 256 zeroed bytes (256-byte aligned): only the
  *   device error word, its first 4 bytes, is used.  A row outside [0, S) is
  *   skipped and sets MOE_DEVERR_BAD_ROW; rows that no slot names are left as
@@ -402,7 +403,7 @@ MOE_API moe_status moe_unpermute_backward(const moe_config* cfg, const moe_sched
 typedef enum moe_act {
     MOE_ACT_NONE = 0,
     MOE_ACT_RELU = 1,
-    MOE_ACT_GELU = 2,        /* z Phi(z), by erf                                      */
+    MOE_ACT_GELU = 2,        /* z Phi(z), Phi the normal distribution (below -6: 0)   */
     MOE_ACT_GELU_TANH = 3,   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))         */
     MOE_ACT_SILU = 4         /* z sigmoid(z)                                          */
 } moe_act;
@@ -427,8 +428,11 @@ MOE_API moe_status moe_linear_workspace_size(const moe_linear_config* cfg, size_
  *   x [M, K], w [N, K] (E > 0: [E, N, K]), bias [N] (or [E, N]; may be NULL),
  *   residual [M, N] (may be NULL; may be y itself), y [M, N] (written),
  *   z [M, N] (written for the backward; may be NULL), all of cfg->dtype.
- *   offsets: NULL if E is 0, else device int32 [E+1] ascending (one macrobatch's
- *   moe_sched.offsets): rows offsets[e] .. offsets[e+1] take expert e's weights.
+ *   offsets: NULL if E is 0, else device int32 [E+1] ascending: rows offsets[e]
+ *   .. offsets[e+1] take expert e's weights.  moe_sched.offsets of one macrobatch:
+ *   they count from its first row, so with several, macrobatch m's call takes
+ *   offsets + m*(E+1) and the rows from m*M*k on of x, residual, y and z, with
+ *   cfg->M = M*k of the layer's M, k (and its own dw, db: they are not added to).
  *   Rows in no group are neither read nor written.  A group that is not inside
  *   [0, M] or not ascending is skipped and sets MOE_DEVERR_BAD_OFFSETS.
  *   fp32 accumulation; the sum, bias, activation and residual in fp32, y and z
@@ -445,8 +449,10 @@ MOE_API moe_status moe_linear_forward(const moe_linear_config* cfg, const int32_
  *   z: as moe_linear_forward wrote it (not read if act is MOE_ACT_NONE); x is
  *   read for dw, w for dx (else they may be NULL).
  *   dz is rounded to cfg->dtype once as the products' operand (db sums it
- *   unrounded); outputs are overwritten and overlap nothing else.  A group without rows gets dw = 0 and
- *   db = 0; rows of dx in no group are left as they were. */
+ *   unrounded), with that type's range: in fp16 a |dz| up to 2^-25 counts as 0
+ *   and one of 65520 or more as infinite, so scale the loss as for dy.
+ *   Outputs are overwritten and overlap nothing else.  A group without rows
+ *   gets dw = 0 and db = 0; rows of dx in no group are left as they were. */
 MOE_API moe_status moe_linear_backward(const moe_linear_config* cfg, const int32_t* offsets, const void* x,
                                        const void* w, const void* z, const void* dy, void* dx, void* dw, void* db,
                                        void* workspace, size_t workspace_bytes, void* stream);

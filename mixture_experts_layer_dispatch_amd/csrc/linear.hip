@@ -158,8 +158,8 @@ __device__ __forceinline__ WaveTiles wave_tiles(const LinTiles& t, bool tell) {
 // 256 x 256 tiles behind the last whole round of 256 that are computed as four
 // 128 x 128 tiles each: up to 64 make one round of those, up to 128 two, which
 // take 0.4 and 0.8 of the time of a round of the large tiles (4096 -> 4096, 5120
-// rows: 320 tiles, 178 -> 138 us; 5632 rows, 352 tiles, 179 -> 168; 6144, 384,
-// 181 -> 174).
+// rows: 320 tiles, 178 -> 143 us; 5632 rows, 352 tiles, 179 -> 169; 6144, 384,
+// 181 -> 179).
 constexpr int kRest256 = 128;
 
 // The tile L of block b of `total`; with `quarter`, the quarter of it for a tile
@@ -723,9 +723,14 @@ __global__ __launch_bounds__(kT2Threads, 2) void k_linear_dw256(LinBwdArgs a) {
 
 // ================================================================ dz and db
 // A block takes a tile of TR rows by 512 columns (8 per lane, rows round
-// robin over four waves): dz = dy act'(z) (rounded once, to the type the
-// products read), and the column sums of the unrounded dz, in fp32, one
-// partial row per tile.  Bound by HBM: 20480 x 1024 bf16, 126 MB in 27 us.
+// robin over four waves): dz = dy act'(z), and the column sums of the
+// unrounded dz, in fp32, one partial row per tile.  dz is rounded once, to the
+// 16-bit type that the MFMA multiplies: both products see an operand half a
+// step off, as random from element to element as the rounding of their result,
+// so dx and dW are off by sqrt(2) times what rounding the result alone costs
+// (1111 x 1000 x 1544 fp16: 2.9e-4 of the norm, 2.1e-4 for products of
+// unrounded dz).  Keeping more of dz takes a second 16-bit operand and twice
+// the products.  Bound by HBM: 20480 x 1024 bf16, 126 MB in 27 us.
 template <class D, int ACT, int TR>
 __global__ __launch_bounds__(256) void k_linear_dz(LinDzArgs a) {
     __shared__ float sums[3][64][8];

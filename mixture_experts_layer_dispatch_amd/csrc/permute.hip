@@ -27,7 +27,8 @@
 
 namespace moe {
 
-// Launches of more than 2^32 threads take a second grid dimension.
+// Launches of more than 2^22 blocks (2^30 threads) take a second grid
+// dimension: a dimension's threads are counted in 32 bits.
 constexpr int64_t kGridX = 1 << 22;
 static dim3 rows_grid(int64_t blocks) {
     if (blocks <= kGridX) return dim3((unsigned)blocks);

@@ -22,8 +22,9 @@
 //
 // 16384 x 4096 x 4096, bf16: x W^T 417 us (1320 TFLOP/s; with gelu 433), dz W
 // 389 (1413), dz^T x 383 (1436); the library's products there: 436, 501 and 915.
-// MFMA busy 69 percent of the cycles, at 1.94 GHz, what power leaves of the
-// clock; 2 percent of the LDS cycles are bank conflicts.  256 x 256 rather than
+// MFMA busy 70 percent of x W^T's cycles (62 with gelu and two outputs), at
+// 1.94 GHz, what power leaves of the clock; 2 percent of the LDS cycles are bank
+// conflicts.  256 x 256 rather than
 // 128 x 128 halves the bytes that each product reads from LDS and L2; the
 // accumulators then take half of a wave's registers, hence eight waves, one
 // block to a CU and the alternating groups instead of several blocks.
@@ -374,14 +375,15 @@ __device__ __forceinline__ void t2_put(const T2Lds& lds, bool nt, uint16_t* out,
 }
 
 // ================================================================ 64 / 128 x 128 tiles
-// Fewer rows, or too few 256 x 256 tiles for the chip: four waves in a 2 x 2
-// grid, each TM / 2 rows by 64 columns, over a ring of NST stages of 64
+// Fewer rows, or too few 256 x 256 tiles for the chip: NW waves in two rows of
+// NW / 2, each TM / 2 rows by 256 / NW columns (64-row tiles: four waves of 64
+// columns; 128-row tiles: eight of 32), over a ring of NST stages of 64
 // reduction indices that copies fill NST - 1 steps ahead; one barrier a step,
 // after which the stage read a step before is filled again.  A block at a time
 // on a CU then has up to 96 KB of copies in flight: with one step in flight
 // (register-staged) such a product took about 1 us a step, the latency of a
 // load from HBM.
-// NW waves in two rows; a wave's columns are NB blocks of 16.
+// A wave's columns are NB blocks of 16.
 template <int NW>
 constexpr int t1_nb() { return 16 / NW; }
 template <int TM, int NW>
