@@ -203,7 +203,8 @@ class Config:
     acc_experts: int = 0
 
     def __setattr__(self, name, value):       # here rather than in c(), which every call pays for
-        _check_field(name, value, 64 if name == "capacity_rows" else 32)
+        if name in Config.__dataclass_fields__:
+            _check_field(name, value, 64 if name == "capacity_rows" else 32)
         object.__setattr__(self, name, value)
 
     def c(self) -> moe_config:

@@ -42,3 +42,10 @@ def test_layer_config(field, sign):
         setattr(cfg, field, wrong)
     assert B.validate_config(cfg) == B.MOE_OK             # as it was
     assert B.validate_config(B.Config(**{**SIZES, "capacity_rows": 1 << 40})) == B.MOE_OK
+
+
+def test_a_config_may_carry_other_attributes():
+    cfg = B.Config(**SIZES)
+    cfg.name = "a label"
+    cfg.note = 1 << 80
+    assert B.validate_config(cfg) == B.MOE_OK and cfg == B.Config(**SIZES)
