@@ -354,7 +354,7 @@ MOE_API moe_status moe_quantize_weights_mxfp4(const moe_config* cfg, const moe_w
 typedef enum moe_dtype {
     MOE_DT_BF16 = 0,
     MOE_DT_FP16 = 1,
-    MOE_DT_FP32 = 2      /* permute and unpermute only */
+    MOE_DT_FP32 = 2      /* permute, unpermute and norm only */
 } moe_dtype;
 
 /* Rows to experts ([AREX] first decision; [ALPHA] 一: dispatch).
@@ -456,6 +456,156 @@ MOE_API moe_status moe_linear_forward(const moe_linear_config* cfg, const int32_
 MOE_API moe_status moe_linear_backward(const moe_linear_config* cfg, const int32_t* offsets, const void* x,
                                        const void* w, const void* z, const void* dy, void* dx, void* dw, void* db,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Around the experts: routing with scores of its own, the norm in front of
+ * the router and the experts, and products with 4-bit weights.  With them a
+ * block of a model is
+ *   moe_norm_forward (residual added), moe_router_forward, moe_route_forward,
+ *   moe_schedule_from_topk, moe_permute_forward, moe_linear_forward or
+ *   moe_linear_w4_forward, moe_unpermute_forward
+ * ------------------------------------------------------------------------ */
+typedef enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,   /* s = softmax of a token's logits over all experts         */
+    MOE_SCORE_SIGMOID = 1    /* s = 1 / (1 + exp(-logit)), each expert by itself          */
+} moe_score;
+
+typedef struct moe_route_config {
+    int32_t score;         /* moe_score                                                 */
+    int32_t n_group;       /* groups of E / n_group consecutive experts, 1..64, divides E */
+    int32_t topk_group;    /* groups a token may choose from, 1..n_group; together they  */
+                           /* hold at least k experts                                   */
+    int32_t group_top;     /* a group's score is the sum of its 1 or 2 best experts'      */
+    int32_t renorm;        /* 1: the chosen experts' weights sum to scale; 0: they are    */
+                           /* scale * s                                                 */
+    float scale;           /* finite                                                    */
+} moe_route_config;
+
+/* The k experts of every token and their weights ([ALPHA] 一 and 四: a router
+ * keeps the top k).  With s the scores and c = s + bias:
+ *   groups: the topk_group groups with the largest sum of their group_top best c;
+ *   topk_idx[t]: the k largest c of those groups, in descending order;
+ *   topk_w[t,j] = scale * s_j / (renorm ? sum of the k chosen s : 1)
+ * The bias steers the choice only.  Ties go to the lower index, of experts and of
+ * groups.  The choice is that of c computed in 64 bits (without a bias and with
+ * group_top 1 that of the logits themselves: s grows with them).
+ *   logits [T, E] fp32; bias [E] fp32 (may be NULL); scores [T, E] fp32 (written;
+ *   may be NULL): all scores.  Of cfg only T, E and k matter (the rest has to be
+ *   valid); of sched only topk_idx and topk_w, both written.  4-byte alignment is enough.
+ * A logit of -inf has the score 0; a NaN counts as one; several +inf share the
+ * softmax among them.  A c of -inf (from the bias; a NaN counts as one) is the
+ * last choice, but a token always has k different experts.  Weights whose sum is 0 are 0.
+ * Outputs overlap nothing else (the same pointer twice is refused). */
+MOE_API moe_status moe_route_forward(const moe_config* cfg, const moe_route_config* route, const float* logits,
+                                     const float* bias, const moe_sched* sched, float* scores, void* stream);
+
+/* Its gradient: d_logits [T, E] fp32 (written) from dw [T, k] fp32, the weights'
+ * (of moe_backward or moe_unpermute_backward), and d_scores [T, E] fp32, that of
+ * `scores` (a balance loss; may be NULL).  The choice itself has none, nor has the
+ * bias.  Reads sched's topk_idx; an expert outside [0, E) is left out and sets
+ * MOE_DEVERR_BAD_EXPERT, one that a caller's table names more than once gets the
+ * sum over its slots.  NULL d_scores with renorm or sigmoid scores: zero for
+ * experts that a token did not choose.  A token whose chosen scores sum to 0 has
+ * no gradient from dw if renorm.  workspace as in moe_permute_forward. */
+MOE_API moe_status moe_route_backward(const moe_config* cfg, const moe_route_config* route, const float* logits,
+                                      const moe_sched* sched, const float* dw, const float* d_scores,
+                                      float* d_logits, void* workspace, size_t workspace_bytes, void* stream);
+
+/* moe_schedule for a choice that is made already: reads sched's topk_idx (topk_w
+ * is left as it is) and writes the rest of the table.  A slot whose expert is
+ * outside [0, E) gets no row (row_of_slot -1, skipped by the calls that read it)
+ * and sets MOE_DEVERR_BAD_EXPERT; the rows at a macrobatch's end that are then
+ * left over have slot_of_row -1. */
+MOE_API moe_status moe_schedule_from_topk(const moe_config* cfg, const moe_sched* sched, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+typedef enum moe_norm_kind {
+    MOE_NORM_LAYER = 0,    /* mean and variance                                         */
+    MOE_NORM_RMS = 1       /* mean square, no mean                                      */
+} moe_norm_kind;
+
+typedef struct moe_norm_config {
+    int32_t M;             /* rows, 1..2^24                                            */
+    int32_t H;             /* row length, a multiple of 8, 8..65536                      */
+    int32_t kind;          /* moe_norm_kind                                            */
+    int32_t dtype;         /* moe_dtype of the rows (bf16, fp16 or fp32)                 */
+    int32_t params;        /* moe_dtype of gamma and beta: dtype or MOE_DT_FP32          */
+    float eps;             /* >= 0, finite                                             */
+} moe_norm_config;
+
+/* Host-only: bytes of workspace moe_norm_backward needs.  One serves any number
+ * of calls on one stream; calls that overlap need one each.  It needs no
+ * initialisation. */
+MOE_API moe_status moe_norm_workspace_size(const moe_norm_config* cfg, size_t* bytes);
+
+/* y = (h - mean) * rstd * gamma + beta with h = x + residual,
+ *   mean = sum(h) / H (MOE_NORM_RMS: 0), rstd = (sum((h - mean)^2) / H + eps)^(-1/2).
+ *   x, residual (may be NULL), y, total [M, H] of cfg->dtype; gamma, beta (may be
+ *   NULL; NULL for MOE_NORM_RMS) [H] of cfg->params; mean (NULL for MOE_NORM_RMS),
+ *   rstd [M] fp32, both written for the backward, both may be NULL.
+ *   total: h, rounded to cfg->dtype (the next skip connection, and the backward's
+ *   x); given if and only if residual is; may be x or residual itself.  The
+ *   statistics and y are those of the rounded h.
+ * Sums in fp32, y rounded once.  Apart from total, outputs overlap nothing else
+ * (the same pointer twice is refused). */
+MOE_API moe_status moe_norm_forward(const moe_norm_config* cfg, const void* x, const void* residual,
+                                    const void* gamma, const void* beta, void* y, void* total, float* mean,
+                                    float* rstd, void* stream);
+
+/* Its gradients, with xh = (x - mean) * rstd and g = dy * gamma:
+ *   dx = rstd * (g - sum(g) / H - xh * sum(g * xh) / H) + d_total
+ *        (MOE_NORM_RMS: without the term sum(g) / H), x's and the residual's alike;
+ *   dgamma [H] = sum over the rows of dy * xh, dbeta [H] = sum of dy.
+ *   x: the forward's x, or its total where it had a residual; d_total [M, H] (may
+ *   be NULL): the gradient that total has from elsewhere; mean (NULL for
+ *   MOE_NORM_RMS) and rstd as the forward wrote them.
+ *   dx, dgamma, dbeta: NULL = not wanted, but not all three; overwritten.  dx may
+ *   be dy or d_total itself; apart from that outputs overlap nothing else.
+ * Sums in fp32 in a fixed order, each result rounded once. */
+MOE_API moe_status moe_norm_backward(const moe_norm_config* cfg, const void* x, const void* gamma,
+                                     const float* mean, const float* rstd, const void* dy, const void* d_total,
+                                     void* dx, void* dgamma, void* dbeta, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+typedef struct moe_linear_w4_config {
+    int32_t M;             /* rows, 1..2^24                                            */
+    int32_t N;             /* outputs, a multiple of 8, 8..65536                       */
+    int32_t K;             /* inputs, a multiple of group, at most 65536                */
+    int32_t E;             /* 0: one dense product; 1..1024: a product per expert      */
+    int32_t group;         /* inputs that share a scale: 32, 64 or 128                  */
+    int32_t dtype;         /* MOE_DT_BF16 or MOE_DT_FP16: x, y, scales, bias, residual   */
+    int32_t act;           /* moe_act                                                  */
+    int32_t flags;         /* 0                                                        */
+} moe_linear_w4_config;
+
+/* Host-only: bytes of workspace moe_linear_w4_forward needs, as
+ * moe_linear_workspace_size. */
+MOE_API moe_status moe_linear_w4_workspace_size(const moe_linear_w4_config* cfg, size_t* bytes);
+
+/* moe_linear_forward with weights of 4 bits, for serving:
+ *   w[n,k] = scales[k / group, n] * (code[n,k] - zeros[k / group, n])
+ *   codes [N, K/2] bytes (E > 0: [E, N, K/2]): code[n,k] is the low nibble of
+ *   byte k/2 for even k, the high one for odd k; scales [K/group, N] (or [E,
+ *   K/group, N]) of cfg->dtype; zeros, bytes of scales' shape, may be NULL: 8.
+ *   The rest as in moe_linear_forward (no z: there is no backward).
+ * The products are those of the exact code - zero, summed in fp32 over a group,
+ * and a group's sum is multiplied by its scale in fp32: the weights are rounded
+ * nowhere.  A scale of 0 switches a group off only where x is finite. */
+MOE_API moe_status moe_linear_w4_forward(const moe_linear_w4_config* cfg, const int32_t* offsets, const void* x,
+                                         const void* codes, const void* scales, const void* zeros,
+                                         const void* bias, const void* residual, void* y, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* The 4-bit form of w [N, K] (E > 0: [E, N, K]) of cfg->dtype: codes, scales and
+ * zeros (may be NULL) as above, all written.  Of a group's values w:
+ *   zeros NULL: scale = max|w| / 7, code = 8 + w / scale;
+ *   else with lo = min(w, 0), hi = max(w, 0): scale = (hi - lo) / 15,
+ *   zero = -lo / scale, code = zero + w / scale;
+ * scale rounded to cfg->dtype first (a group whose scale is 0 has the codes of 0:
+ * 8, or zero = 0), quotients rounded to the nearest whole number (ties to even),
+ * zero and codes cut to 0..15.  w is finite.  Of cfg N, K, E, group and dtype matter. */
+MOE_API moe_status moe_linear_w4_quantize(const moe_linear_w4_config* cfg, const void* w, void* codes,
+                                          void* scales, void* zeros, void* stream);
 
 /* Reads and clears the sticky device error word that kernels set when a
  * caller-built schedule holds an out-of-range expert, slot or row (those

@@ -37,6 +37,9 @@ EXPORTED = [
     "moe_router_forward", "moe_router_backward", "moe_quantize_weights_mxfp4",
     "moe_permute_forward", "moe_permute_backward", "moe_unpermute_forward", "moe_unpermute_backward",
     "moe_linear_workspace_size", "moe_linear_forward", "moe_linear_backward",
+    "moe_route_forward", "moe_route_backward", "moe_schedule_from_topk",
+    "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward",
+    "moe_linear_w4_workspace_size", "moe_linear_w4_forward", "moe_linear_w4_quantize",
 ]
 
 FLAG_RECOMPUTE = 1
@@ -58,6 +61,19 @@ class moe_config(ctypes.Structure):
 
 class moe_linear_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "E", "dtype", "act", "flags")]
+
+
+class moe_route_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_group", "topk_group", "group_top", "renorm")] + [
+                ("scale", ctypes.c_float)]
+
+
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "H", "kind", "dtype", "params")] + [("eps", ctypes.c_float)]
+
+
+class moe_linear_w4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "E", "group", "dtype", "act", "flags")]
 
 
 class moe_sched(ctypes.Structure):
@@ -147,6 +163,16 @@ def lib() -> ctypes.CDLL:
         L.moe_linear_workspace_size.argtypes = [lcp, ctypes.POINTER(sz)]
         L.moe_linear_forward.argtypes = [lcp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_linear_backward.argtypes = [lcp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        rcp, ncp, wcp = (ctypes.POINTER(c) for c in (moe_route_config, moe_norm_config, moe_linear_w4_config))
+        L.moe_route_forward.argtypes = [cfgp, rcp, vp, vp, sp, vp, vp]
+        L.moe_route_backward.argtypes = [cfgp, rcp, vp, sp, vp, vp, vp, vp, sz, vp]
+        L.moe_schedule_from_topk.argtypes = [cfgp, sp, vp, sz, vp]
+        L.moe_norm_workspace_size.argtypes = [ncp, ctypes.POINTER(sz)]
+        L.moe_norm_forward.argtypes = [ncp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_norm_backward.argtypes = [ncp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_w4_workspace_size.argtypes = [wcp, ctypes.POINTER(sz)]
+        L.moe_linear_w4_forward.argtypes = [wcp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_w4_quantize.argtypes = [wcp, vp, vp, vp, vp, vp]
         for name in EXPORTED:
             if name != "moe_status_string":
                 getattr(L, name).restype = ctypes.c_int
@@ -782,6 +808,253 @@ def moe_linear_backward(lc: LinearConfig, x, w, z, dy: torch.Tensor, ws: torch.T
     _check_tensors(specs, optional)
     _check(lib().moe_linear_backward(c, _ptr(offsets), _ptr(x), _ptr(w), _ptr(z), dy.data_ptr(), _ptr(dx), _ptr(dw),
                                      _ptr(db), ws.data_ptr(), ws.numel(), _stream(stream)), "moe_linear_backward")
+
+
+# ------------------------------------------------------------------ around the experts
+SCORES = {"softmax": 0, "sigmoid": 1}
+NORMS = {"layer": 0, "rms": 1}
+
+
+@dataclass(frozen=True)
+class RouteConfig:
+    """moe_route_config: scores over all experts ("softmax" or "sigmoid"); a token chooses inside the
+    topk_group best of n_group groups, a group counting as the sum of its group_top best experts;
+    renorm: the weights of the chosen sum to scale."""
+    score: str = "softmax"
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renorm: bool = True
+    scale: float = 1.0
+
+    @functools.cached_property
+    def checked(self) -> moe_route_config:
+        if self.score not in SCORES:
+            raise ValueError(f"score: {self.score!r}, expected one of {', '.join(SCORES)}")
+        for name in ("n_group", "topk_group", "group_top"):
+            _check_field(name, getattr(self, name))
+        return moe_route_config(SCORES[self.score], self.n_group, self.topk_group, self.group_top, bool(self.renorm),
+                                self.scale)
+
+
+def _topk(cfg: Config, sched: dict, names):
+    """(moe_sched of the named [T, k] arrays, their specs)"""
+    st, specs = moe_sched(), []
+    for name in names:
+        t = sched.get(name)
+        specs.append((name, t, (cfg.T, cfg.k), torch.float32 if name == "topk_w" else torch.int32))
+        if isinstance(t, torch.Tensor):
+            setattr(st, name, t.data_ptr())
+    return st, specs
+
+
+def moe_route_forward(cfg: Config, route: RouteConfig, logits: torch.Tensor, sched: dict, bias=None, scores=None,
+                      stream=None):
+    """sched["topk_idx"], sched["topk_w"] [T, k]: the experts of every token and their weights, from the
+    scores of logits [T, E]; bias [E] is added for the choice only; scores [T, E] gets all of them."""
+    rc, f32_ = route.checked, torch.float32
+    st, specs = _topk(cfg, sched, ("topk_idx", "topk_w"))
+    specs.append(("logits", logits, (cfg.T, cfg.E), f32_))
+    _check_tensors(specs, (("bias", bias, (cfg.E,), f32_), ("scores", scores, (cfg.T, cfg.E), f32_)))
+    _check(lib().moe_route_forward(cfg.c(), rc, logits.data_ptr(), _ptr(bias), st, _ptr(scores), _stream(stream)),
+           "moe_route_forward")
+
+
+def moe_route_backward(cfg: Config, route: RouteConfig, logits: torch.Tensor, sched: dict, dw: torch.Tensor,
+                       d_logits: torch.Tensor, ws: torch.Tensor, d_scores=None, stream=None):
+    """d_logits [T, E] from dw [T, k], the gradient of topk_w, and d_scores [T, E], that of scores."""
+    rc, f32_, te = route.checked, torch.float32, (cfg.T, cfg.E)
+    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
+    if 0 <= n < 256:
+        raise ValueError(f"workspace: {n} bytes, at least 256 are needed")
+    st, specs = _topk(cfg, sched, ("topk_idx",))
+    specs += [("workspace", ws, (n,), torch.uint8), ("logits", logits, te, f32_), ("dw", dw, (cfg.T, cfg.k), f32_),
+              ("d_logits", d_logits, te, f32_)]
+    _check_tensors(specs, (("d_scores", d_scores, te, f32_),))
+    _check(lib().moe_route_backward(cfg.c(), rc, logits.data_ptr(), st, dw.data_ptr(), _ptr(d_scores),
+                                    d_logits.data_ptr(), ws.data_ptr(), n, _stream(stream)), "moe_route_backward")
+
+
+def moe_schedule_from_topk(cfg: Config, sched: dict, ws: torch.Tensor, stream=None):
+    """moe_schedule for experts that are chosen already: sched["topk_idx"] is read, topk_w left as it is."""
+    specs = _spec_sched(cfg, sched) + _spec_ws(cfg, ws)
+    _check_tensors(specs)
+    _check(lib().moe_schedule_from_topk(cfg.c(), _sched(sched), ws.data_ptr(), ws.numel(), _stream(stream)),
+           "moe_schedule_from_topk")
+
+
+@dataclass(frozen=True)
+class NormConfig:
+    """moe_norm_config: M rows of H elements of dtype; kind "layer" or "rms"; params: the type of gamma
+    and beta, dtype (None) or torch.float32."""
+    M: int
+    H: int
+    dtype: torch.dtype = torch.bfloat16
+    kind: str = "layer"
+    eps: float = 1e-5
+    params: torch.dtype = None
+
+    @property
+    def params_dtype(self) -> torch.dtype:
+        return self.dtype if self.params is None else self.params
+
+    @functools.cached_property
+    def checked(self) -> tuple:
+        """(moe_norm_config, bytes of workspace); raises what is wrong with the config."""
+        c, v = self.c(), ctypes.c_size_t()
+        _check(lib().moe_norm_workspace_size(c, ctypes.byref(v)), "moe_norm_workspace_size")
+        return c, v.value
+
+    def c(self) -> moe_norm_config:
+        if self.kind not in NORMS:
+            raise ValueError(f"kind: {self.kind!r}, expected one of {', '.join(NORMS)}")
+        if self.dtype not in DTYPES:
+            raise ValueError(f"dtype: {self.dtype}, expected torch.bfloat16, torch.float16 or torch.float32")
+        if self.params_dtype not in (self.dtype, torch.float32):
+            raise ValueError(f"params: {self.params}, expected {self.dtype} or torch.float32")
+        for name in ("M", "H"):
+            _check_field(name, getattr(self, name))
+        return moe_norm_config(self.M, self.H, NORMS[self.kind], DTYPES[self.dtype], DTYPES[self.params_dtype],
+                               self.eps)
+
+
+def norm_workspace_size(nc: NormConfig) -> int:
+    return nc.checked[1]
+
+
+def alloc_norm_workspace(nc: NormConfig, device="cuda") -> torch.Tensor:
+    """Workspace of moe_norm_backward."""
+    return torch.empty(norm_workspace_size(nc), dtype=torch.uint8, device=device)
+
+
+def moe_norm_forward(nc: NormConfig, x: torch.Tensor, gamma: torch.Tensor, y: torch.Tensor, beta=None, residual=None,
+                     total=None, mean=None, rstd=None, stream=None):
+    """y = (h - mean) rstd gamma + beta with h = x + residual, which total keeps (x or residual itself may
+    be total); mean, rstd [M] fp32 keep the rows' statistics for the backward."""
+    c, _ = nc.checked
+    dt, p, mh, f32_ = nc.dtype, nc.params_dtype, (nc.M, nc.H), torch.float32
+    if (residual is None) != (total is None):
+        raise ValueError("total: given if and only if residual is")
+    if nc.kind == "rms" and (beta is not None or mean is not None):
+        raise ValueError("beta, mean: not with kind rms")
+    _check_tensors((("x", x, mh, dt), ("gamma", gamma, (nc.H,), p), ("y", y, mh, dt)),
+                   (("beta", beta, (nc.H,), p), ("residual", residual, mh, dt), ("total", total, mh, dt),
+                    ("mean", mean, (nc.M,), f32_), ("rstd", rstd, (nc.M,), f32_)))
+    _check(lib().moe_norm_forward(c, x.data_ptr(), _ptr(residual), gamma.data_ptr(), _ptr(beta), y.data_ptr(),
+                                  _ptr(total), _ptr(mean), _ptr(rstd), _stream(stream)), "moe_norm_forward")
+
+
+def moe_norm_backward(nc: NormConfig, x: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor,
+                      dx, ws: torch.Tensor, mean=None, d_total=None, dgamma=None, dbeta=None, stream=None):
+    """The gradients whose output is given: dx (the residual's too), dgamma, dbeta.  x is the forward's x,
+    or its total where it had a residual; d_total, the gradient total has from elsewhere, is added to dx."""
+    c, need = nc.checked
+    dt, p, mh, f32_ = nc.dtype, nc.params_dtype, (nc.M, nc.H), torch.float32
+    if dx is None and dgamma is None and dbeta is None:
+        raise ValueError("dx, dgamma, dbeta: at least one is needed")
+    if (mean is None) != (nc.kind == "rms"):
+        raise ValueError("mean: given if and only if kind is layer")
+    if nc.kind == "rms" and dbeta is not None:
+        raise ValueError("dbeta: not with kind rms")
+    if dx is None and d_total is not None:
+        raise ValueError("d_total: only with dx")
+    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
+    if 0 <= n < need:
+        raise ValueError(f"workspace: {n} bytes, the config needs {need}")
+    _check_tensors((("workspace", ws, (n,), torch.uint8), ("x", x, mh, dt), ("gamma", gamma, (nc.H,), p),
+                    ("rstd", rstd, (nc.M,), f32_), ("dy", dy, mh, dt)),
+                   (("mean", mean, (nc.M,), f32_), ("d_total", d_total, mh, dt), ("dx", dx, mh, dt),
+                    ("dgamma", dgamma, (nc.H,), p), ("dbeta", dbeta, (nc.H,), p)))
+    _check(lib().moe_norm_backward(c, x.data_ptr(), gamma.data_ptr(), _ptr(mean), rstd.data_ptr(), dy.data_ptr(),
+                                   _ptr(d_total), _ptr(dx), _ptr(dgamma), _ptr(dbeta), ws.data_ptr(), n,
+                                   _stream(stream)), "moe_norm_backward")
+
+
+@dataclass(frozen=True)
+class LinearW4Config:
+    """moe_linear_w4_config: LinearConfig's sizes, and `group` inputs to a scale (32, 64 or 128)."""
+    M: int
+    N: int
+    K: int
+    E: int = 0
+    group: int = 128
+    dtype: torch.dtype = torch.bfloat16
+    act: str = "none"
+
+    @functools.cached_property
+    def checked(self) -> tuple:
+        """(moe_linear_w4_config, bytes of workspace); raises what is wrong with the config."""
+        c, v = self.c(), ctypes.c_size_t()
+        _check(lib().moe_linear_w4_workspace_size(c, ctypes.byref(v)), "moe_linear_w4_workspace_size")
+        return c, v.value
+
+    def c(self) -> moe_linear_w4_config:
+        if self.act not in ACTS:
+            raise ValueError(f"act: {self.act!r}, expected one of {', '.join(ACTS)}")
+        if self.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype: {self.dtype}, expected torch.bfloat16 or torch.float16")
+        for name in ("M", "N", "K", "E", "group"):
+            _check_field(name, getattr(self, name))
+        return moe_linear_w4_config(self.M, self.N, self.K, self.E, self.group, DTYPES[self.dtype], ACTS[self.act], 0)
+
+    @functools.cached_property
+    def shapes(self) -> tuple:
+        """Shapes of the codes, and of the scales and zeros."""
+        lead = (self.E,) if self.E else ()
+        return (*lead, self.N, self.K // 2), (*lead, self.K // self.group, self.N)
+
+
+def linear_w4_workspace_size(wc: LinearW4Config) -> int:
+    return wc.checked[1]
+
+
+def alloc_linear_w4_workspace(wc: LinearW4Config, device="cuda") -> torch.Tensor:
+    """Workspace of moe_linear_w4_forward, its device error word cleared."""
+    ws = torch.empty(linear_w4_workspace_size(wc), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def alloc_linear_w4_weights(wc: LinearW4Config, zeros: bool = False, device="cuda") -> dict:
+    """Buffers of codes, scales and (if asked for) zeros."""
+    codes, groups = wc.shapes
+    out = {"codes": torch.empty(codes, dtype=torch.uint8, device=device),
+           "scales": torch.empty(groups, dtype=wc.dtype, device=device)}
+    if zeros:
+        out["zeros"] = torch.empty(groups, dtype=torch.uint8, device=device)
+    return out
+
+
+def moe_linear_w4_forward(wc: LinearW4Config, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                          y: torch.Tensor, ws: torch.Tensor, zeros=None, bias=None, residual=None, offsets=None,
+                          stream=None):
+    """moe_linear_forward with w[n, k] = scales[k // group, n] * (code[n, k] - zeros[k // group, n]), two
+    codes to a byte (the low nibble is the even k); zeros None: 8.  residual may be y itself."""
+    c, need = wc.checked
+    n = ws.numel() if isinstance(ws, torch.Tensor) else -1
+    if 0 <= n < need:
+        raise ValueError(f"workspace: {n} bytes, the config needs {need}")
+    if (offsets is None) != (wc.E == 0):
+        raise ValueError("offsets: given if and only if E > 0")
+    dt, mn, lead, (cs, gs) = wc.dtype, (wc.M, wc.N), (wc.E,) if wc.E else (), wc.shapes
+    _check_tensors((("workspace", ws, (n,), torch.uint8), ("x", x, (wc.M, wc.K), dt),
+                    ("codes", codes, cs, torch.uint8), ("scales", scales, gs, dt), ("y", y, mn, dt)),
+                   (("zeros", zeros, gs, torch.uint8), ("bias", bias, (*lead, wc.N), dt),
+                    ("residual", residual, mn, dt), ("offsets", offsets, (wc.E + 1,), torch.int32)))
+    _check(lib().moe_linear_w4_forward(c, _ptr(offsets), x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                       _ptr(zeros), _ptr(bias), _ptr(residual), y.data_ptr(), ws.data_ptr(), n,
+                                       _stream(stream)), "moe_linear_w4_forward")
+
+
+def moe_linear_w4_quantize(wc: LinearW4Config, w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros=None,
+                           stream=None):
+    """The codes, scales and (if given) zeros of w [N, K] or [E, N, K]."""
+    c, _ = wc.checked
+    cs, gs = wc.shapes
+    _check_tensors((("w", w, (*cs[:-1], wc.K), wc.dtype), ("codes", codes, cs, torch.uint8),
+                    ("scales", scales, gs, wc.dtype)), (("zeros", zeros, gs, torch.uint8),))
+    _check(lib().moe_linear_w4_quantize(c, w.data_ptr(), codes.data_ptr(), scales.data_ptr(), _ptr(zeros),
+                                        _stream(stream)), "moe_linear_w4_quantize")
 
 
 # device error bits (moe_check_device_error)

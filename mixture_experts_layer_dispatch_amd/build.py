@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe_mi355x.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["route_sched.hip", "elementwise.hip", "gemm.hip", "gemm_mx.hip", "mx.hip", "router.hip", "permute.hip",
-           "linear.hip", "api.hip", "api_ops.hip", "profile.hip"]
+           "linear.hip", "linear_w4.hip", "route.hip", "norm.hip", "api.hip", "api_ops.hip", "profile.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

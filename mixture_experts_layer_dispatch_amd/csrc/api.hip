@@ -701,6 +701,31 @@ moe_status moe_schedule_noalloc(const moe_config* cfg, const float* logits, cons
     return MOE_OK;
 }
 
+moe_status moe_schedule_from_topk(const moe_config* cfg, const moe_sched* sched, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    Geom g;
+    Layout L;
+    moe_status s = common_checks(cfg, g, L, workspace, workspace_bytes);
+    if (s != MOE_OK) return s;
+    // the outputs have to be other buffers than topk_idx, and each other
+    if (!sched_ok(sched)) return MOE_ERR_INVALID_ARG;
+    const void* all[] = {sched->topk_idx, sched->topk_w, sched->counts, sched->offsets, sched->mini_counts,
+                         sched->row_of_slot, sched->slot_of_row};
+    for (int i = 0; i < 7; ++i)
+        for (int j = 0; j < i; ++j)
+            if (all[i] == all[j]) return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    hipStream_t st = (hipStream_t)stream;
+    char* ws = (char*)workspace;
+    int32_t* err = (int32_t*)(ws + L.err);
+    k_clear_word<<<1, 1, 0, st>>>(err);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+    return launch_schedule(sched->topk_idx, g.T, g.E, g.k, g.M, g.mb, (int32_t*)(ws + L.hist), (int32_t*)(ws + L.base),
+                           sched->counts, sched->offsets, sched->mini_counts, sched->row_of_slot, sched->slot_of_row,
+                           err, st)
+               ? MOE_ERR_HIP : MOE_OK;
+}
+
 moe_status moe_router_forward(const moe_config* cfg, const void* x, const void* w_router, float* logits,
                               void* stream) {
     Geom g;

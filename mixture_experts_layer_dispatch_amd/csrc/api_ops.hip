@@ -1,6 +1,7 @@
 // C ABI of the building-block operators: argument validation, workspace
-// layout and the launch sequence of permute / unpermute and linear.  Host
-// code only.
+// layout and the launch sequence of permute / unpermute, linear, routing with
+// scores, norm and linear with 4-bit weights.  Host code only.
+#include <cmath>
 #include <initializer_list>
 
 #include "../../include/moe.h"
@@ -67,15 +68,15 @@ struct Tiles {
     LinTiles* t;
     int C, tn;
 };
-int lin_tiles(const moe_linear_config& c, const int32_t* offsets, char* ws, const LinLayout& L,
-              std::initializer_list<Tiles> sets, hipStream_t st) {
+int lin_tiles(int E, const int32_t* offsets, char* ws, const size_t* lists, std::initializer_list<Tiles> sets,
+              hipStream_t st) {
     LinPrefix p{};
     for (const Tiles& s : sets) {
         s.t->err = (int32_t*)ws;
-        if (c.E == 0) continue;
+        if (E == 0) continue;
         s.t->offsets = offsets;
         if (s.t->tm == 0 || linear_inline_tiles(*s.t, s.C, s.tn)) continue;
-        s.t->list = (const int32_t*)(ws + L.lists[p.n]);
+        s.t->list = (const int32_t*)(ws + lists[p.n]);
         p.t[p.n++] = *s.t;
     }
     return p.n ? launch_linear_prefix(p, st) : 0;
@@ -98,6 +99,62 @@ bool among(const void* out, std::initializer_list<const void*> others) {
         if (out && p == out) return true;
     return false;
 }
+
+// ---------------------------------------------------------------- routing with scores
+moe_status route_args(const moe_config* cfg, const moe_route_config* r, const float* logits, const moe_sched* sched,
+                      RouteArgs& a) {
+    const moe_status s = moe_validate_config(cfg);
+    if (s != MOE_OK) return s;
+    if (!r || (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) || r->n_group < 1 || r->n_group > 64 ||
+        cfg->E % r->n_group || r->topk_group < 1 || r->topk_group > r->n_group || r->group_top < 1 ||
+        r->group_top > 2 || r->group_top > cfg->E / r->n_group || cfg->k > r->topk_group * (cfg->E / r->n_group) ||
+        (r->renorm != 0 && r->renorm != 1) || !std::isfinite(r->scale))
+        return MOE_ERR_INVALID_ARG;
+    if (!at(logits, 4) || !sched || !at(sched->topk_idx, 4)) return MOE_ERR_INVALID_ARG;
+    a = RouteArgs{};
+    a.T = cfg->T;
+    a.E = cfg->E;
+    a.k = cfg->k;
+    a.score = r->score;
+    a.n_group = r->n_group;
+    a.topk_group = r->topk_group;
+    a.group_top = r->group_top;
+    a.renorm = r->renorm == 1;
+    a.scale = r->scale;
+    a.logits = logits;
+    a.idx = sched->topk_idx;
+    return MOE_OK;
+}
+
+// ---------------------------------------------------------------- norm
+moe_status norm_check(const moe_norm_config* c) {
+    if (!c || c->M < 1 || c->M > (1 << 24) || c->H < 8 || c->H > (1 << 16) || c->H % 8) return MOE_ERR_INVALID_ARG;
+    if (c->kind != MOE_NORM_LAYER && c->kind != MOE_NORM_RMS) return MOE_ERR_INVALID_ARG;
+    if (c->dtype != MOE_DT_BF16 && c->dtype != MOE_DT_FP16 && c->dtype != MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
+    if (c->params != c->dtype && c->params != MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
+    if (!(c->eps >= 0.f) || !std::isfinite(c->eps)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+size_t norm_bytes(const moe_norm_config& c) { return up256((size_t)norm_parts(c.M, c.H, c.dtype) * 2 * c.H * 4); }
+
+// ---------------------------------------------------------------- linear with 4-bit weights
+struct W4Layout {
+    size_t list, total;
+};
+
+moe_status w4_check(const moe_linear_w4_config* c) {
+    if (!c || c->M < 1 || c->M > (1 << 24) || c->N < 8 || c->N > (1 << 16) || c->N % 8 || c->E < 0 ||
+        c->E > kMaxExperts || c->flags != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (c->group != 32 && c->group != 64 && c->group != 128) return MOE_ERR_INVALID_ARG;
+    if (c->K < c->group || c->K > (1 << 16) || c->K % c->group) return MOE_ERR_INVALID_ARG;
+    if (c->dtype != MOE_DT_BF16 && c->dtype != MOE_DT_FP16) return MOE_ERR_INVALID_ARG;
+    if (c->act < 0 || c->act >= LIN_ACTS) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+W4Layout w4_layout(const moe_linear_w4_config& c) { return {256, 256 + up256((size_t)(c.E + 1) * 4)}; }
 
 }  // namespace
 
@@ -176,7 +233,7 @@ moe_status moe_linear_forward(const moe_linear_config* c, const int32_t* offsets
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     LinPlan p = linear_plan(c->M, c->E, c->K, c->N, false);
-    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->N, p.stream ? 32 : 128}, {&p.big, c->N, 256}}, st))
+    if (lin_tiles(c->E, offsets, ws, L.lists, {{&p.small, c->N, p.stream ? 32 : 128}, {&p.big, c->N, 256}}, st))
         return MOE_ERR_HIP;
     const LinFwdArgs a{{}, c->dtype, c->act, c->N, c->K, (const uint16_t*)x, (const uint16_t*)w,
                        (const uint16_t*)bias, (const uint16_t*)residual, (uint16_t*)y, (uint16_t*)z, 1,
@@ -201,7 +258,7 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
     char* ws = (char*)workspace;
     LinPlan p = linear_plan(c->M, c->E, c->N, c->K, true);
     LinTiles strips{nullptr, nullptr, c->E, c->M, linear_dz_rows(c->M, c->E, c->N), nullptr};
-    if (lin_tiles(*c, offsets, ws, L, {{&p.small, c->K, 128}, {&p.big, c->K, 256}, {&strips, c->N, 512}}, st))
+    if (lin_tiles(c->E, offsets, ws, L.lists, {{&p.small, c->K, 128}, {&p.big, c->K, 256}, {&strips, c->N, 512}}, st))
         return MOE_ERR_HIP;
     uint16_t* dz = (uint16_t*)(ws + L.dz);
     float* part = db ? (float*)(ws + L.part) : nullptr;
@@ -212,6 +269,129 @@ moe_status moe_linear_backward(const moe_linear_config* c, const int32_t* offset
                        (float*)(ws + L.sums), 0, 0, 0};
     if (launch_linear_bwd(p, b, st)) return MOE_ERR_HIP;
     return MOE_OK;
+}
+
+moe_status moe_route_forward(const moe_config* cfg, const moe_route_config* route, const float* logits,
+                             const float* bias, const moe_sched* sched, float* scores, void* stream) {
+    RouteArgs a;
+    const moe_status s = route_args(cfg, route, logits, sched, a);
+    if (s != MOE_OK) return s;
+    if ((bias && !at(bias, 4)) || !at(sched->topk_w, 4) || (scores && !at(scores, 4))) return MOE_ERR_INVALID_ARG;
+    if (among(a.idx, {logits, bias, sched->topk_w, scores}) || among(sched->topk_w, {logits, bias, scores}) ||
+        among(scores, {logits, bias}))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    a.bias = bias;
+    a.w = sched->topk_w;
+    a.scores = scores;
+    return launch_route(a, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
+}
+
+moe_status moe_route_backward(const moe_config* cfg, const moe_route_config* route, const float* logits,
+                              const moe_sched* sched, const float* dw, const float* d_scores, float* d_logits,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    RouteArgs a;
+    const moe_status s = route_args(cfg, route, logits, sched, a);
+    if (s != MOE_OK) return s;
+    if (!at(workspace, 256) || workspace_bytes < 256) return MOE_ERR_WORKSPACE;
+    if (!at(dw, 4) || (d_scores && !at(d_scores, 4)) || !at(d_logits, 4) ||
+        among(d_logits, {logits, sched->topk_idx, dw, d_scores}))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    a.dw = dw;
+    a.d_scores = d_scores;
+    a.d_logits = d_logits;
+    a.err = (int32_t*)workspace;
+    return launch_route_bwd(a, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
+}
+
+moe_status moe_norm_workspace_size(const moe_norm_config* cfg, size_t* bytes) {
+    const moe_status s = norm_check(cfg);
+    if (s != MOE_OK) return s;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = norm_bytes(*cfg);
+    return MOE_OK;
+}
+
+moe_status moe_norm_forward(const moe_norm_config* c, const void* x, const void* residual, const void* gamma,
+                            const void* beta, void* y, void* total, float* mean, float* rstd, void* stream) {
+    const moe_status s = norm_check(c);
+    if (s != MOE_OK) return s;
+    const bool rms = c->kind == MOE_NORM_RMS;
+    if (!at(x, 16) || !at_or_null(residual) || !at(gamma, 16) || !at_or_null(beta) || !at(y, 16) ||
+        !at_or_null(total) || !residual != !total || (mean && !at(mean, 4)) || (rstd && !at(rstd, 4)) ||
+        (rms && (beta || mean)))
+        return MOE_ERR_INVALID_ARG;
+    if (among(y, {x, residual, gamma, beta, total, mean, rstd}) || among(total, {gamma, beta, mean, rstd}) ||
+        among(mean, {x, residual, gamma, beta, rstd}) || among(rstd, {x, residual, gamma, beta}))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    const NormArgs a{c->M, c->H, c->dtype, c->params, rms, c->eps, x, gamma, beta, residual, y, total, mean, rstd,
+                     nullptr, nullptr, nullptr, nullptr};
+    return launch_norm(a, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
+}
+
+moe_status moe_norm_backward(const moe_norm_config* c, const void* x, const void* gamma, const float* mean,
+                             const float* rstd, const void* dy, const void* d_total, void* dx, void* dgamma,
+                             void* dbeta, void* workspace, size_t workspace_bytes, void* stream) {
+    const moe_status s = norm_check(c);
+    if (s != MOE_OK) return s;
+    const bool rms = c->kind == MOE_NORM_RMS;
+    if (!at(workspace, 256) || workspace_bytes < norm_bytes(*c)) return MOE_ERR_WORKSPACE;
+    if (!at(x, 16) || !at(gamma, 16) || (rms ? mean != nullptr : !at(mean, 4)) || !at(rstd, 4) || !at(dy, 16) ||
+        !at_or_null(d_total) || (!dx && !dgamma && !dbeta) || !at_or_null(dx) || !at_or_null(dgamma) ||
+        !at_or_null(dbeta) || (rms && dbeta) || (d_total && !dx))
+        return MOE_ERR_INVALID_ARG;
+    if (among(dx, {x, gamma, mean, rstd, dgamma, dbeta}) || among(dgamma, {x, gamma, mean, rstd, dy, d_total, dbeta}) ||
+        among(dbeta, {x, gamma, mean, rstd, dy, d_total}))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    const NormArgs a{c->M, c->H, c->dtype, c->params, rms, c->eps, x, gamma, nullptr, d_total, dx, nullptr,
+                     const_cast<float*>(mean), const_cast<float*>(rstd), dy, dgamma, dbeta, (float*)workspace};
+    return launch_norm_bwd(a, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
+}
+
+moe_status moe_linear_w4_workspace_size(const moe_linear_w4_config* cfg, size_t* bytes) {
+    const moe_status s = w4_check(cfg);
+    if (s != MOE_OK) return s;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = w4_layout(*cfg).total;
+    return MOE_OK;
+}
+
+moe_status moe_linear_w4_forward(const moe_linear_w4_config* c, const int32_t* offsets, const void* x,
+                                 const void* codes, const void* scales, const void* zeros, const void* bias,
+                                 const void* residual, void* y, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    const moe_status s = w4_check(c);
+    if (s != MOE_OK) return s;
+    const W4Layout L = w4_layout(*c);
+    if (!at(workspace, 256) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if ((c->E > 0 ? !at(offsets, 4) : offsets != nullptr) || !at(x, 16) || !at(codes, 16) || !at(scales, 16) ||
+        !at_or_null(zeros) || !at_or_null(bias) || !at_or_null(residual) || !at(y, 16) ||
+        among(y, {offsets, x, codes, scales, zeros, bias}))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    hipStream_t st = (hipStream_t)stream;
+    LinTiles t = w4_tiles(c->M, c->E, c->K, c->N);
+    if (lin_tiles(c->E, offsets, (char*)workspace, &L.list, {{&t, c->N, w4_tile_columns(t)}}, st)) return MOE_ERR_HIP;
+    const W4Args a{{t, c->dtype, c->act, c->N, c->K, (const uint16_t*)x, nullptr, (const uint16_t*)bias,
+                    (const uint16_t*)residual, (uint16_t*)y, nullptr, 1, nullptr},
+                   (const uint8_t*)codes, (const uint16_t*)scales, (const uint8_t*)zeros, c->group};
+    return launch_w4(a, st) ? MOE_ERR_HIP : MOE_OK;
+}
+
+moe_status moe_linear_w4_quantize(const moe_linear_w4_config* c, const void* w, void* codes, void* scales,
+                                  void* zeros, void* stream) {
+    const moe_status s = w4_check(c);
+    if (s != MOE_OK) return s;
+    if (!at(w, 16) || !at(codes, 16) || !at(scales, 16) || !at_or_null(zeros) || among(codes, {w, scales, zeros}) ||
+        among(scales, {w, zeros}) || among(zeros, {w}))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
+    const W4QuantArgs a{(int64_t)(c->E ? c->E : 1) * c->N, c->N, c->K, c->group, c->dtype, (const uint16_t*)w,
+                        (uint8_t*)codes, (uint16_t*)scales, (uint8_t*)zeros};
+    return launch_w4_quant(a, (hipStream_t)stream) ? MOE_ERR_HIP : MOE_OK;
 }
 
 }  // extern "C"

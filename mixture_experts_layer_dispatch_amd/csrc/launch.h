@@ -459,6 +459,76 @@ int launch_linear_fwd(const LinPlan& p, const LinFwdArgs& a, hipStream_t st);
 int launch_linear_dz(const LinDzArgs& a, hipStream_t st);
 int launch_linear_bwd(const LinPlan& p, const LinBwdArgs& a, hipStream_t st);    // all that follows dz
 
+// ---------------------------------------------------------------- routing with scores, norm, 4-bit weights
+enum { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
+
+struct RouteArgs {
+    int T, E, k;
+    int score, n_group, topk_group, group_top;
+    bool renorm;
+    float scale;
+    const float* logits;      // [T, E]
+    const float* bias;        // [E] or null
+    int32_t* idx;             // [T, k]: written forward, read backward
+    float* w;                 // [T, k]
+    float* scores;            // [T, E] or null
+    const float* dw;          // [T, k]
+    const float* d_scores;    // [T, E] or null
+    float* d_logits;          // [T, E]
+    int32_t* err;
+};
+
+// route.hip
+int launch_route(const RouteArgs& a, hipStream_t st);
+int launch_route_bwd(const RouteArgs& a, hipStream_t st);
+
+struct NormArgs {
+    int M, H;
+    int dtype, params;        // 0 bf16, 1 fp16, 2 fp32; params: dtype or 2
+    bool rms;
+    float eps;
+    const void* x;            // [M, H]
+    const void* gamma;        // [H]
+    const void* beta;         // [H] or null
+    const void* residual;     // [M, H] or null; backward: the gradient of total
+    void* y;                  // [M, H]; backward: dx or null
+    void* total;              // [M, H] if residual
+    float* mean;              // [M] or null
+    float* rstd;              // [M] or null
+    const void* dy;           // [M, H]
+    void* dgamma;             // [H] or null
+    void* dbeta;              // [H] or null
+    float* part;              // [norm_parts, 2, H]
+};
+
+// norm.hip
+int norm_parts(int M, int H, int dtype);
+int launch_norm(const NormArgs& a, hipStream_t st);
+int launch_norm_bwd(const NormArgs& a, hipStream_t st);
+
+struct W4Args {
+    LinFwdArgs f;             // x, bias, residual, y; w and z null
+    const uint8_t* codes;     // [E, N, K / 2]
+    const uint16_t* scales;   // [E, K / G, N]
+    const uint8_t* zeros;     // as scales, or null: 8
+    int G;
+};
+
+struct W4QuantArgs {
+    int64_t rows;             // of all experts
+    int N, K, G, dtype;
+    const uint16_t* w;        // [rows, K]
+    uint8_t* codes;           // [rows, K / 2]
+    uint16_t* scales;         // [E, K / G, N]
+    uint8_t* zeros;           // as scales, or null
+};
+
+// linear_w4.hip
+LinTiles w4_tiles(int M, int E, int K, int N);
+int w4_tile_columns(const LinTiles& t);
+int launch_w4(const W4Args& a, hipStream_t st);
+int launch_w4_quant(const W4QuantArgs& a, hipStream_t st);
+
 // api.hip
 bool device_ok();             // the current device is gfx950
 

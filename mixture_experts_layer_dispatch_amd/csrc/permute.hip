@@ -24,17 +24,9 @@
 #include "dtype.h"
 #include "launch.h"
 #include "profile.h"
+#include "rows.h"
 
 namespace moe {
-
-// Launches of more than 2^22 blocks (2^30 threads) take a second grid
-// dimension: a dimension's threads are counted in 32 bits.
-constexpr int64_t kGridX = 1 << 22;
-static dim3 rows_grid(int64_t blocks) {
-    if (blocks <= kGridX) return dim3((unsigned)blocks);
-    return dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
-}
-__device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // Lane j < k of the wave holds the row of the token's slot j (-1: bad).
 __device__ __forceinline__ int slot_row(const int32_t* __restrict__ row_of_slot, int t, int k, int S, int lane,
@@ -46,30 +38,6 @@ __device__ __forceinline__ int slot_row(const int32_t* __restrict__ row_of_slot,
         else raise_err(err, ERR_BAD_ROW);
     }
     return row;
-}
-
-__device__ __forceinline__ int lane_value(int v, int j) { return __builtin_amdgcn_readlane(v, j); }
-__device__ __forceinline__ float lane_value(float v, int j) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
-}
-
-// ---------------------------------------------------------------- non-temporal accesses
-// The expert rows are read once: non-temporal loads (16384 tokens x 10 x 4096
-// bf16: unpermute 312 -> 291 us, permute backward 287 -> 256; 2048 tokens:
-// 38 -> 34, 35 -> 33).  Expert rows that are written are too many to be found
-// in a cache later and go past it (NT) once they are more than the 32 MB of the
-// L2s: 8192 tokens x 8 x 1024 (134 MB) permute 27.3 -> 24.2 us, unpermute
-// backward 56 -> 52; 16384 x 10 x 4096 (1.3 GB) 292 -> 298 and 585 -> 564.
-constexpr int64_t kCacheBytes = 32ll << 20;
-
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint4 ld_once(const uint4* p) {
-    return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4_t*)p));
-}
-template <bool NT>
-__device__ __forceinline__ void st_row(uint4* p, const uint4& v) {
-    if constexpr (NT) __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), (u32x4_t*)p);
-    else *p = v;
 }
 
 // ================================================================ permute

@@ -203,7 +203,11 @@ __global__ __launch_bounds__(64) void k_sched_scatter(const int32_t* __restrict_
             const int grow = m * g.Sm + row;
             row_of_slot[s] = grow;
             slot_of_row[grow] = s;
+        } else if (s < hi) {
+            row_of_slot[s] = -1;                                // an expert outside the layer: no row
         }
+        // the rows that such slots leave over at the macrobatch's end
+        if (s < hi && s - m * g.Sm >= off[g.E]) slot_of_row[s] = -1;
     }
 }
 
