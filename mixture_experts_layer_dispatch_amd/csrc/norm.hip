@@ -17,14 +17,11 @@
 namespace moe {
 
 // ---------------------------------------------------------------- sums of a row
-// A row is W waves; `s` holds a value per wave and row, for two sums at once.
+// A row is W waves; `s` holds a value per wave of the block, for two sums at once.
 template <int W>
 __device__ __forceinline__ f32x2 row_sums(f32x2 v, f32x2* s) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        v[0] += __shfl_xor(v[0], off);
-        v[1] += __shfl_xor(v[1], off);
-    }
+    v[0] = wave_total(v[0]);
+    v[1] = wave_total(v[1]);
     if constexpr (W > 1) {
         const int wv = wave_id(), first = wv / W * W;
         __syncthreads();                           // (what was there has been read)
@@ -144,20 +141,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_norm(NormArgs a) {
 }
 
 // ================================================================ backward
-// Block b goes over the rows b, b + parts, ...; a thread keeps its columns'
-// sums for dgamma and dbeta, which k_norm_params adds up block by block.
-template <class D, class P, int W, int NC>
-__global__ __launch_bounds__(64 * W) void k_norm_bwd(NormArgs a, int parts) {
-    constexpr int PER = D::PER16;
+// A block has RG rows at a time, W waves each (one, or the whole block), and
+// goes over the rows RG b, RG b + 1, ..., then RG (b + parts), ...  A thread keeps its
+// columns' sums for dgamma and dbeta over its rows; the block adds them up over its
+// rows in LDS and writes one part, which k_norm_params adds up block by block.
+template <class D, class P, int W, int NC, int RG>
+__global__ __launch_bounds__(64 * W * RG, 1) void k_norm_bwd(NormArgs a, int parts) {
+    constexpr int PER = D::PER16, Q = PER / 4;
     __shared__ f32x2 sums[W];
-    const int C = a.H / PER, c0 = threadIdx.x;
+    __shared__ f32x4 cols[RG > 1 ? RG : 1][RG > 1 ? 2 * Q : 1][64 * W];
+    const int C = a.H / PER, rg = wave_id() / W, c0 = wave_id() % W * 64 + lane_id();
     const bool params = a.dgamma || a.dbeta;
     float dg[NC][PER], db[NC][PER];
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int q = 0; q < PER; ++q) dg[i][q] = db[i][q] = 0.f;
-    for (int64_t row = blockIdx.x; row < a.M; row += parts) {
+    for (int64_t row = (int64_t)blockIdx.x * RG + rg; row < a.M; row += (int64_t)parts * RG) {
         const uint4* x = (const uint4*)a.x + row * C;
         const uint4* dy = (const uint4*)a.dy + row * C;
         uint4 xv[NC], gv[NC];
@@ -210,46 +210,139 @@ __global__ __launch_bounds__(64 * W) void k_norm_bwd(NormArgs a, int parts) {
         }
     }
     if (!params) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.H;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = c0 + i * 64 * W;
-        if (c >= C) continue;
-        float* p = a.part + (int64_t)blockIdx.x * 2 * a.H + c * PER;
+        f32x4 v[2 * Q];
 #pragma unroll
-        for (int q = 0; q < PER; q += 4) {
-            *(f32x4*)(p + q) = f32x4{dg[i][q], dg[i][q + 1], dg[i][q + 2], dg[i][q + 3]};
-            *(f32x4*)(p + a.H + q) = f32x4{db[i][q], db[i][q + 1], db[i][q + 2], db[i][q + 3]};
+        for (int q = 0; q < 2 * Q; ++q) {
+            const float* f = q < Q ? dg[i] + 4 * q : db[i] + 4 * (q - Q);
+            v[q] = f32x4{f[0], f[1], f[2], f[3]};
+        }
+        if constexpr (RG > 1) {
+            if (i > 0) __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 2 * Q; ++q) cols[rg][q][c0] = v[q];
+            __syncthreads();
+            // wave rg adds up quad rg
+            if (rg < 2 * Q && c < C) {
+                f32x4 t = cols[0][rg][c0];
+#pragma unroll
+                for (int g = 1; g < RG; ++g) t += cols[g][rg][c0];
+                *(f32x4*)(part + (rg < Q ? 0 : a.H) + c * PER + 4 * (rg % Q)) = t;
+            }
+        } else if (c < C) {
+#pragma unroll
+            for (int q = 0; q < 2 * Q; ++q) *(f32x4*)(part + (q < Q ? 0 : a.H) + c * PER + 4 * (q % Q)) = v[q];
         }
     }
 }
 
-// dgamma (y 0) and dbeta (y 1): the parts' sums in order, eight columns a thread
-template <class P>
-__global__ __launch_bounds__(64) void k_norm_params(NormArgs a, int parts) {
-    void* out = blockIdx.y ? a.dbeta : a.dgamma;
-    const int at = (blockIdx.x * 64 + threadIdx.x) * 8;
-    if (!out || at >= a.H) return;
-    float f[8] = {};
-    const float* p = a.part + blockIdx.y * a.H + at;
-    for (int b = 0; b < parts; ++b) {
-        const f32x4 lo = *(const f32x4*)(p + (int64_t)b * 2 * a.H), hi = *(const f32x4*)(p + (int64_t)b * 2 * a.H + 4);
+// Rows too long for a block's registers beside the sums for dgamma and dbeta: a
+// block per row reads it twice, the second time from the caches,
+template <class D, class P>
+__global__ __launch_bounds__(1024) void k_norm_bwd_long(NormArgs a) {
+    constexpr int PER = D::PER16, W = 16;
+    __shared__ f32x2 sums[W];
+    const int C = a.H / PER;
+    const int64_t row = block_number();
+    if (row >= a.M) return;
+    const uint4* x = (const uint4*)a.x + row * C;
+    const uint4* dy = (const uint4*)a.dy + row * C;
+    const float mean = a.mean ? a.mean[row] : 0.f, rstd = a.rstd[row];
+    f32x2 s = {0.f, 0.f};
+    for (int c = threadIdx.x; c < C; c += 64 * W) {
+        float f[PER], d[PER], g[PER];
+        D::unpack(x[c], f);
+        D::unpack(dy[c], d);
+        load_params<D, P>(a.gamma, c * PER, g);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            f[q] += lo[q];
-            f[4 + q] += hi[q];
+        for (int q = 0; q < PER; ++q) {
+            const float w = d[q] * g[q];
+            s[0] += w;
+            s[1] = fmaf(w, (f[q] - mean) * rstd, s[1]);
         }
     }
-    if constexpr (P::PER16 == 8) {
-        store_params<P, P>(out, at, f);
-    } else {
-        store_params<P, P>(out, at, f);
-        store_params<P, P>(out, at + 4, f + 4);
+    s = row_sums<W>(s, sums);
+    const float mg = a.rms ? 0.f : s[0] / a.H, mx = s[1] / a.H;
+    uint4* dx = (uint4*)a.y + row * C;
+    const uint4* skip = (const uint4*)a.residual + row * C;
+    for (int c = threadIdx.x; c < C; c += 64 * W) {
+        float f[PER], d[PER], g[PER], r[PER];
+        D::unpack(x[c], f);
+        D::unpack(dy[c], d);
+        load_params<D, P>(a.gamma, c * PER, g);
+        if (a.residual) D::unpack(skip[c], r);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            f[q] = rstd * (d[q] * g[q] - mg - (f[q] - mean) * rstd * mx);
+            if (a.residual) f[q] += r[q];
+        }
+        dx[c] = D::pack(f);
     }
+}
+
+// and the sums over the rows have blocks of their own (before dx, which may be dy):
+// 64 chunks of columns, four waves that share the part's rows.
+template <class D>
+__global__ __launch_bounds__(256) void k_norm_cols(NormArgs a, int parts) {
+    constexpr int PER = D::PER16, Q = PER / 4;
+    __shared__ f32x4 cols[4][2 * Q][64];
+    const int C = a.H / PER, c = blockIdx.x * 64 + lane_id(), wv = wave_id();
+    float dg[PER] = {}, db[PER] = {};
+    if (c < C)
+        for (int64_t row = (int64_t)blockIdx.y * 4 + wv; row < a.M; row += (int64_t)parts * 4) {
+            const float mean = a.mean ? a.mean[row] : 0.f, rstd = a.rstd[row];
+            float f[PER], d[PER];
+            D::unpack(((const uint4*)a.x)[row * C + c], f);
+            D::unpack(((const uint4*)a.dy)[row * C + c], d);
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                dg[q] = fmaf(d[q], (f[q] - mean) * rstd, dg[q]);
+                db[q] += d[q];
+            }
+        }
+#pragma unroll
+    for (int q = 0; q < 2 * Q; ++q) {
+        const float* f = q < Q ? dg + 4 * q : db + 4 * (q - Q);
+        cols[wv][q][lane_id()] = f32x4{f[0], f[1], f[2], f[3]};
+    }
+    __syncthreads();
+    if (wv >= 2 * Q || c >= C) return;
+    f32x4 t = cols[0][wv][lane_id()];
+#pragma unroll
+    for (int g = 1; g < 4; ++g) t += cols[g][wv][lane_id()];
+    float* part = a.part + (int64_t)blockIdx.y * 2 * a.H;
+    *(f32x4*)(part + (wv < Q ? 0 : a.H) + c * PER + 4 * (wv % Q)) = t;
+}
+
+// dgamma (y 0) and dbeta (y 1): a block's 16 quarters of columns, four each, over 64
+// slices of the parts, whose sums are added in order.
+template <class P>
+__global__ __launch_bounds__(1024) void k_norm_params(NormArgs a, int parts) {
+    __shared__ f32x4 sums[64][16];
+    void* out = blockIdx.y ? a.dbeta : a.dgamma;
+    if (!out) return;
+    const int col = (blockIdx.x * 16 + (threadIdx.x & 15)) * 4, sl = threadIdx.x >> 4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (col < a.H) {
+        const float* p = a.part + (int64_t)blockIdx.y * a.H + col;
+#pragma unroll 4
+        for (int b = sl; b < parts; b += 64) v += *(const f32x4*)(p + (int64_t)b * 2 * a.H);
+    }
+    sums[sl][threadIdx.x & 15] = v;
+    __syncthreads();
+    if (threadIdx.x >= 16 || col >= a.H) return;
+    for (int q = 1; q < min(parts, 64); ++q) v += sums[q][threadIdx.x];
+    if constexpr (P::PER16 == 4) *(f32x4*)((float*)out + col) = v;
+    else *(uint2*)((uint16_t*)out + col) = make_uint2(P::pack2(v[0], v[1]), P::pack2(v[2], v[3]));
 }
 
 // ================================================================ launchers
-// (rows of at most 2^16 elements: 2^14 chunks of fp32, 16 to a thread of 1024)
-template <class F>
+// The forward's rows: f(W, NC).  (Rows of at most 2^16 elements: 2^13 chunks of
+// 16 bits, 2^14 of fp32.)
+template <class D, class F>
 static int with_shape(int C, const F& f) {
     using std::integral_constant;
     if (C <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
@@ -257,7 +350,9 @@ static int with_shape(int C, const F& f) {
     if (C <= 512) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
     if (C <= 1024) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
     if (C <= 4096) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-    return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    if constexpr (D::PER16 == 4)
+        if (C > 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
 }
 
 template <class F>
@@ -267,8 +362,26 @@ static int with_types(int dtype, int params, const F& f) {
     return params == 0 ? f(Bf16{}, Bf16{}) : f(Bf16{}, Fp32{});
 }
 
+// The backward's rows: up to 512 chunks in a wave, eight rows to a block, up to
+// 2048 a block each, f(W, NC, RG); longer ones go over memory twice, f(0, 0, 1)
+template <class F>
+static int with_bwd_shape(int C, const F& g) {
+    using std::integral_constant;
+    if (C <= 64) return g(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 8>{});
+    if (C <= 128) return g(integral_constant<int, 1>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
+    if (C <= 256) return g(integral_constant<int, 1>{}, integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    if (C <= 512) return g(integral_constant<int, 1>{}, integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (C <= 1024) return g(integral_constant<int, 8>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
+    if (C <= 2048) return g(integral_constant<int, 8>{}, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    return g(integral_constant<int, 0>{}, integral_constant<int, 0>{}, integral_constant<int, 1>{});
+}
+
 int norm_parts(int M, int H, int dtype) {
-    return M < 1024 ? M : 1024;
+    return with_bwd_shape(H / (dtype == 2 ? 4 : 8), [&](auto w, auto n, auto rg) {
+        constexpr int RG = decltype(rg)::value, most = RG > 1 ? 256 : decltype(w)::value ? 512 : 64;
+        const int blocks = (M + RG - 1) / RG;
+        return blocks < most ? blocks : most;
+    });
 }
 
 int launch_norm(const NormArgs& a, hipStream_t st) {
@@ -276,7 +389,7 @@ int launch_norm(const NormArgs& a, hipStream_t st) {
     return with_types(a.dtype, a.params, [&](auto d, auto p) {
         using D = decltype(d);
         using P = decltype(p);
-        return with_shape(a.H / D::PER16, [&](auto w, auto n) {
+        return with_shape<D>(a.H / D::PER16, [&](auto w, auto n) {
             constexpr int W = decltype(w)::value, RB = W == 1 ? 4 : 1;
             constexpr int threads = W == 1 ? 256 : 64 * W;
             k_norm<D, P, W, decltype(n)::value><<<rows_grid(((int64_t)a.M + RB - 1) / RB, threads), threads, 0, st>>>(a);
@@ -292,19 +405,25 @@ int launch_norm_bwd(const NormArgs& a, hipStream_t st) {
         const int r = with_types(a.dtype, a.params, [&](auto d, auto p) {
             using D = decltype(d);
             using P = decltype(p);
-            return with_shape(a.H / D::PER16, [&](auto w, auto n) {
-                constexpr int W = decltype(w)::value;
-                k_norm_bwd<D, P, W, decltype(n)::value><<<parts, 64 * W, 0, st>>>(a, parts);
+            return with_bwd_shape(a.H / D::PER16, [&](auto w, auto n, auto rg) {
+                constexpr int W = decltype(w)::value, RG = decltype(rg)::value;
+                if constexpr (W > 0) {
+                    k_norm_bwd<D, P, W, decltype(n)::value, RG><<<parts, 64 * W * RG, 0, st>>>(a, parts);
+                } else {
+                    if (a.dgamma || a.dbeta)
+                        k_norm_cols<D><<<dim3((a.H / D::PER16 + 63) / 64, parts), 256, 0, st>>>(a, parts);
+                    if (a.y) k_norm_bwd_long<D, P><<<rows_grid(a.M, 1024), 1024, 0, st>>>(a);
+                }
                 return hipGetLastError() == hipSuccess ? 0 : -1;
             });
         });
         if (r || (!a.dgamma && !a.dbeta)) return r;
     }
     ProfScope prof_(st, "norm_params");
-    const dim3 grid((a.H + 511) / 512, 2);
-    if (a.params == 2) k_norm_params<Fp32><<<grid, 64, 0, st>>>(a, parts);
-    else if (a.params == 1) k_norm_params<Fp16><<<grid, 64, 0, st>>>(a, parts);
-    else k_norm_params<Bf16><<<grid, 64, 0, st>>>(a, parts);
+    const dim3 grid((a.H + 63) / 64, 2);
+    if (a.params == 2) k_norm_params<Fp32><<<grid, 1024, 0, st>>>(a, parts);
+    else if (a.params == 1) k_norm_params<Fp16><<<grid, 1024, 0, st>>>(a, parts);
+    else k_norm_params<Bf16><<<grid, 1024, 0, st>>>(a, parts);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -11,16 +11,6 @@
 namespace moe {
 
 // ---------------------------------------------------------------- wave reductions
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-    return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-    return v;
-}
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
@@ -75,7 +65,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L) {
     const bool by_logit = !a.bias && !two;
     double key[EPL];
     double z = 0.0;
-    m = wave_max(m);
+    m = wave_most(m);
     if (softmax) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
@@ -212,7 +202,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
             }
         }
         if (softmax) {
-            m = wave_max(m);
+            m = wave_most(m);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -226,20 +216,20 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
     const float rz = z > 0.f ? 1.f / z : 0.f;
     float p = 0.f;
     if (a.renorm) {
-        const float ml = wave_max(l);
+        const float ml = wave_most(l);
         if (softmax) p = soft_exp(l, ml);
         else if (l != -INFINITY) {
             const float c = fminf(ml, 0.f);
             p = l < 0.f ? expf(l - c) / (1.f + expf(l)) : expf(-c) / (1.f + expf(-l));
         }
-        const float sum = wave_sum(p);
+        const float sum = wave_total(p);
         p = sum > 0.f ? p / sum : 0.f;
-        p = a.scale * p * (dw - wave_sum(p * dw));
+        p = a.scale * p * (dw - wave_total(p * dw));
     } else {
         p = a.scale * dw * (softmax ? soft_exp(l, m) * rz : 1.f / (1.f + expf(-l)));
     }
     if (e < 0) p = 0.f;
-    float dot = softmax && !a.renorm ? wave_sum(p) : 0.f;
+    float dot = softmax && !a.renorm ? wave_total(p) : 0.f;
     if (!softmax) p *= 1.f / (1.f + expf(l));
     if (softmax && a.d_scores) {
         float d = 0.f;
@@ -247,7 +237,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int q = 0; q < V; ++q) d = fmaf(g[i][q], s[i][q] * rz, d);
-        dot += wave_sum(d);
+        dot += wave_total(d);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {

@@ -20,6 +20,30 @@ __device__ __forceinline__ float lane_value(float v, int j) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
 }
 
+// ---------------------------------------------------------------- over a wave
+// In a fixed order, without the LDS: within rows of 16 lanes by shifts, then
+// across them; lane 63 has the result.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or(float v, float other) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(other), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+template <class F>
+__device__ __forceinline__ float wave_fold(float v, float none, const F& f) {
+    v = f(v, dpp_or<0x111, 0xf>(v, none));         // from the lane 1, 2, 4, 8 below
+    v = f(v, dpp_or<0x112, 0xf>(v, none));
+    v = f(v, dpp_or<0x114, 0xf>(v, none));
+    v = f(v, dpp_or<0x118, 0xf>(v, none));
+    v = f(v, dpp_or<0x142, 0xa>(v, none));         // lane 15 of the row below into rows 1 and 3
+    v = f(v, dpp_or<0x143, 0xc>(v, none));         // lane 31 into rows 2 and 3
+    return lane_value(v, 63);
+}
+__device__ __forceinline__ float wave_total(float v) {
+    return wave_fold(v, 0.f, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float wave_most(float v) {
+    return wave_fold(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+}
+
 // ---------------------------------------------------------------- non-temporal accesses
 // The expert rows are read once: non-temporal loads (16384 tokens x 10 x 4096
 // bf16: unpermute 312 -> 291 us, permute backward 287 -> 256; 2048 tokens:
