@@ -16,6 +16,7 @@
 #include "linear_common.h"
 #include "profile.h"
 #include "rows.h"
+#include "tile256.h"
 
 namespace moe {
 
@@ -43,18 +44,35 @@ __device__ __forceinline__ void transpose_quarters(uint4& v) {
     swap16(v.z, v.w);
 }
 
-// Eight codes (low nibble first) minus zero, as a fragment of D.
+// Eight codes (low nibble first) minus zero, as a fragment of D.  A byte of 0 .. 15
+// is an E4M3 number of that many times 2^-9 (subnormal or of the smallest exponent),
+// so one conversion makes two codes fp32.
 template <class D>
 __device__ __forceinline__ uint4 codes8(uint32_t w, float zero) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)(w >> (4 * i) & 15u) - zero;
-    return D::pack(f);
+    const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+    const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)even, 512.f, false);
+    const f32x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)even, 512.f, true);
+    const f32x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)odd, 512.f, false);
+    const f32x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)odd, 512.f, true);
+    return make_uint4(D::pack2(e0[0] - zero, o0[0] - zero), D::pack2(e0[1] - zero, o0[1] - zero),
+                      D::pack2(e1[0] - zero, o1[0] - zero), D::pack2(e1[1] - zero, o1[1] - zero));
+}
+
+// four consecutive outputs from col, the activation chosen at run time
+template <class D>
+__device__ __forceinline__ void w4_out(const LinFwdArgs& f, int e, int row, int col, const f32x4& v) {
+    switch (f.act) {
+        case LIN_RELU: return lin_out<D, LIN_RELU>(f, e, row, col, v);
+        case LIN_GELU: return lin_out<D, LIN_GELU>(f, e, row, col, v);
+        case LIN_GELU_TANH: return lin_out<D, LIN_GELU_TANH>(f, e, row, col, v);
+        case LIN_SILU: return lin_out<D, LIN_SILU>(f, e, row, col, v);
+        default: return lin_out<D, LIN_NONE>(f, e, row, col, v);
+    }
 }
 
 // ================================================================ few rows
 // 16 rows by 16 columns a block, its W waves split the reduction in units of 128.
-template <class D, int ACT, int G, int W>
+template <class D, int G, int W>
 __global__ __launch_bounds__(64 * W) void k_w4_stream(W4Args a) {
     __shared__ __attribute__((aligned(16))) float sums[W][16][20];
     const LinFwdArgs& f = a.f;
@@ -97,7 +115,132 @@ __global__ __launch_bounds__(64 * W) void k_w4_stream(W4Args a) {
     f32x4 v = *(const f32x4*)&sums[0][r][c];
 #pragma unroll
     for (int p = 1; p < W; ++p) v += *(const f32x4*)&sums[p][r][c];
-    if (lo + r < hi && nt * 16 + c < f.N) lin_out<D, ACT>(f, e, lo + r, nt * 16 + c, v);
+    if (lo + r < hi && nt * 16 + c < f.N) w4_out<D>(f, e, lo + r, nt * 16 + c, v);
+}
+
+// ================================================================ tiles
+// 16 MB rows by 64 NW columns, a wave all the rows of 64 columns: each weight is
+// taken apart once per row tile.  x goes through a ring of three LDS stages of 128
+// inputs, copied two steps ahead (in two arrays of 64 each; arrays of their own, so
+// that reads wait for no copies in flight), the codes two steps ahead into
+// registers.  Lane j of a quarter has the columns 4 j .. 4 j + 3 of its wave's 64, one
+// to an MFMA, so that scales come and outputs go as four neighbours.
+template <int MB>
+struct W4Ring {
+    uint16_t* h[3][2];
+};
+
+template <class D, int G, int MB, int NW>
+struct W4Loop {
+    static constexpr int NG = 128 / G, KS = G / 32, NC = 2 * MB * 16 * 8 / (64 * NW);
+    const W4Args& a;
+    const TileOperand<false, 16 * MB, 1, 64 * NW>& x;
+    const W4Ring<MB>& ring;
+    const uint8_t* codes[4];      // of the lane's four rows, its quarter's 16 bytes
+    const uint16_t* scales;       // of its four columns
+    const uint8_t* zeros;
+    int steps, lane;
+    f32x4 acc[MB][4];             // [rows 16 mb + 4 q + r][column 4 j + nb], r in the vector
+    uint4 w[3][4];
+    uint2 sc[3][NG];
+    uint32_t zr[3][NG];
+
+    __device__ __forceinline__ void load(int s, int buf) {
+        const int K = a.f.K, q = lane >> 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int kt = 2 * s + h;
+            if (kt < K / 64) x.copy(0, kt, ring.h[buf][h]);
+            else if (kt == K / 64 && K % 64) x.copy_tail(0, kt, K % 64, ring.h[buf][h]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const int at = min(s * 128 + 32 * q, K - 32) / 2;      // (behind the row: not used)
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) w[buf][nb] = *(const uint4*)(codes[nb] + at);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int64_t row = (int64_t)min(s * NG + g, K / G - 1) * a.f.N;
+            sc[buf][g] = *(const uint2*)(scales + row);
+            zr[buf][g] = zeros ? *(const uint32_t*)(zeros + row) : 0x08080808u;
+        }
+        t2_fence();
+    }
+    template <int BUF>
+    __device__ __forceinline__ void step(int s) {
+        const int left = steps - 1 - s, K = a.f.K;
+        if (left > 1 || (left == 1 && K % 128 == 0)) t2_wait<NC + 8>();
+        else t2_wait<0>();
+        t2_barrier();
+        if (left >= 2) load(s + 2, (BUF + 2) % 3);
+        const int ksteps = min(4, (K - s * 128) / 32);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) transpose_quarters(w[BUF][nb]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (g * KS >= ksteps) break;
+            uint4 b[KS][4];
+            const f32x4 scale = unpack4<D>(sc[BUF][g]);
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                const float zero = (float)(zr[BUF][g] >> (8 * nb) & 255u);
+                const uint32_t c[4] = {w[BUF][nb].x, w[BUF][nb].y, w[BUF][nb].z, w[BUF][nb].w};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) b[ks][nb] = codes8<D>(c[g * KS + ks], zero);
+            }
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                f32x4 part[4];
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const int k = g * KS + ks;
+                    const uint4 fx = t2_frag<false>(ring.h[BUF][k >> 1], 16 * mb, 32 * (k & 1));
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb)
+                        part[nb] = D::mfma(fx, b[ks][nb], ks ? part[nb] : f32x4{0.f, 0.f, 0.f, 0.f});
+                }
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[mb][nb][r] = fmaf(scale[nb], part[nb][r], acc[mb][nb][r]);
+            }
+        }
+    }
+};
+
+template <class D, int G, int MB, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_w4_tile(W4Args a) {
+    constexpr int TM = 16 * MB, TN = 64 * NW;
+    __shared__ __attribute__((aligned(16))) uint16_t s00[TM * 64], s01[TM * 64], s10[TM * 64], s11[TM * 64],
+        s20[TM * 64], s21[TM * 64];
+    const LinFwdArgs& f = a.f;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<TM, 1>(f.t, (f.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
+    const W4Ring<MB> ring{{{s00, s01}, {s10, s11}, {s20, s21}}};
+    const TileOperand<false, TM, 1, 64 * NW> x(f.x, f.K, lo, hi);
+    const int lane = lane_id(), col = nt * TN + 64 * wave_id() + 4 * (lane & 15), colc = min(col, f.N - 4);
+    const int64_t ge = (int64_t)e * (f.K / G) * f.N + colc;
+    W4Loop<D, G, MB, NW> l{a, x, ring, {}, a.scales + ge, a.zeros ? a.zeros + ge : nullptr, (f.K + 127) / 128, lane};
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+        l.codes[nb] = a.codes + ((int64_t)e * f.N + colc + nb) * (f.K / 2);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) l.acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    l.load(0, 0);
+    if (l.steps > 1) l.load(1, 1);
+    for (int s = 0; s < l.steps; s += 3) {
+        l.template step<0>(s);
+        if (s + 1 < l.steps) l.template step<1>(s + 1);
+        if (s + 2 < l.steps) l.template step<2>(s + 2);
+    }
+    if (col >= f.N) return;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = lo + 16 * mb + 4 * (lane >> 4) + r;
+            if (row < hi) w4_out<D>(f, e, row, col, f32x4{l.acc[mb][0][r], l.acc[mb][1][r], l.acc[mb][2][r], l.acc[mb][3][r]});
+        }
 }
 
 // ================================================================ quantiser
@@ -146,15 +289,18 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a, int64_t total) 
 }
 
 // ================================================================ launchers
-LinTiles w4_tiles(int M, int E, int K, int N) { return {nullptr, nullptr, E, M, 16, nullptr}; }
+LinTiles w4_tiles(int M, int E, int K, int N) {
+    const int tm = (E ? M <= 8LL * E : M <= 16) ? 16 : 64;
+    return {nullptr, nullptr, E, M, tm, nullptr};
+}
 
-int w4_tile_columns(const LinTiles& t) { return 16; }
+int w4_tile_columns(const LinTiles& t) { return t.tm == 16 ? 16 : 256; }
 
 template <class D, int G>
 static int w4_(const W4Args& a, hipStream_t st) {
-    return with_act(a.f.act, [&](auto A) {
-        return go(k_w4_stream<D, A(), G, 8>, max_tiles(a.f.t) * ((a.f.N + 15) / 16), 512, a, st);
-    });
+    const int64_t grid = max_tiles(a.f.t) * ((a.f.N + w4_tile_columns(a.f.t) - 1) / w4_tile_columns(a.f.t));
+    if (a.f.t.tm == 16) return go(k_w4_stream<D, G, 8>, grid, 512, a, st);
+    return go(k_w4_tile<D, G, 4, 4>, grid, 256, a, st);
 }
 
 template <class F>
