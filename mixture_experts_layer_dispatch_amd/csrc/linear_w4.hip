@@ -44,18 +44,41 @@ __device__ __forceinline__ void transpose_quarters(uint4& v) {
     swap16(v.z, v.w);
 }
 
-// Eight codes (low nibble first) minus zero, as a fragment of D.  A byte of 0 .. 15
-// is an E4M3 number of that many times 2^-9 (subnormal or of the smallest exponent),
-// so one conversion makes two codes fp32.
+// Eight codes (low nibble first) as they are, 0 .. 15, as a fragment of D.  A byte of
+// 0 .. 15 is an E4M3 number of that many times 2^-9 (subnormal or of the smallest
+// exponent), so one conversion makes two codes.
+template <class D>
+__device__ __forceinline__ uint4 codes8(uint32_t w) {
+    const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+    const int lo = (int)__builtin_amdgcn_perm(odd, even, 0x05010400u);
+    const int hi = (int)__builtin_amdgcn_perm(odd, even, 0x07030602u);
+    auto two = [](int v, auto upper) {
+        if constexpr (std::is_same<D, Bf16>::value)
+            return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, decltype(upper)::value));
+        else
+            return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.f, decltype(upper)::value));
+    };
+    return make_uint4(two(lo, std::false_type{}), two(lo, std::true_type{}), two(hi, std::false_type{}),
+                      two(hi, std::true_type{}));
+}
+
+// The same minus zero, exactly: fp16 by pairs, bf16 by way of fp32.
 template <class D>
 __device__ __forceinline__ uint4 codes8(uint32_t w, float zero) {
-    const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
-    const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)even, 512.f, false);
-    const f32x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)even, 512.f, true);
-    const f32x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)odd, 512.f, false);
-    const f32x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)odd, 512.f, true);
-    return make_uint4(D::pack2(e0[0] - zero, o0[0] - zero), D::pack2(e0[1] - zero, o0[1] - zero),
-                      D::pack2(e1[0] - zero, o1[0] - zero), D::pack2(e1[1] - zero, o1[1] - zero));
+    if constexpr (std::is_same<D, Fp16>::value) {
+        const uint4 v = codes8<D>(w);
+        const f16x2 z = {(_Float16)zero, (_Float16)zero};
+        auto sub = [&](uint32_t p) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) - z); };
+        return make_uint4(sub(v.x), sub(v.y), sub(v.z), sub(v.w));
+    } else {
+        const int even = (int)(w & 0x0f0f0f0fu), odd = (int)(w >> 4 & 0x0f0f0f0fu);
+        const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(even, 512.f, false);
+        const f32x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(even, 512.f, true);
+        const f32x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(odd, 512.f, false);
+        const f32x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(odd, 512.f, true);
+        return make_uint4(D::pack2(e0[0] - zero, o0[0] - zero), D::pack2(e0[1] - zero, o0[1] - zero),
+                          D::pack2(e1[0] - zero, o1[0] - zero), D::pack2(e1[1] - zero, o1[1] - zero));
+    }
 }
 
 // four consecutive outputs from col, the activation chosen at run time
@@ -67,6 +90,18 @@ __device__ __forceinline__ void w4_out(const LinFwdArgs& f, int e, int row, int 
         case LIN_GELU_TANH: return lin_out<D, LIN_GELU_TANH>(f, e, row, col, v);
         case LIN_SILU: return lin_out<D, LIN_SILU>(f, e, row, col, v);
         default: return lin_out<D, LIN_NONE>(f, e, row, col, v);
+    }
+}
+
+// f with the activation as a type
+template <class F>
+__device__ __forceinline__ void dev_act(int act, const F& f) {
+    switch (act) {
+        case LIN_RELU: f(std::integral_constant<int, LIN_RELU>{}); break;
+        case LIN_GELU: f(std::integral_constant<int, LIN_GELU>{}); break;
+        case LIN_GELU_TANH: f(std::integral_constant<int, LIN_GELU_TANH>{}); break;
+        case LIN_SILU: f(std::integral_constant<int, LIN_SILU>{}); break;
+        default: f(std::integral_constant<int, LIN_NONE>{});
     }
 }
 
@@ -119,128 +154,328 @@ __global__ __launch_bounds__(64 * W) void k_w4_stream(W4Args a) {
 }
 
 // ================================================================ tiles
-// 16 MB rows by 64 NW columns, a wave all the rows of 64 columns: each weight is
-// taken apart once per row tile.  x goes through a ring of three LDS stages of 128
-// inputs, copied two steps ahead (in two arrays of 64 each; arrays of their own, so
-// that reads wait for no copies in flight), the codes two steps ahead into
-// registers.  Lane j of a quarter has the columns 4 j .. 4 j + 3 of its wave's 64, one
-// to an MFMA, so that scales come and outputs go as four neighbours.
-template <int MB>
-struct W4Ring {
-    uint16_t* h[3][2];
-};
+// 64 rows by 512 columns, eight waves with all the rows of 64 columns each (2 x 2 MFMAs
+// of 32 x 32), so that each weight is taken apart once per row tile; steps of 128
+// inputs.  Lane j of a half wave has the columns 2 j and 2 j + 1 of its wave's 64, one to
+// an MFMA.  A pair of MFMA steps, 32 inputs (number c), takes the 16-byte chunk c of a
+// weight row: lane half h its words 2 h and 2 h + 1, one to a step, and of x the same
+// inputs.
+//
+// All operands are copied into LDS, two steps ahead and never drained: x in three
+// stages that the block shares, a wave's codes in three and its scales and zeros in two
+// stages of its own (what a wave copies, only it reads: no barrier).  The stages are
+// arrays of their own, since a read waits for the copies in flight into its array.  A
+// load into registers in the loop would wait for every copy before it.
+//
+// MID: the MFMAs multiply the codes themselves, and their sums start at -8 times the
+// sum of x over the group, which each wave computes for the eight rows that it copied,
+// one step ahead (bf16 codes minus 8 take twice the instructions).
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <class D, int G, int MB, int NW>
+template <class D>
+__device__ __forceinline__ f32x16 mfma32(const uint4& x, const uint4& w, const f32x16& c) {
+    if constexpr (std::is_same<D, Bf16>::value)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, w), c, 0, 0, 0);
+}
+
+// SIZE bytes a lane (16 or 4) to the wave's part of an LDS array, lane by lane; the
+// address a scalar and a 32-bit offset
+template <int SIZE>
+__device__ __forceinline__ void copy_lds(const char* base, uint32_t o, void* dst) {
+    asm volatile("" : "+v"(o));
+    if constexpr (SIZE == 16) __builtin_amdgcn_global_load_lds((glb_void_t*)(base + o), (lds_void_t*)dst, 16, 0, 0);
+    else __builtin_amdgcn_global_load_lds((glb_void_t*)(base + o), (lds_void_t*)dst, 4, 0, 0);
+}
+
+constexpr int kW4Waves = 8, kW4Cols = 64 * kW4Waves;
+
+// what is taken off the codes: 8, by the sums of x; 8, exactly; zeros, exactly
+enum { W4_MID, W4_EIGHT, W4_ZEROS };
+
+template <class D, int G, int MODE>
 struct W4Loop {
-    static constexpr int NG = 128 / G, KS = G / 32, NC = 2 * MB * 16 * 8 / (64 * NW);
-    const W4Args& a;
-    const TileOperand<false, 16 * MB, 1, 64 * NW>& x;
-    const W4Ring<MB>& ring;
-    const uint8_t* codes[4];      // of the lane's four rows, its quarter's 16 bytes
-    const uint16_t* scales;       // of its four columns
-    const uint8_t* zeros;
-    int steps, lane;
-    f32x4 acc[MB][4];             // [rows 16 mb + 4 q + r][column 4 j + nb], r in the vector
-    uint4 w[3][4];
-    uint2 sc[3][NG];
-    uint32_t zr[3][NG];
+    static constexpr bool MID = MODE == W4_MID;
+    static constexpr int NG = 128 / G, PER = G / 16;      // groups of a step, MFMA steps of a group
+    static constexpr bool ZEROS = MODE == W4_ZEROS;
+    static constexpr int SC = (NG + 1) / 2;               // copies of scales, two groups each
+    static constexpr int NS = SC + ZEROS;                 // and with that of zeros
+    int K, N, last, lane;
+    uint16_t* xs[3];              // [half of 64 inputs][64 rows]
+    uint8_t* ws[3];               // the wave's 4 KB of a stage
+    uint8_t* ss[2];               // its 256 NS bytes: [group][column 2 j + n] scales, [group][column] zeros
+    float* sums;                  // [2][NG][64] MID: -8 times the sums of x
+    const char *x, *codes, *scales, *zeros;               // of the tile's first row, of its expert and first column
+    uint32_t xo, xk;              // the thread's row and chunk of x, the chunk's first input in 64
+    uint32_t co[4], ck;           // its rows and its chunk of codes, the chunk's place in 64 bytes
+    uint32_t so, zo;              // its two columns, the four whose zeros it copies
+    uint32_t at[2];               // its columns' first words in a stage
+    f32x16 acc[2][2];             // [rows 32 m + 8 (r / 4) + 4 h + r % 4][column 2 j + n]
 
-    __device__ __forceinline__ void load(int s, int buf) {
-        const int K = a.f.K, q = lane >> 4;
+    // Steps behind the last are the last one again, so that every step has the same copies
+    // in flight; inputs behind the rows are their last ones again, and their groups are
+    // not added.
+    __device__ __forceinline__ void load_x(int s, int buf) {
+        s = min(s, last - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int kt = 2 * s + h;
-            if (kt < K / 64) x.copy(0, kt, ring.h[buf][h]);
-            else if (kt == K / 64 && K % 64) x.copy_tail(0, kt, K % 64, ring.h[buf][h]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        const int at = min(s * 128 + 32 * q, K - 32) / 2;      // (behind the row: not used)
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) w[buf][nb] = *(const uint4*)(codes[nb] + at);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int64_t row = (int64_t)min(s * NG + g, K / G - 1) * a.f.N;
-            sc[buf][g] = *(const uint2*)(scales + row);
-            zr[buf][g] = zeros ? *(const uint32_t*)(zeros + row) : 0x08080808u;
+            const int k0 = min(s * 128 + 64 * h, (K - 1) / 64 * 64);
+            uint32_t back = 0;                                 // (at most the chunk's place in the row)
+            if (G < 128 && k0 + 64 > K) back = (uint32_t)max(k0 + (int)xk + 8 - K, 0) * 2;
+            copy_lds<16>(x + (int64_t)k0 * 2, xo - back, xs[buf] + h * 4096 + wave_id() * 512);
         }
         t2_fence();
     }
-    template <int BUF>
-    __device__ __forceinline__ void step(int s) {
-        const int left = steps - 1 - s, K = a.f.K;
-        if (left > 1 || (left == 1 && K % 128 == 0)) t2_wait<NC + 8>();
-        else t2_wait<0>();
-        t2_barrier();
-        if (left >= 2) load(s + 2, (BUF + 2) % 3);
-        const int ksteps = min(4, (K - s * 128) / 32);
+    __device__ __forceinline__ void load_codes(int s, int buf) {
+        s = min(s, last - 1);
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) transpose_quarters(w[BUF][nb]);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t back = 0;
+            if (G < 128 && s * 128 + 128 > K) back = (uint32_t)max(s * 64 + (int)ck + 16 - K / 2, 0);   // (at most ck)
+            copy_lds<16>(codes + s * 64, co[i] - back, ws[buf] + i * 1024);
+        }
+        t2_fence();
+    }
+    __device__ __forceinline__ void load_scales(int s, int buf) {
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {                         // lane half h: group 2 i + h
+            const int row = min(s * NG + min(2 * i + (lane >> 5), NG - 1), K / G - 1);
+            copy_lds<4>(scales, ((uint32_t)row * N + so) * 2, ss[buf] + i * 256);
+        }
+        if (ZEROS) {                                           // lane quarter q: group q
+            const int row = min(s * NG + min(lane >> 4, NG - 1), K / G - 1);
+            copy_lds<4>(zeros, (uint32_t)row * N + zo, ss[buf] + SC * 256);
+        }
+        t2_fence();
+    }
+    // sums(s) of the wave's eight rows, which its own copies have brought
+    __device__ __forceinline__ void put_sums(int xb, int buf) {
+        if constexpr (MID) {
+            const uint32_t m8 = 0xc100c100u;                   // -8, -8
+            const int r = 8 * wave_id() + (lane & 7), q = lane >> 4;
+            // (in assembly, with its wait: the compiler would wait for the copies in flight
+            // in every second step, and counts them right in the others)
+            auto address = [&](int i) {
+                return (uint32_t)(uintptr_t)(lds_void_t*)(xs[xb] + (i >> 1) * 4096 + kc_off(r, 64 * (i & 1) + 16 * q));
+            };
+            typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+            u32x4_t v0, v1, v2, v3;
+            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3)
+                         : "v"(address(0)), "v"(address(1)), "v"(address(2)), "v"(address(3))
+                         : "memory");
+            const uint4 v[4] = {__builtin_bit_cast(uint4, v0), __builtin_bit_cast(uint4, v1), __builtin_bit_cast(uint4, v2),
+                                __builtin_bit_cast(uint4, v3)};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = g * (G / 32); i < (g + 1) * (G / 32); ++i) t = D::mfma(v[i], make_uint4(m8, m8, m8, m8), t);
+                // (rows 4 q + r, of which 8 .. 15 are 0 .. 7 again)
+                if ((lane & 47) == 0) *(f32x4*)(sums + (buf * NG + g) * 64 + 8 * wave_id() + 4 * q) = t;
+            }
+        }
+    }
+    // x's fragment of 32 rows for MFMA step t = 2 c + u
+    __device__ __forceinline__ uint4 frag(int xb, int m, int t) {
+        const int j = lane & 31, h = lane >> 5;
+        return *(const uint4*)(xs[xb] + (t >> 2) * 4096 + kc_off(32 * m + j, 16 * ((2 * t - (t & 1) + 2 * h) & 7)));
+    }
+    // In flight at the top of a step: its codes, x and scales; then, not waited for, codes,
+    // x, scales and codes of the next two.  W: s % 3, S: s % 2.
+    template <int W, int S>
+    __device__ __forceinline__ void step(int s) {
+        t2_wait<10 + NS>();
+        t2_barrier();
+        load_x(s + 2, (W + 2) % 3);
+        uint4 b[2][2], fx[4][2];                               // [MFMA step][n or m]
+        uint2 w[2];
+        uint32_t sc[NG], zr[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            if (g * KS >= ksteps) break;
-            uint4 b[KS][4];
-            const f32x4 scale = unpack4<D>(sc[BUF][g]);
+            sc[g] = *(const uint32_t*)(ss[S] + g * 128 + (lane & 31) * 4);
+            if (ZEROS) zr[g] = *(const uint16_t*)(ss[S] + SC * 256 + g * 64 + (lane & 31) * 2);
+        }
+        auto take = [&](int t) {
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                const float zero = (float)(zr[BUF][g] >> (8 * nb) & 255u);
-                const uint32_t c[4] = {w[BUF][nb].x, w[BUF][nb].y, w[BUF][nb].z, w[BUF][nb].w};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) b[ks][nb] = codes8<D>(c[g * KS + ks], zero);
+            for (int n = 0; n < 2; ++n) {
+                // (at: two addresses that the compiler cannot put together, or it reads both
+                // columns' words at once and then waits for the copies in flight, no longer
+                // knowing what is read)
+                if (t % 2 == 0) w[n] = *(const uint2*)(ws[W] + (at[n] ^ (t / 2 * 16)));
+                const uint32_t v = t % 2 ? w[n].y : w[n].x;
+                if constexpr (MID) b[t & 1][n] = codes8<D>(v);
+                else if constexpr (ZEROS) b[t & 1][n] = codes8<D>(v, (float)(zr[t / PER] >> (8 * n) & 255u));
+                else b[t & 1][n] = codes8<D>(v, 8.f);
             }
+        };
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                f32x4 part[4];
+            for (int m = 0; m < 2; ++m) fx[t & 3][m] = frag(W, m, t);
+        };
+        fetch(0);
+        take(0);
+        fetch(1);
+        f32x16 part[2][2];
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const int k = g * KS + ks;
-                    const uint4 fx = t2_frag<false>(ring.h[BUF][k >> 1], 16 * mb, 32 * (k & 1));
+        for (int t = 0; t < 8; ++t) {
+            if (t % PER == 0) {
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb)
-                        part[nb] = D::mfma(fx, b[ks][nb], ks ? part[nb] : f32x4{0.f, 0.f, 0.f, 0.f});
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                            if (MID) v = *(const f32x4*)(sums + (S * NG + t / PER) * 64 + 32 * m + 8 * i + 4 * (lane >> 5));
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) part[m][n][4 * i + r] = v[r];
+                        }
+            }
+            if (t < 6) fetch(t + 2);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) part[m][n] = mfma32<D>(fx[t & 3][m], b[t & 1][n], part[m][n]);
+            if (t < 7) take(t + 1);
+            if (t == 6) {                                      // all of the step's codes are in registers
+                if constexpr (MID) {
+                    t2_wait<6 + NS>();                         // the wave's copies of the next x
+                    t2_fence();
+                    put_sums((W + 1) % 3, S ^ 1);
                 }
+                __builtin_amdgcn_s_waitcnt(0xc07f);            // (lgkmcnt 0)
+                t2_fence();
+                load_scales(s + 2, S);
+                load_codes(s + 3, W);
+            }
+            if (t % PER == PER - 1 && (NG == 1 || s * NG + t / PER < K / G)) {
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb)
+                for (int n = 0; n < 2; ++n) {
+                    const float scale = n ? D::hi(sc[t / PER]) : D::lo(sc[t / PER]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[mb][nb][r] = fmaf(scale[nb], part[nb][r], acc[mb][nb][r]);
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[m][n][r] = fmaf(scale, part[m][n][r], acc[m][n][r]);
+                }
             }
         }
     }
 };
 
-template <class D, int G, int MB, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void k_w4_tile(W4Args a) {
-    constexpr int TM = 16 * MB, TN = 64 * NW;
-    __shared__ __attribute__((aligned(16))) uint16_t s00[TM * 64], s01[TM * 64], s10[TM * 64], s11[TM * 64],
-        s20[TM * 64], s21[TM * 64];
+template <class D, int G, int MODE>
+__global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
+    typedef W4Loop<D, G, MODE> Loop;
+    constexpr int TM = 64, TN = kW4Cols, XS = TM * 128, WS = TN * 64, SS = kW4Waves * Loop::NS * 256;
+    __shared__ __attribute__((aligned(16))) uint16_t x0[XS], x1[XS], x2[XS];
+    __shared__ __attribute__((aligned(16))) uint8_t w0[WS], w1[WS], w2[WS], s0[SS], s1[SS];
+    __shared__ __attribute__((aligned(16))) float sums[Loop::MID ? 2 * Loop::NG * 64 : 4];
     const LinFwdArgs& f = a.f;
     int e, lo, hi, nt, mt;
     if (!lin_tile<TM, 1>(f.t, (f.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
-    const W4Ring<MB> ring{{{s00, s01}, {s10, s11}, {s20, s21}}};
-    const TileOperand<false, TM, 1, 64 * NW> x(f.x, f.K, lo, hi);
-    const int lane = lane_id(), col = nt * TN + 64 * wave_id() + 4 * (lane & 15), colc = min(col, f.N - 4);
-    const int64_t ge = (int64_t)e * (f.K / G) * f.N + colc;
-    W4Loop<D, G, MB, NW> l{a, x, ring, {}, a.scales + ge, a.zeros ? a.zeros + ge : nullptr, (f.K + 127) / 128, lane};
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-        l.codes[nb] = a.codes + ((int64_t)e * f.N + colc + nb) * (f.K / 2);
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) l.acc[mb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int lane = lane_id(), wv = wave_id(), n0 = nt * TN, col = n0 + 64 * wv + 2 * (lane & 31);
+    const int64_t ge = (int64_t)e * (f.K / G) * f.N + n0;
+    Loop l;
+    l.K = f.K;
+    l.N = f.N;
+    l.last = (f.K + 127) / 128;
+    l.lane = lane;
+    l.xs[0] = x0; l.xs[1] = x1; l.xs[2] = x2;
+    l.ws[0] = w0 + wv * 4096; l.ws[1] = w1 + wv * 4096; l.ws[2] = w2 + wv * 4096;
+    l.ss[0] = s0 + wv * Loop::NS * 256; l.ss[1] = s1 + wv * Loop::NS * 256;
+    l.sums = sums;
+    l.x = (const char*)(f.x + (int64_t)lo * f.K);
+    l.codes = (const char*)a.codes + ((int64_t)e * f.N + n0) * (f.K / 2);
+    l.scales = (const char*)(a.scales + ge);
+    l.zeros = a.zeros ? (const char*)a.zeros + ge : nullptr;
+    {
+        // chunk c of row r goes to slot c ^ (r / 2 % 8) (kc_off)
+        const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) ^ (r >> 1 & 7);
+        l.xk = 8 * c;
+        l.xo = (uint32_t)min(r, hi - lo - 1) * f.K * 2 + 16 * c;
     }
-    l.load(0, 0);
-    if (l.steps > 1) l.load(1, 1);
-    for (int s = 0; s < l.steps; s += 3) {
-        l.template step<0>(s);
-        if (s + 1 < l.steps) l.template step<1>(s + 1);
-        if (s + 2 < l.steps) l.template step<2>(s + 2);
+    l.so = min(64 * wv + 2 * (lane & 31), f.N - 2 - n0);
+    l.zo = min(64 * wv + 4 * (lane & 15), f.N - 4 - n0);
+    l.ck = 16 * ((lane & 3) ^ (lane >> 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // copy i of lane l goes to row 16 i + l / 4 of the wave's stage (column 2 j + n at 32 n + j), slot l % 4
+        // with chunk l % 4 ^ j / 4 % 4
+        const int r = 16 * i + (lane >> 2), j = r & 31, n = r >> 5;
+        l.co[i] = (uint32_t)min(64 * wv + 2 * j + n, f.N - 1 - n0) * (f.K / 2) + l.ck;
     }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        l.at[n] = n * 2048 + (lane & 31) * 64 + (lane >> 2 & 3) * 16 + (lane >> 5) * 8;
+        asm volatile("" : "+v"(l.at[n]));
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) l.acc[m][n][r] = 0.f;
+    l.load_codes(0, 0);
+    l.load_x(0, 0);
+    l.load_scales(0, 0);
+    l.load_codes(1, 1);
+    l.load_x(1, 1);
+    l.load_scales(1, 1);
+    l.load_codes(2, 2);
+    if (Loop::MID) {
+        t2_wait<10 + Loop::NS>();
+        t2_fence();
+        l.put_sums(0, 0);
+    }
+    // (left at once after the last step: the compiler counts what may be in flight at a
+    // read over every way that leads there)
+    for (int s = 0;; s += 6) {
+        l.template step<0, 0>(s);
+        if (s + 1 >= l.last) break;
+        l.template step<1, 1>(s + 1);
+        if (s + 2 >= l.last) break;
+        l.template step<2, 0>(s + 2);
+        if (s + 3 >= l.last) break;
+        l.template step<0, 1>(s + 3);
+        if (s + 4 >= l.last) break;
+        l.template step<1, 0>(s + 4);
+        if (s + 5 >= l.last) break;
+        l.template step<2, 1>(s + 5);
+        if (s + 6 >= l.last) break;
+    }
+    t2_wait<0>();                              // (the copies of the last step again)
     if (col >= f.N) return;
+    float bias[2] = {0.f, 0.f};
+    if (f.bias) {
+        const uint32_t v = *(const uint32_t*)(f.bias + (int64_t)e * f.N + col);
+        bias[0] = D::lo(v);
+        bias[1] = D::hi(v);
+    }
+    // 16 rows at a time, their residual (which may be y) loaded ahead of their stores
+    auto out = [&](auto A) {
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+        for (int m = 0; m < 2; ++m) {
+            uint32_t res[16];
+            const int r0 = lo + 32 * m + 4 * (lane >> 5);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = lo + 16 * mb + 4 * (lane >> 4) + r;
-            if (row < hi) w4_out<D>(f, e, row, col, f32x4{l.acc[mb][0][r], l.acc[mb][1][r], l.acc[mb][2][r], l.acc[mb][3][r]});
+            for (int r = 0; r < 16; ++r) {
+                const int row = r0 + 8 * (r >> 2) + (r & 3);
+                res[r] = f.residual ? *(const uint32_t*)(f.residual + (int64_t)min(row, hi - 1) * f.N + col) : 0u;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = r0 + 8 * (r >> 2) + (r & 3);
+                float v[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) v[n] = act<decltype(A)::value>(l.acc[m][n][r] + bias[n]);
+                if (row < hi)
+                    *(uint32_t*)(f.y + (int64_t)row * f.N + col) = D::pack2(v[0] + D::lo(res[r]), v[1] + D::hi(res[r]));
+            }
         }
+    };
+    dev_act(f.act, out);
 }
 
 // ================================================================ quantiser
@@ -294,13 +529,14 @@ LinTiles w4_tiles(int M, int E, int K, int N) {
     return {nullptr, nullptr, E, M, tm, nullptr};
 }
 
-int w4_tile_columns(const LinTiles& t) { return t.tm == 16 ? 16 : 256; }
+int w4_tile_columns(const LinTiles& t) { return t.tm == 16 ? 16 : kW4Cols; }
 
 template <class D, int G>
 static int w4_(const W4Args& a, hipStream_t st) {
     const int64_t grid = max_tiles(a.f.t) * ((a.f.N + w4_tile_columns(a.f.t) - 1) / w4_tile_columns(a.f.t));
     if (a.f.t.tm == 16) return go(k_w4_stream<D, G, 8>, grid, 512, a, st);
-    return go(k_w4_tile<D, G, 4, 4>, grid, 256, a, st);
+    if (a.zeros) return go(k_w4_tile<D, G, W4_ZEROS>, grid, 64 * kW4Waves, a, st);
+    return go(k_w4_tile<D, G, std::is_same<D, Bf16>::value ? W4_MID : W4_EIGHT>, grid, 64 * kW4Waves, a, st);
 }
 
 template <class F>
