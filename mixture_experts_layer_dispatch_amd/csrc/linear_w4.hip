@@ -216,26 +216,18 @@ struct W4Loop {
     // Steps behind the last are the last one again, so that every step has the same copies
     // in flight; inputs behind the rows are their last ones again, and their groups are
     // not added.
-    __device__ __forceinline__ void load_x(int s, int buf) {
+    __device__ __forceinline__ void load_x(int s, int buf, int h) {
         s = min(s, last - 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k0 = min(s * 128 + 64 * h, (K - 1) / 64 * 64);
-            uint32_t back = 0;                                 // (at most the chunk's place in the row)
-            if (G < 128 && k0 + 64 > K) back = (uint32_t)max(k0 + (int)xk + 8 - K, 0) * 2;
-            copy_lds<16>(x + (int64_t)k0 * 2, xo - back, xs[buf] + h * 4096 + wave_id() * 512);
-        }
-        t2_fence();
+        const int k0 = min(s * 128 + 64 * h, (K - 1) / 64 * 64);
+        uint32_t back = 0;                                     // (at most the chunk's place in the row)
+        if (G < 128 && k0 + 64 > K) back = (uint32_t)max(k0 + (int)xk + 8 - K, 0) * 2;
+        copy_lds<16>(x + (int64_t)k0 * 2, xo - back, xs[buf] + h * 4096 + wave_id() * 512);
     }
-    __device__ __forceinline__ void load_codes(int s, int buf) {
+    __device__ __forceinline__ void load_codes(int s, int buf, int i) {
         s = min(s, last - 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t back = 0;
-            if (G < 128 && s * 128 + 128 > K) back = (uint32_t)max(s * 64 + (int)ck + 16 - K / 2, 0);   // (at most ck)
-            copy_lds<16>(codes + s * 64, co[i] - back, ws[buf] + i * 1024);
-        }
-        t2_fence();
+        uint32_t back = 0;
+        if (G < 128 && s * 128 + 128 > K) back = (uint32_t)max(s * 64 + (int)ck + 16 - K / 2, 0);   // (at most ck)
+        copy_lds<16>(codes + s * 64, co[i] - back, ws[buf] + i * 1024);
     }
     __device__ __forceinline__ void load_scales(int s, int buf) {
 #pragma unroll
@@ -247,7 +239,13 @@ struct W4Loop {
             const int row = min(s * NG + min(lane >> 4, NG - 1), K / G - 1);
             copy_lds<4>(zeros, (uint32_t)row * N + zo, ss[buf] + SC * 256);
         }
-        t2_fence();
+    }
+    // copy number i of a step's (all of the scales are one), spread over the MFMAs of the
+    // step two before: in one place they hold up the wave
+    __device__ __forceinline__ void load(int i, int s, int xw, int sb) {
+        if (i < 2) load_x(s, xw, i);
+        else if (i == 2) load_scales(s, sb);
+        else if (i < 7) load_codes(s, xw, i - 3);
     }
     // sums(s) of the wave's eight rows, which its own copies have brought
     __device__ __forceinline__ void put_sums(int xb, int buf) {
@@ -283,13 +281,12 @@ struct W4Loop {
         const int j = lane & 31, h = lane >> 5;
         return *(const uint4*)(xs[xb] + (t >> 2) * 4096 + kc_off(32 * m + j, 16 * ((2 * t - (t & 1) + 2 * h) & 7)));
     }
-    // In flight at the top of a step: its codes, x and scales; then, not waited for, codes,
-    // x, scales and codes of the next two.  W: s % 3, S: s % 2.
+    // In flight at the top of a step: its own copies; then, not waited for, the next
+    // step's.  W: s % 3, S: s % 2.
     template <int W, int S>
     __device__ __forceinline__ void step(int s) {
-        t2_wait<10 + NS>();
+        t2_wait<6 + NS>();
         t2_barrier();
-        load_x(s + 2, (W + 2) % 3);
         uint4 b[2][2], fx[4][2];                               // [MFMA step][n or m]
         uint2 w[2];
         uint32_t sc[NG], zr[NG];
@@ -339,17 +336,12 @@ struct W4Loop {
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int n = 0; n < 2; ++n) part[m][n] = mfma32<D>(fx[t & 3][m], b[t & 1][n], part[m][n]);
+            load(t, s + 2, (W + 2) % 3, S);
             if (t < 7) take(t + 1);
-            if (t == 6) {                                      // all of the step's codes are in registers
-                if constexpr (MID) {
-                    t2_wait<6 + NS>();                         // the wave's copies of the next x
-                    t2_fence();
-                    put_sums((W + 1) % 3, S ^ 1);
-                }
-                __builtin_amdgcn_s_waitcnt(0xc07f);            // (lgkmcnt 0)
+            if (MID && t == 6) {
+                t2_wait<10 + 2 * NS>();                        // the wave's copies of the next x
                 t2_fence();
-                load_scales(s + 2, S);
-                load_codes(s + 3, W);
+                put_sums((W + 1) % 3, S ^ 1);
             }
             if (t % PER == PER - 1 && (NG == 1 || s * NG + t / PER < K / G)) {
 #pragma unroll
@@ -417,15 +409,12 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) l.acc[m][n][r] = 0.f;
-    l.load_codes(0, 0);
-    l.load_x(0, 0);
-    l.load_scales(0, 0);
-    l.load_codes(1, 1);
-    l.load_x(1, 1);
-    l.load_scales(1, 1);
-    l.load_codes(2, 2);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 7; ++i) l.load(i, s, s, s);
     if (Loop::MID) {
-        t2_wait<10 + Loop::NS>();
+        t2_wait<10 + 2 * Loop::NS>();
         t2_fence();
         l.put_sums(0, 0);
     }
