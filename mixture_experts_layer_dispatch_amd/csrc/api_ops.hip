@@ -140,7 +140,7 @@ size_t norm_bytes(const moe_norm_config& c) { return up256((size_t)norm_parts(c.
 
 // ---------------------------------------------------------------- linear with 4-bit weights
 struct W4Layout {
-    size_t list, total;
+    size_t list, sums, total;
 };
 
 moe_status w4_check(const moe_linear_w4_config* c) {
@@ -154,7 +154,11 @@ moe_status w4_check(const moe_linear_w4_config* c) {
     return MOE_OK;
 }
 
-W4Layout w4_layout(const moe_linear_w4_config& c) { return {256, 256 + up256((size_t)(c.E + 1) * 4)}; }
+W4Layout w4_layout(const moe_linear_w4_config& c) {
+    const int ks = w4_plan(c.M, c.E, c.K, c.N).ksplit;
+    const size_t sums = 256 + up256((size_t)(c.E + 1) * 4);
+    return {256, sums, sums + up256(ks > 1 ? (size_t)ks * c.M * c.N * 4 : 0)};
+}
 
 }  // namespace
 
@@ -373,10 +377,11 @@ moe_status moe_linear_w4_forward(const moe_linear_w4_config* c, const int32_t* o
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
-    LinTiles t = w4_tiles(c->M, c->E, c->K, c->N);
-    if (lin_tiles(c->E, offsets, (char*)workspace, &L.list, {{&t, c->N, w4_tile_columns(t)}}, st)) return MOE_ERR_HIP;
-    const W4Args a{{t, c->dtype, c->act, c->N, c->K, (const uint16_t*)x, nullptr, (const uint16_t*)bias,
-                    (const uint16_t*)residual, (uint16_t*)y, nullptr, 1, nullptr},
+    char* ws = (char*)workspace;
+    W4Plan p = w4_plan(c->M, c->E, c->K, c->N);
+    if (lin_tiles(c->E, offsets, ws, &L.list, {{&p.t, c->N, w4_tile_columns(p)}}, st)) return MOE_ERR_HIP;
+    const W4Args a{{p.t, c->dtype, c->act, c->N, c->K, (const uint16_t*)x, nullptr, (const uint16_t*)bias,
+                    (const uint16_t*)residual, (uint16_t*)y, nullptr, p.ksplit, (float*)(ws + L.sums)},
                    (const uint8_t*)codes, (const uint16_t*)scales, (const uint8_t*)zeros, c->group};
     return launch_w4(a, st) ? MOE_ERR_HIP : MOE_OK;
 }

@@ -524,8 +524,12 @@ struct W4QuantArgs {
 };
 
 // linear_w4.hip
-LinTiles w4_tiles(int M, int E, int K, int N);
-int w4_tile_columns(const LinTiles& t);
+struct W4Plan {
+    LinTiles t;               // 16 rows: k_w4_stream, 64: k_w4_tile
+    int ksplit;               // parts of the reduction (k_w4_tile)
+};
+W4Plan w4_plan(int M, int E, int K, int N);
+int w4_tile_columns(const W4Plan& p);
 int launch_w4(const W4Args& a, hipStream_t st);
 int launch_w4_quant(const W4QuantArgs& a, hipStream_t st);
 

@@ -105,52 +105,107 @@ __device__ __forceinline__ void dev_act(int act, const F& f) {
     }
 }
 
+// what is taken off the codes: 8, by the sums of x; 8, exactly; zeros, exactly
+enum { W4_MID, W4_EIGHT, W4_ZEROS };
+
 // ================================================================ few rows
-// 16 rows by 16 columns a block, its W waves split the reduction in units of 128.
-template <class D, int G, int W>
+// A handful of rows: the codes are read once and everything else is small, so the
+// product is a stream.  A block computes 16 rows by 16 NB columns; its W waves split
+// the reduction in units of 128 inputs, whose codes they read straight into registers,
+// UNITS at a time.  A lane quarter reads 16 bytes of a row, 32 inputs in a row; groups of
+// 128 are multiplied in that order (word s of every quarter, and the same inputs of x,
+// to an MFMA), smaller ones are first transposed over the quarters.
+template <class D, int G, int MODE, int NB, int W, int UNITS>
 __global__ __launch_bounds__(64 * W) void k_w4_stream(W4Args a) {
-    __shared__ __attribute__((aligned(16))) float sums[W][16][20];
+    constexpr int TN = 16 * NB, NG = 128 / G, PER = G / 32;
+    __shared__ __attribute__((aligned(16))) float sums[W][16][TN + 4];
     const LinFwdArgs& f = a.f;
     int e, lo, hi, nt, mt;
-    if (!lin_tile<16, 1>(f.t, (f.N + 15) / 16, blockIdx.x, e, lo, hi, nt, mt)) return;
-    const int lane = lane_id(), wv = wave_id(), j = lane & 15, q = lane >> 4;
-    const int col = min(nt * 16 + j, f.N - 1), groups = f.K / G;
+    if (!lin_tile<16, 1>(f.t, (f.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
+    const int lane = lane_id(), wv = wave_id(), j = lane & 15, q = lane >> 4, groups = f.K / G;
     const uint16_t* x = f.x + (int64_t)min(lo + j, hi - 1) * f.K;
-    const uint8_t* codes = a.codes + ((int64_t)e * f.N + col) * (f.K / 2);
-    const uint16_t* scales = a.scales + (int64_t)e * groups * f.N + col;
-    const uint8_t* zeros = a.zeros ? a.zeros + (int64_t)e * groups * f.N + col : nullptr;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int k0 = wv * 128; k0 < f.K; k0 += W * 128) {
-        // (behind the row: its last codes, times zeros in place of x)
-        uint4 c = *(const uint4*)(codes + min(k0 + 32 * q, f.K - 32) / 2);
-        transpose_quarters(c);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        f32x4 part = {0.f, 0.f, 0.f, 0.f};
-        float scale = 0.f, zero = 8.f;
+    const uint8_t* codes[NB];
+    int64_t ge[NB];
+    f32x4 acc[NB];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = k0 + 32 * s;
-            if (k >= f.K) break;
-            if (k % G == 0) {
-                part = f32x4{0.f, 0.f, 0.f, 0.f};
-                scale = D::lo(scales[(int64_t)(k / G) * f.N]);
-                if (zeros) zero = zeros[(int64_t)(k / G) * f.N];
+    for (int n = 0; n < NB; ++n) {
+        const int col = min(nt * TN + 16 * n + j, f.N - 1);
+        codes[n] = a.codes + ((int64_t)e * f.N + col) * (f.K / 2);
+        ge[n] = (int64_t)e * groups * f.N + col;
+        acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int units = (f.K + 127) / 128;
+    for (int u0 = wv; u0 < units; u0 += W * UNITS) {
+        uint4 c[UNITS][NB];
+        uint16_t sc[UNITS][NB][NG];
+        uint8_t zr[UNITS][NB][NG];
+        uint4 xv[UNITS][4];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int k0 = min(u0 + u * W, units - 1) * 128;   // (one behind the last: read, not added)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                c[u][n] = *(const uint4*)(codes[n] + min(k0 + 32 * q, f.K - 32) / 2);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int64_t at = ge[n] + (int64_t)min(k0 / G + g, groups - 1) * f.N;
+                    sc[u][n][g] = a.scales[at];
+                    if (MODE == W4_ZEROS) zr[u][n][g] = a.zeros[at];
+                }
             }
-            part = D::mfma(*(const uint4*)(x + k + 8 * q), codes8<D>(w[s], zero), part);
-            if ((k + 32) % G == 0)
+        }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] = fmaf(scale, part[r], acc[r]);
+        for (int u = 0; u < UNITS; ++u) {
+            const int k0 = min(u0 + u * W, units - 1) * 128;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                xv[u][s] = *(const uint4*)(x + (G == 128 ? k0 + 32 * q + 8 * s : min(k0 + 32 * s, f.K - 32) + 8 * q));
+        }
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            if (u0 + u * W >= units) break;
+            const int k0 = (u0 + u * W) * 128;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                if (G < 128) transpose_quarters(c[u][n]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (g > 0 && k0 + g * G >= f.K) break;
+                f32x4 start = {0.f, 0.f, 0.f, 0.f};
+                if (MODE == W4_MID) {
+#pragma unroll
+                    for (int s = g * PER; s < (g + 1) * PER; ++s)
+                        start = D::mfma(xv[u][s], make_uint4(0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u), start);
+                }
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const uint32_t w[4] = {c[u][n].x, c[u][n].y, c[u][n].z, c[u][n].w};
+                    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = g * PER; s < (g + 1) * PER; ++s) {
+                        uint4 b;
+                        if constexpr (MODE == W4_MID) b = codes8<D>(w[s]);
+                        else b = codes8<D>(w[s], MODE == W4_ZEROS ? (float)zr[u][n][g] : 8.f);
+                        part = D::mfma(xv[u][s], b, part);
+                    }
+                    const float scale = D::lo(sc[u][n][g]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[n][r] = fmaf(scale, MODE == W4_MID ? part[r] + start[r] : part[r], acc[n][r]);
+                }
+            }
         }
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sums[wv][4 * q + r][j] = acc[r];
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sums[wv][4 * q + r][16 * n + j] = acc[n][r];
     __syncthreads();
-    if (threadIdx.x >= 64) return;
-    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
+    if (threadIdx.x >= 64 * NB) return;
+    const int r = threadIdx.x / (4 * NB), c = threadIdx.x % (4 * NB) * 4;
     f32x4 v = *(const f32x4*)&sums[0][r][c];
 #pragma unroll
     for (int p = 1; p < W; ++p) v += *(const f32x4*)&sums[p][r][c];
-    if (lo + r < hi && nt * 16 + c < f.N) w4_out<D>(f, e, lo + r, nt * 16 + c, v);
+    if (lo + r < hi && nt * TN + c < f.N) w4_out<D>(f, e, lo + r, nt * TN + c, v);
 }
 
 // ================================================================ tiles
@@ -191,9 +246,6 @@ __device__ __forceinline__ void copy_lds(const char* base, uint32_t o, void* dst
 
 constexpr int kW4Waves = 8, kW4Cols = 64 * kW4Waves;
 
-// what is taken off the codes: 8, by the sums of x; 8, exactly; zeros, exactly
-enum { W4_MID, W4_EIGHT, W4_ZEROS };
-
 template <class D, int G, int MODE>
 struct W4Loop {
     static constexpr bool MID = MODE == W4_MID;
@@ -201,7 +253,8 @@ struct W4Loop {
     static constexpr bool ZEROS = MODE == W4_ZEROS;
     static constexpr int SC = (NG + 1) / 2;               // copies of scales, two groups each
     static constexpr int NS = SC + ZEROS;                 // and with that of zeros
-    int K, N, last, lane;
+    int K, N, lane;
+    int last;                     // the part's steps end here
     uint16_t* xs[3];              // [half of 64 inputs][64 rows]
     uint8_t* ws[3];               // the wave's 4 KB of a stage
     uint8_t* ss[2];               // its 256 NS bytes: [group][column 2 j + n] scales, [group][column] zeros
@@ -366,13 +419,15 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
     __shared__ __attribute__((aligned(16))) float sums[Loop::MID ? 2 * Loop::NG * 64 : 4];
     const LinFwdArgs& f = a.f;
     int e, lo, hi, nt, mt;
-    if (!lin_tile<TM, 1>(f.t, (f.N + TN - 1) / TN, blockIdx.x, e, lo, hi, nt, mt)) return;
+    const int ks = f.ksplit, part = ks > 1 ? blockIdx.x % ks : 0;
+    if (!lin_tile<TM, 1>(f.t, (f.N + TN - 1) / TN, ks > 1 ? blockIdx.x / ks : blockIdx.x, e, lo, hi, nt, mt)) return;
     const int lane = lane_id(), wv = wave_id(), n0 = nt * TN, col = n0 + 64 * wv + 2 * (lane & 31);
     const int64_t ge = (int64_t)e * (f.K / G) * f.N + n0;
     Loop l;
     l.K = f.K;
     l.N = f.N;
-    l.last = (f.K + 127) / 128;
+    const int steps = (f.K + 127) / 128, first = (int)((int64_t)steps * part / ks);
+    l.last = (int)((int64_t)steps * (part + 1) / ks);
     l.lane = lane;
     l.xs[0] = x0; l.xs[1] = x1; l.xs[2] = x2;
     l.ws[0] = w0 + wv * 4096; l.ws[1] = w1 + wv * 4096; l.ws[2] = w2 + wv * 4096;
@@ -412,7 +467,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 7; ++i) l.load(i, s, s, s);
+        for (int i = 0; i < 7; ++i) l.load(i, first + s, s, s);
     if (Loop::MID) {
         t2_wait<10 + 2 * Loop::NS>();
         t2_fence();
@@ -420,7 +475,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
     }
     // (left at once after the last step: the compiler counts what may be in flight at a
     // read over every way that leads there)
-    for (int s = 0;; s += 6) {
+    for (int s = first;; s += 6) {
         l.template step<0, 0>(s);
         if (s + 1 >= l.last) break;
         l.template step<1, 1>(s + 1);
@@ -436,6 +491,17 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
     }
     t2_wait<0>();                              // (the copies of the last step again)
     if (col >= f.N) return;
+    if (ks > 1) {                              // k_w4_sum does the rest
+        float* out = f.part + (int64_t)part * f.t.rows * f.N + col;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = lo + 32 * m + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                if (row < hi) *(f32x2*)(out + (int64_t)row * f.N) = f32x2{l.acc[m][0][r], l.acc[m][1][r]};
+            }
+        return;
+    }
     float bias[2] = {0.f, 0.f};
     if (f.bias) {
         const uint32_t v = *(const uint32_t*)(f.bias + (int64_t)e * f.N + col);
@@ -465,6 +531,20 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
         }
     };
     dev_act(f.act, out);
+}
+
+// The parts of a split reduction, added in order: eight rows of a tile, 128 columns.
+template <class D>
+__global__ __launch_bounds__(256) void k_w4_sum(W4Args a) {
+    const LinFwdArgs& f = a.f;
+    int e, lo, hi, nt, mt;
+    if (!lin_tile<64, 1>(f.t, (f.N + 127) / 128, blockIdx.x / 8, e, lo, hi, nt, mt)) return;
+    const int row = lo + blockIdx.x % 8 * 8 + (threadIdx.x >> 5), col = nt * 128 + (threadIdx.x & 31) * 4;
+    if (row >= hi || col >= f.N) return;
+    f32x4 v = *(const f32x4*)(f.part + (int64_t)row * f.N + col);
+#pragma unroll 4
+    for (int q = 1; q < f.ksplit; ++q) v += *(const f32x4*)(f.part + ((int64_t)q * f.t.rows + row) * f.N + col);
+    w4_out<D>(f, e, row, col, v);
 }
 
 // ================================================================ quantiser
@@ -513,19 +593,46 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a, int64_t total) 
 }
 
 // ================================================================ launchers
-LinTiles w4_tiles(int M, int E, int K, int N) {
-    const int tm = (E ? M <= 8LL * E : M <= 16) ? 16 : 64;
-    return {nullptr, nullptr, E, M, tm, nullptr};
+// The tiles of a product and the parts of its reduction.  Few rows go as a stream, 16
+// at a time (512 experts, 4096 -> 1024: of 8 rows 291 us, in tiles of 64 rows 336; of 12
+// 335 both, of 16 395 and 339; dense 4096 x 4096, 32 rows 12 and 18, 64 rows 15 and 19).
+// A round of tiles over the
+// 256 CUs takes 2.3 us a step of 128 inputs, its beginning and end about 5; parts
+// cost a launch more (6 us) and their sums' way through memory.
+W4Plan w4_plan(int M, int E, int K, int N) {
+    W4Plan p{{nullptr, nullptr, E, M, (E ? M <= 12LL * E : M <= 64) ? 16 : 64, nullptr}, 1};
+    if (p.t.tm == 16) return p;
+    const int64_t tiles = max_tiles(p.t) * ((N + kW4Cols - 1) / kW4Cols);
+    const int steps = (K + 127) / 128;
+    float least = 1e30f;
+    for (int ks = 1; ks <= 16 && ks * 2 <= steps + 1; ++ks) {
+        const float us = (float)((tiles * ks + 255) / 256) * (2.3f * ((steps + ks - 1) / ks) + 5.f) +
+                         (ks > 1 ? 6.f + 2.5e-6f * ks * M * N : 0.f);
+        if (us < least) {
+            least = us;
+            p.ksplit = ks;
+        }
+    }
+    return p;
 }
 
-int w4_tile_columns(const LinTiles& t) { return t.tm == 16 ? 16 : kW4Cols; }
+int w4_tile_columns(const W4Plan& p) { return p.t.tm == 16 ? 16 : kW4Cols; }
 
-template <class D, int G>
+template <class D, int G, int MODE>
 static int w4_(const W4Args& a, hipStream_t st) {
-    const int64_t grid = max_tiles(a.f.t) * ((a.f.N + w4_tile_columns(a.f.t) - 1) / w4_tile_columns(a.f.t));
-    if (a.f.t.tm == 16) return go(k_w4_stream<D, G, 8>, grid, 512, a, st);
-    if (a.zeros) return go(k_w4_tile<D, G, W4_ZEROS>, grid, 64 * kW4Waves, a, st);
-    return go(k_w4_tile<D, G, std::is_same<D, Bf16>::value ? W4_MID : W4_EIGHT>, grid, 64 * kW4Waves, a, st);
+    const LinFwdArgs& f = a.f;
+    const int64_t tiles = max_tiles(f.t);
+    if (f.t.tm == 16) {
+        // Several columns of 16 share the loads of x, and few waves a block's beginning and
+        // end, where the blocks are enough for the chip (4 rows, 4096 -> 65536: by 64
+        // columns 28 us, by 32 36; 160 rows at 512 experts 70 and 72, by 16 92).
+        const int64_t four = tiles * ((f.N + 63) / 64), two = tiles * ((f.N + 31) / 32);
+        if (four >= 1024) return go(k_w4_stream<D, G, MODE, 4, 4, 2>, four, 256, a, st);
+        if (two >= 512) return go(k_w4_stream<D, G, MODE, 2, 4, 4>, two, 256, a, st);
+        return go(k_w4_stream<D, G, MODE, 1, 8, 4>, tiles * ((f.N + 15) / 16), 512, a, st);
+    }
+    if (go(k_w4_tile<D, G, MODE>, tiles * ((f.N + kW4Cols - 1) / kW4Cols) * f.ksplit, 64 * kW4Waves, a, st)) return -1;
+    return f.ksplit > 1 ? go(k_w4_sum<D>, tiles * ((f.N + 127) / 128) * 8, 256, a, st) : 0;
 }
 
 template <class F>
@@ -538,7 +645,9 @@ static int with_group(int G, const F& f) {
 int launch_w4(const W4Args& a, hipStream_t st) {
     ProfScope prof_(st, "linear_w4");
     return with_group(a.G, [&](auto g) {
-        return a.f.dtype == 0 ? w4_<Bf16, decltype(g)::value>(a, st) : w4_<Fp16, decltype(g)::value>(a, st);
+        constexpr int G = decltype(g)::value;
+        if (a.f.dtype == 0) return a.zeros ? w4_<Bf16, G, W4_ZEROS>(a, st) : w4_<Bf16, G, W4_MID>(a, st);
+        return a.zeros ? w4_<Fp16, G, W4_ZEROS>(a, st) : w4_<Fp16, G, W4_EIGHT>(a, st);
     });
 }
 

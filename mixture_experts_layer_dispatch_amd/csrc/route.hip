@@ -45,52 +45,36 @@ __device__ __forceinline__ int first_expert(const Lanes& L, int n_group, int lan
 }
 
 // ================================================================ forward
+// The choice in 64 bits, for the tokens whose scores 32 bits cannot tell apart: k
+// rounds of a wave's largest, the lower index first.  sel: lane r has the r-th choice.
 template <int EPL>
-__global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L) {
-    const int64_t t = block_number() * 4 + wave_id();
-    if (t >= a.T) return;
-    const int lane = lane_id();
-    const float* row = a.logits + t * a.E;
+__device__ __forceinline__ int choose64(const RouteArgs& a, const Lanes& L, const float* row, int lane) {
     int n;
     const int e0 = first_expert<EPL>(L, a.n_group, lane, n);
-    float v[EPL];
+    const bool two = a.n_group > 1 && a.group_top == 2;
+    double key[EPL], z = 0.0;
     float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        v[j] = j < n ? no_nan(row[e0 + j]) : -INFINITY;
-        m = fmaxf(m, v[j]);
-    }
-    const bool softmax = a.score == SCORE_SOFTMAX;
-    const bool groups = a.n_group > 1, two = groups && a.group_top == 2;
-    const bool by_logit = !a.bias && !two;
-    double key[EPL];
-    double z = 0.0;
+    for (int j = 0; j < n; ++j) m = fmaxf(m, no_nan(row[e0 + j]));
     m = wave_most(m);
-    if (softmax) {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (j < n) z += soft_exp((double)v[j], (double)m);
+    if (a.score == SCORE_SOFTMAX) {
+        for (int j = 0; j < n; ++j) z += soft_exp((double)no_nan(row[e0 + j]), (double)m);
         z = wave_sum(z);
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        key[j] = v[j];
-        if (j < n && (a.scores || !by_logit)) {
-            const double s = !softmax ? 1.0 / (1.0 + exp(-(double)v[j])) : z > 0.0 ? soft_exp((double)v[j], (double)m) / z : 0.0;
-            if (a.scores) a.scores[t * a.E + e0 + j] = (float)s;
-            if (!by_logit) key[j] = no_nan(s + (a.bias ? (double)a.bias[e0 + j] : 0.0));
-        }
+        if (j >= n) continue;
+        const double v = no_nan(row[e0 + j]);
+        const double s = a.score == SCORE_SIGMOID ? 1.0 / (1.0 + exp(-v)) : z > 0.0 ? soft_exp(v, (double)m) / z : 0.0;
+        key[j] = no_nan(s + (a.bias ? (double)a.bias[e0 + j] : 0.0));
     }
-    // the places still to be chosen
-    uint32_t open = n >= 32 ? ~0u : (1u << n) - 1u;
-    if (groups) {
+    uint32_t open = n >= 32 ? ~0u : (1u << n) - 1u;        // the places still to be chosen
+    if (a.n_group > 1) {
         double t1 = -(double)INFINITY, t2 = t1;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            if (j < n) {
-                t2 = fmax(t2, fmin(t1, key[j]));
-                t1 = fmax(t1, key[j]);
-            }
+            if (j >= n) continue;
+            t2 = fmax(t2, fmin(t1, key[j]));
+            t1 = fmax(t1, key[j]);
         }
         for (int off = L.per >> 1; off >= 1; off >>= 1) {
             const double o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
@@ -98,20 +82,14 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L) {
             t1 = fmax(t1, o1);
         }
         const double score = two ? no_nan(t1 + t2) : t1;
-        bool left = lane / L.per < a.n_group, kept = false;
-        for (int r = 0; r < a.topk_group; ++r) {
-            double b = score;
-            int at = left ? lane / L.per : 64;
-            for (int off = 32; off >= 1; off >>= 1) {
-                const double ob = __shfl_xor(b, off);
-                const int oat = __shfl_xor(at, off);
-                if (oat < 64 && (at == 64 || ob > b || (ob == b && oat < at))) { b = ob; at = oat; }
-            }
-            if (lane / L.per == at) { kept = true; left = false; }
+        int better = 0;
+        for (int g = 0; g < a.n_group; ++g) {
+            const double o = __shfl(score, g * L.per);
+            better += o > score || (o == score && g < lane / L.per);
         }
-        if (!kept) open = 0;
+        if (better >= a.topk_group) open = 0;
     }
-    int sel = 0;                                   // lane r < k: the r-th choice
+    int sel = 0;
     for (int r = 0; r < a.k; ++r) {
         double b = -(double)INFINITY;
         int at = 0x7fffffff;
@@ -126,31 +104,178 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L) {
         if (n > 0 && at >= e0 && at < e0 + n) open &= ~(1u << (at - e0));
         if (lane == r) sel = at;
     }
-    // the weights, in 64 bits: k of them
-    const bool in = lane < a.k;
-    const double l = in ? (double)no_nan(row[sel]) : -(double)INFINITY;
-    double p = 0.0, sum = 1.0;
-    if (a.renorm) {
-        // only the ratios of the chosen matter: the scores relative to the largest of
-        // them, so that none is lost where all are tiny
-        double ml = l;
-        for (int off = 32; off >= 1; off >>= 1) ml = fmax(ml, __shfl_xor(ml, off));
-        if (softmax) p = soft_exp(l, ml);
-        else {
-            const double c = fmin(ml, 0.0);
-            p = l == -(double)INFINITY ? 0.0 : l < 0.0 ? exp(l - c) / (1.0 + exp(l)) : exp(-c) / (1.0 + exp(-l));
+    return sel;
+}
+
+// Whole numbers in the order of floats (-0 as 0, NaN as -inf), none of them 0
+__device__ __forceinline__ uint32_t order(float v) {
+    const int b = __float_as_int(v + 0.f);
+    return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __int_as_float((int)(o ^ ((o & 0x80000000u) ? 0x80000000u : ~0u)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or0(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ uint32_t wave_most(uint32_t v) {
+    v = max(v, dpp_or0<0x111, 0xf>(v));
+    v = max(v, dpp_or0<0x112, 0xf>(v));
+    v = max(v, dpp_or0<0x114, 0xf>(v));
+    v = max(v, dpp_or0<0x118, 0xf>(v));
+    v = max(v, dpp_or0<0x142, 0xa>(v));
+    v = max(v, dpp_or0<0x143, 0xc>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The choice is the one in 64 bits.  Without a bias (and sums of two in the groups) it is
+// that of the logits, exactly.  Else the scores are computed in 32 bits, each off by
+// less than `err`, and where two that the choice tells apart, neighbours among the k + 1
+// best or a kept group's and another's, are closer than both errors, the token is done
+// again in 64 bits (16384 x 512, sigmoid and bias: one token in a thousand).  In half steps
+// of 1 (2^-24):
+//   sigmoid: exp(-v) by exp2 is off by 1.5 |v| + 2 relative, the score by s (1 - s) times
+//     that, below 0.5 + 0.5, and by 3 s from 1 + exp and the reciprocal; 8 are taken;
+//   softmax: s (|v - m| + 32), with s |v - m| <= 0.37 and 32 for the exponential and the sum
+//     over the experts, 1 / z the largest s;
+//   both: the rounding of c, |c| <= 1 + the largest |bias|; 2 (1 + that) are taken.
+template <int EPL, bool SCORES>
+__global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
+    const int lane = lane_id();
+    int n;
+    const int e0 = first_expert<EPL>(L, a.n_group, lane, n);
+    const bool softmax = a.score == SCORE_SOFTMAX;
+    const bool groups = a.n_group > 1, two = groups && a.group_top == 2;
+    const bool by_logit = !a.bias && !two;
+    float bias[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bias[j] = a.bias && j < n ? a.bias[e0 + j] : 0.f;
+    float size = 0.f;                                          // 1 + the largest finite |bias|
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        if (fabsf(bias[j]) < INFINITY) size = fmaxf(size, fabsf(bias[j]));
+    size = a.bias ? 1.f + wave_most(size) : 1.f;
+    for (int64_t t = block_number() * 4 + wave_id(); t < a.T; t += (int64_t)gridDim.x * gridDim.y * 4) {
+        const float* row = a.logits + t * a.E;
+        float v[EPL], m = -INFINITY;
+        if (EPL % 4 == 0 && vec) {                             // (n is a multiple of 4)
+#pragma unroll
+            for (int j = 0; j + 3 < EPL; j += 4) {
+                f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (j < n) q = *(const f32x4*)(row + e0 + j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j + i] = no_nan(q[i]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) v[j] = j < n ? no_nan(row[e0 + j]) : -INFINITY;
         }
-        sum = 0.0;
-        for (int r = 0; r < a.k; ++r) sum += __shfl(p, r);
-    } else if (softmax) {
-        p = soft_exp(l, (double)m);
-        sum = z;
-    } else {
-        p = 1.0 / (1.0 + exp(-l));
-    }
-    if (in) {
-        a.idx[t * a.k + lane] = sel;
-        a.w[t * a.k + lane] = sum > 0.0 ? (float)(a.scale * p / sum) : 0.f;
+        float z = 0.f;
+        if (softmax && (SCORES || !by_logit || !a.renorm)) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) m = fmaxf(m, v[j]);
+            m = wave_most(m);
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) z += soft_exp(v[j], m);
+            z = wave_total(z);
+        }
+        const float rz = z > 0.f ? 1.f / z : 0.f;
+        uint32_t key[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            float c = v[j];
+            if (SCORES || !by_logit) {
+                float s;
+                if (softmax) s = soft_exp(v[j], m) * rz;
+                else if (SCORES) s = 1.f / (1.f + expf(-v[j]));
+                else s = __builtin_amdgcn_rcpf(1.f + __expf(-v[j]));
+                if (SCORES && j < n) a.scores[t * a.E + e0 + j] = s;
+                if (!by_logit) c = no_nan(s + bias[j]);
+            }
+            key[j] = j < n ? order(c) : 0u;
+        }
+        bool sure = true;
+        const float err = (softmax ? 0x1p-24f + 0x1p-19f * rz : 0x1p-21f) + 0x1p-23f * size;
+        if (groups) {
+            uint32_t t1 = 0, t2 = 0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                t2 = max(t2, min(t1, key[j]));
+                t1 = max(t1, key[j]);
+            }
+            for (int off = L.per >> 1; off >= 1; off >>= 1) {
+                const uint32_t o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
+                t2 = max(max(t2, o2), min(t1, o1));
+                t1 = max(t1, o1);
+            }
+            const bool mine = lane / L.per < a.n_group;
+            const uint32_t score = !mine ? 0 : two ? order(no_nan(value_of(t1) + value_of(t2))) : t1;
+            int better = 0;
+            for (int g = 0; g < a.n_group; ++g) {
+                const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)score, g * L.per);
+                better += o > score || (o == score && g < lane / L.per);
+            }
+            const bool kept = mine && better < a.topk_group;
+            if (!by_logit && a.topk_group < a.n_group) {       // the worst kept and the best other
+                const float lo = value_of(~wave_most(kept ? ~score : 0u)), hi = value_of(wave_most(mine && !kept ? score : 0u));
+                sure = lo - hi > (two ? 4.f * err + 0x1p-22f * size : 2.f * err);      // (equal infinities: not sure)
+            }
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) key[j] = kept ? key[j] : 0u;
+        }
+        int sel = 0;                                           // lane r < k: the r-th choice
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
+        float above = INFINITY;
+        for (int r = 0;; ++r) {
+            const uint32_t most = wave_most(best);
+            if (!by_logit && most) {
+                const float c = value_of(most);
+                if (r > 0) sure = sure && above - c > 2.f * err;
+                above = c;
+            }
+            if (r == a.k) break;
+            // the lowest lane that has it, and the lowest place there
+            const int owner = __builtin_ctzll(__ballot(best == most));
+            int at = 0;
+#pragma unroll
+            for (int j = EPL - 1; j >= 0; --j)
+                if (key[j] == most) at = j;
+            at = __builtin_amdgcn_readlane(at, owner);
+            best = 0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                if (j == at && lane == owner) key[j] = 0u;
+                best = max(best, key[j]);
+            }
+            const int e = __builtin_amdgcn_readlane(e0, owner) + at;
+            if (lane == r) sel = e;
+        }
+        if (!sure) sel = choose64<EPL>(a, L, row, lane);
+        // the weights
+        const bool in = lane < a.k;
+        const float l = in ? no_nan(row[sel]) : -INFINITY;
+        float p;
+        if (a.renorm) {
+            // only the ratios of the chosen matter: the scores relative to the largest of
+            // them, so that none is lost where all are tiny
+            const float ml = wave_most(l);
+            if (softmax) p = soft_exp(l, ml);
+            else {
+                const float c = fminf(ml, 0.f);
+                p = l == -INFINITY ? 0.f : l < 0.f ? expf(l - c) / (1.f + expf(l)) : expf(-c) / (1.f + expf(-l));
+            }
+            const float sum = wave_total(in ? p : 0.f);
+            p = sum > 0.f ? p / sum : 0.f;
+        } else {
+            p = softmax ? soft_exp(l, m) * rz : 1.f / (1.f + expf(-l));
+        }
+        if (in) {
+            a.idx[t * a.k + lane] = sel;
+            a.w[t * a.k + lane] = a.scale * p;
+        }
     }
 }
 
@@ -276,19 +401,28 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
 }
 
 // ================================================================ launchers
+template <int EPL>
+static int route_(const RouteArgs& a, const Lanes& L, hipStream_t st) {
+    const bool vec = a.E % 4 == 0 && L.Eg % 4 == 0 && (uintptr_t)a.logits % 16 == 0;
+    // (from 8192 blocks on a wave goes over several tokens and keeps the bias)
+    const int64_t blocks = ((int64_t)a.T + 3) / 4;
+    const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
+    if (a.scores) k_route<EPL, true><<<grid, 256, 0, st>>>(a, L, vec);
+    else k_route<EPL, false><<<grid, 256, 0, st>>>(a, L, vec);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
 int launch_route(const RouteArgs& a, hipStream_t st) {
     ProfScope prof_(st, "route");
     Lanes L{64, a.E / a.n_group};
     for (int g = 1; g < a.n_group; g <<= 1) L.per >>= 1;
     const int need = (L.Eg + L.per - 1) / L.per;
-    const dim3 grid = rows_grid(((int64_t)a.T + 3) / 4);
-    if (need <= 1) k_route<1><<<grid, 256, 0, st>>>(a, L);
-    else if (need <= 2) k_route<2><<<grid, 256, 0, st>>>(a, L);
-    else if (need <= 4) k_route<4><<<grid, 256, 0, st>>>(a, L);
-    else if (need <= 8) k_route<8><<<grid, 256, 0, st>>>(a, L);
-    else if (need <= 16) k_route<16><<<grid, 256, 0, st>>>(a, L);
-    else k_route<32><<<grid, 256, 0, st>>>(a, L);
-    return hipGetLastError() == hipSuccess ? 0 : -1;
+    if (need <= 1) return route_<1>(a, L, st);
+    if (need <= 2) return route_<2>(a, L, st);
+    if (need <= 4) return route_<4>(a, L, st);
+    if (need <= 8) return route_<8>(a, L, st);
+    if (need <= 16) return route_<16>(a, L, st);
+    return route_<32>(a, L, st);
 }
 
 int launch_route_bwd(const RouteArgs& a, hipStream_t st) {
