@@ -3,6 +3,8 @@
 // the gradient of the logits (include/moe.h: moe_route_forward).  The layer's
 // own routing, plain top-k of the logits, is k_topk_route; the pages feed it
 // Gaussian logits (alphalab.site "Mixture-of-Kittens" sections 一 and 四).
+#include <cfloat>
+
 #include "common.h"
 #include "launch.h"
 #include "profile.h"
@@ -21,8 +23,11 @@ __device__ __forceinline__ float no_nan(float v) { return v == v ? v : -INFINITY
 __device__ __forceinline__ double no_nan(double v) { return v == v ? v : -(double)INFINITY; }
 
 // exp(v - m) with m the largest of the v: 1 for the largest (infinite ones
-// too), 0 for -inf
-__device__ __forceinline__ float soft_exp(float v, float m) { return v == -INFINITY ? 0.f : v == m ? 1.f : expf(v - m); }
+// too), 0 for -inf (where all are)
+__device__ __forceinline__ float soft_exp(float v, float m) {
+    const float top = fmaxf(m, -FLT_MAX);
+    return expf(v == top ? 0.f : v - top);
+}
 __device__ __forceinline__ double soft_exp(double v, double m) {
     return v == -(double)INFINITY ? 0.0 : v == m ? 1.0 : exp(v - m);
 }
@@ -45,68 +50,6 @@ __device__ __forceinline__ int first_expert(const Lanes& L, int n_group, int lan
 }
 
 // ================================================================ forward
-// The choice in 64 bits, for the tokens whose scores 32 bits cannot tell apart: k
-// rounds of a wave's largest, the lower index first.  sel: lane r has the r-th choice.
-template <int EPL>
-__device__ __forceinline__ int choose64(const RouteArgs& a, const Lanes& L, const float* row, int lane) {
-    int n;
-    const int e0 = first_expert<EPL>(L, a.n_group, lane, n);
-    const bool two = a.n_group > 1 && a.group_top == 2;
-    double key[EPL], z = 0.0;
-    float m = -INFINITY;
-    for (int j = 0; j < n; ++j) m = fmaxf(m, no_nan(row[e0 + j]));
-    m = wave_most(m);
-    if (a.score == SCORE_SOFTMAX) {
-        for (int j = 0; j < n; ++j) z += soft_exp((double)no_nan(row[e0 + j]), (double)m);
-        z = wave_sum(z);
-    }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        if (j >= n) continue;
-        const double v = no_nan(row[e0 + j]);
-        const double s = a.score == SCORE_SIGMOID ? 1.0 / (1.0 + exp(-v)) : z > 0.0 ? soft_exp(v, (double)m) / z : 0.0;
-        key[j] = no_nan(s + (a.bias ? (double)a.bias[e0 + j] : 0.0));
-    }
-    uint32_t open = n >= 32 ? ~0u : (1u << n) - 1u;        // the places still to be chosen
-    if (a.n_group > 1) {
-        double t1 = -(double)INFINITY, t2 = t1;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            if (j >= n) continue;
-            t2 = fmax(t2, fmin(t1, key[j]));
-            t1 = fmax(t1, key[j]);
-        }
-        for (int off = L.per >> 1; off >= 1; off >>= 1) {
-            const double o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
-            t2 = fmax(fmax(t2, o2), fmin(t1, o1));
-            t1 = fmax(t1, o1);
-        }
-        const double score = two ? no_nan(t1 + t2) : t1;
-        int better = 0;
-        for (int g = 0; g < a.n_group; ++g) {
-            const double o = __shfl(score, g * L.per);
-            better += o > score || (o == score && g < lane / L.per);
-        }
-        if (better >= a.topk_group) open = 0;
-    }
-    int sel = 0;
-    for (int r = 0; r < a.k; ++r) {
-        double b = -(double)INFINITY;
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if ((open >> j & 1u) && (at == 0x7fffffff || key[j] > b)) { b = key[j]; at = e0 + j; }
-        for (int off = 32; off >= 1; off >>= 1) {
-            const double ob = __shfl_xor(b, off);
-            const int oat = __shfl_xor(at, off);
-            if (oat != 0x7fffffff && (at == 0x7fffffff || ob > b || (ob == b && oat < at))) { b = ob; at = oat; }
-        }
-        if (n > 0 && at >= e0 && at < e0 + n) open &= ~(1u << (at - e0));
-        if (lane == r) sel = at;
-    }
-    return sel;
-}
-
 // Whole numbers in the order of floats (-0 as 0, NaN as -inf), none of them 0
 __device__ __forceinline__ uint32_t order(float v) {
     const int b = __float_as_int(v + 0.f);
@@ -129,6 +72,90 @@ __device__ __forceinline__ uint32_t wave_most(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
+// ---------------------------------------------------------------- where 32 bits do not tell
+// The scores of a token in 64 bits
+struct Exact {
+    double m, z;
+    __device__ __forceinline__ double operator()(const RouteArgs& a, const float* row, int e) const {
+        const double v = no_nan(row[e]);
+        const double s = a.score == SCORE_SIGMOID ? 1.0 / (1.0 + exp(-v)) : z > 0.0 ? soft_exp(v, m) / z : 0.0;
+        return no_nan(s + (a.bias ? (double)a.bias[e] : 0.0));
+    }
+};
+
+// The groups kept by their scores in 64 bits: whether this lane's is
+__device__ __forceinline__ bool kept64(const RouteArgs& a, const Lanes& L, const Exact& exact, const float* row, int e0,
+                                       int n, int lane) {
+    double t1 = -(double)INFINITY, t2 = t1;
+    for (int j = 0; j < n; ++j) {
+        const double c = exact(a, row, e0 + j);
+        t2 = fmax(t2, fmin(t1, c));
+        t1 = fmax(t1, c);
+    }
+    for (int off = L.per >> 1; off >= 1; off >>= 1) {
+        const double o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
+        t2 = fmax(fmax(t2, o2), fmin(t1, o1));
+        t1 = fmax(t1, o1);
+    }
+    const double score = a.group_top == 2 ? no_nan(t1 + t2) : t1;
+    int better = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+        const double o = __shfl(score, g * L.per);
+        better += o > score || (o == score && g < lane / L.per);
+    }
+    return better < a.topk_group;
+}
+
+// The choice among the places of `key`, each off by less than err: k rounds of the largest,
+// and where others are as close to it as both errors, the largest of those in 64 bits, the
+// lower index first.  kept: 1 or 0, or -1 where the groups are not sure either.
+template <int EPL>
+__device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, const float* row, const uint32_t (&key)[EPL],
+                                            float err, int e0, int n, int kept, int lane) {
+    Exact exact{0.0, 0.0};
+    if (a.score == SCORE_SOFTMAX) {
+        float m = -INFINITY;
+        for (int j = 0; j < n; ++j) m = fmaxf(m, no_nan(row[e0 + j]));
+        exact.m = wave_most(m);
+        for (int j = 0; j < n; ++j) exact.z += soft_exp((double)no_nan(row[e0 + j]), exact.m);
+        exact.z = wave_sum(exact.z);
+    }
+    if (kept < 0) kept = kept64(a, L, exact, row, e0, n, lane);
+    uint32_t open = !kept ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;       // the places still to be chosen
+    int sel = 0;
+    for (int r = 0; r < a.k; ++r) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) best = max(best, open >> j & 1u ? key[j] : 0u);
+        best = wave_most(best);
+        const float c = value_of(best);
+        const uint32_t thr = fabsf(c) < INFINITY ? order(c - 3.f * err) : best;       // (c - 3 err is rounded itself)
+        uint32_t close = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) close |= (key[j] >= thr ? 1u : 0u) << j;
+        close &= open;
+        int at = close ? e0 + __builtin_ctz(close) : 0x7fffffff;
+        const uint64_t who = __ballot(close != 0);
+        if ((__ballot((close & (close - 1)) != 0) || (who & (who - 1))) && fabsf(c) < INFINITY) {
+            double b = -(double)INFINITY;
+            for (uint32_t left = close; left; left &= left - 1) {
+                const double x = exact(a, row, e0 + __builtin_ctz(left));
+                if (x > b) { b = x; at = e0 + __builtin_ctz(left); }
+            }
+            for (int off = 32; off >= 1; off >>= 1) {
+                const double ob = __shfl_xor(b, off);
+                const int oat = __shfl_xor(at, off);
+                if (ob > b || (ob == b && oat < at)) { b = ob; at = oat; }
+            }
+        } else {
+            at = lane_value(at, __builtin_ctzll(who));
+        }
+        if (n > 0 && at >= e0 && at < e0 + n) open &= ~(1u << (at - e0));
+        if (lane == r) sel = at;
+    }
+    return sel;
+}
+
 // The choice is the one in 64 bits.  Without a bias (and sums of two in the groups) it is
 // that of the logits, exactly.  Else the scores are computed in 32 bits, each off by
 // less than `err`, and where two that the choice tells apart, neighbours among the k + 1
@@ -148,134 +175,152 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
     const bool softmax = a.score == SCORE_SOFTMAX;
     const bool groups = a.n_group > 1, two = groups && a.group_top == 2;
     const bool by_logit = !a.bias && !two;
-    float bias[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) bias[j] = a.bias && j < n ? a.bias[e0 + j] : 0.f;
-    float size = 0.f;                                          // 1 + the largest finite |bias|
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-        if (fabsf(bias[j]) < INFINITY) size = fmaxf(size, fabsf(bias[j]));
-    size = a.bias ? 1.f + wave_most(size) : 1.f;
-    for (int64_t t = block_number() * 4 + wave_id(); t < a.T; t += (int64_t)gridDim.x * gridDim.y * 4) {
-        const float* row = a.logits + t * a.E;
-        float v[EPL], m = -INFINITY;
-        if (EPL % 4 == 0 && vec) {                             // (n is a multiple of 4)
+    const int64_t t = block_number() * 4 + wave_id();
+    if (t >= a.T) return;
+    const float* row = a.logits + t * a.E;
+    // (vec: rows, groups and bias in whole chunks of four)
+    auto load = [&](const float* p, float none, float (&to)[EPL]) {
+        if (EPL % 4 == 0 && vec) {
 #pragma unroll
             for (int j = 0; j + 3 < EPL; j += 4) {
-                f32x4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (j < n) q = *(const f32x4*)(row + e0 + j);
+                f32x4 q = {none, none, none, none};
+                if (j < n) q = *(const f32x4*)(p + e0 + j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[j + i] = no_nan(q[i]);
+                for (int i = 0; i < 4; ++i) to[j + i] = q[i];
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) v[j] = j < n ? no_nan(row[e0 + j]) : -INFINITY;
+            for (int j = 0; j < EPL; ++j) to[j] = j < n ? p[e0 + j] : none;
         }
-        float z = 0.f;
-        if (softmax && (SCORES || !by_logit || !a.renorm)) {
+    };
+    float v[EPL], bias[EPL];
+    load(row, -INFINITY, v);
+    float m = -INFINITY, size = 1.f;                           // size: 1 + the largest finite |bias|
+    if (a.bias) {
+        load(a.bias, 0.f, bias);
+        float most = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) m = fmaxf(m, v[j]);
-            m = wave_most(m);
+        for (int j = 0; j < EPL; ++j) most = fmaxf(most, fabsf(bias[j]) < INFINITY ? fabsf(bias[j]) : 0.f);
+        size = 1.f + wave_most(most);
+    } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) z += soft_exp(v[j], m);
-            z = wave_total(z);
+        for (int j = 0; j < EPL; ++j) bias[j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) v[j] = no_nan(v[j]);
+    float z = 0.f;
+    if (softmax && (SCORES || !by_logit || !a.renorm)) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) m = fmaxf(m, v[j]);
+        m = wave_most(m);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) z += soft_exp(v[j], m);
+        z = wave_total(z);
+    }
+    const float rz = z > 0.f ? 1.f / z : 0.f;
+    uint32_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        float c = v[j];
+        if (SCORES || !by_logit) {
+            float s;
+            if (softmax) s = soft_exp(v[j], m) * rz;
+            else if (SCORES) s = 1.f / (1.f + expf(-v[j]));
+            else s = __builtin_amdgcn_rcpf(1.f + __expf(-v[j]));
+            if (SCORES && j < n) a.scores[t * a.E + e0 + j] = s;
+            if (!by_logit) c = no_nan(s + bias[j]);
         }
-        const float rz = z > 0.f ? 1.f / z : 0.f;
-        uint32_t key[EPL];
+        key[j] = j < n ? order(c) : 0u;
+    }
+    const float err = (softmax ? 0x1p-24f + 0x1p-19f * rz : 0x1p-21f) + 0x1p-23f * size;
+    bool kept = true, sure = true;
+    if (groups) {
+        uint32_t t1 = 0, t2 = 0;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            float c = v[j];
-            if (SCORES || !by_logit) {
-                float s;
-                if (softmax) s = soft_exp(v[j], m) * rz;
-                else if (SCORES) s = 1.f / (1.f + expf(-v[j]));
-                else s = __builtin_amdgcn_rcpf(1.f + __expf(-v[j]));
-                if (SCORES && j < n) a.scores[t * a.E + e0 + j] = s;
-                if (!by_logit) c = no_nan(s + bias[j]);
-            }
-            key[j] = j < n ? order(c) : 0u;
+            t2 = max(t2, min(t1, key[j]));
+            t1 = max(t1, key[j]);
         }
-        bool sure = true;
-        const float err = (softmax ? 0x1p-24f + 0x1p-19f * rz : 0x1p-21f) + 0x1p-23f * size;
-        if (groups) {
-            uint32_t t1 = 0, t2 = 0;
+        for (int off = L.per >> 1; off >= 1; off >>= 1) {
+            const uint32_t o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
+            t2 = max(max(t2, o2), min(t1, o1));
+            t1 = max(t1, o1);
+        }
+        const bool mine = lane / L.per < a.n_group;
+        const uint32_t score = !mine ? 0 : two ? order(no_nan(value_of(t1) + value_of(t2))) : t1;
+        int better = 0;
+        for (int g = 0; g < a.n_group; ++g) {
+            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)score, g * L.per);
+            better += o > score || (o == score && g < lane / L.per);
+        }
+        kept = mine && better < a.topk_group;
+        if (!by_logit && a.topk_group < a.n_group) {       // the worst kept and the best other
+            const float lo = value_of(~wave_most(kept ? ~score : 0u)), hi = value_of(wave_most(mine && !kept ? score : 0u));
+            sure = lo - hi > (two ? 4.f * err + 0x1p-22f * size : 2.f * err);      // (equal infinities: not sure)
+        }
+    }
+    // Rounds of the wave's largest.  A lane has its two largest at hand and looks at its
+    // keys again when both are taken: what is left of them comes after the last one taken.
+    int sel = 0;                                           // lane r < k: the r-th choice
+    const bool groups_sure = sure;
+    if (sure) {
+        uint32_t b1 = 0, b2 = 0;
+        int e1 = 0, e2 = 0;
+        auto largest_two = [&](uint32_t last, int e) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
-                t2 = max(t2, min(t1, key[j]));
-                t1 = max(t1, key[j]);
+                const bool after = (key[j] < last) | ((key[j] == last) & (e0 + j > e));
+                const uint32_t c = after ? key[j] : 0u;
+                const bool first = c > b1;
+                e2 = first ? e1 : c > b2 ? e0 + j : e2;
+                b2 = max(b2, min(b1, c));
+                e1 = first ? e0 + j : e1;
+                b1 = max(b1, c);
             }
-            for (int off = L.per >> 1; off >= 1; off >>= 1) {
-                const uint32_t o1 = __shfl_xor(t1, off), o2 = __shfl_xor(t2, off);
-                t2 = max(max(t2, o2), min(t1, o1));
-                t1 = max(t1, o1);
-            }
-            const bool mine = lane / L.per < a.n_group;
-            const uint32_t score = !mine ? 0 : two ? order(no_nan(value_of(t1) + value_of(t2))) : t1;
-            int better = 0;
-            for (int g = 0; g < a.n_group; ++g) {
-                const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)score, g * L.per);
-                better += o > score || (o == score && g < lane / L.per);
-            }
-            const bool kept = mine && better < a.topk_group;
-            if (!by_logit && a.topk_group < a.n_group) {       // the worst kept and the best other
-                const float lo = value_of(~wave_most(kept ? ~score : 0u)), hi = value_of(wave_most(mine && !kept ? score : 0u));
-                sure = lo - hi > (two ? 4.f * err + 0x1p-22f * size : 2.f * err);      // (equal infinities: not sure)
-            }
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) key[j] = kept ? key[j] : 0u;
-        }
-        int sel = 0;                                           // lane r < k: the r-th choice
-        uint32_t best = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
-        float above = INFINITY;
+        };
+        if (kept) largest_two(~0u, 0);
+        float above = INFINITY, gap = INFINITY;            // (equal infinities need no 64 bits)
         for (int r = 0;; ++r) {
-            const uint32_t most = wave_most(best);
+            const uint32_t most = wave_most(b1);
             if (!by_logit && most) {
-                const float c = value_of(most);
-                if (r > 0) sure = sure && above - c > 2.f * err;
-                above = c;
+                gap = fminf(gap, above - value_of(most));
+                above = value_of(most);
             }
             if (r == a.k) break;
-            // the lowest lane that has it, and the lowest place there
-            const int owner = __builtin_ctzll(__ballot(best == most));
-            int at = 0;
-#pragma unroll
-            for (int j = EPL - 1; j >= 0; --j)
-                if (key[j] == most) at = j;
-            at = __builtin_amdgcn_readlane(at, owner);
-            best = 0;
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                if (j == at && lane == owner) key[j] = 0u;
-                best = max(best, key[j]);
-            }
-            const int e = __builtin_amdgcn_readlane(e0, owner) + at;
+            const int owner = __builtin_ctzll(__ballot(b1 == most));
+            const int e = lane_value(e1, owner);
             if (lane == r) sel = e;
-        }
-        if (!sure) sel = choose64<EPL>(a, L, row, lane);
-        // the weights
-        const bool in = lane < a.k;
-        const float l = in ? no_nan(row[sel]) : -INFINITY;
-        float p;
-        if (a.renorm) {
-            // only the ratios of the chosen matter: the scores relative to the largest of
-            // them, so that none is lost where all are tiny
-            const float ml = wave_most(l);
-            if (softmax) p = soft_exp(l, ml);
-            else {
-                const float c = fminf(ml, 0.f);
-                p = l == -INFINITY ? 0.f : l < 0.f ? expf(l - c) / (1.f + expf(l)) : expf(-c) / (1.f + expf(-l));
+            if (lane == owner) {
+                b1 = b2;
+                e1 = e2;
+                b2 = 0;
             }
-            const float sum = wave_total(in ? p : 0.f);
-            p = sum > 0.f ? p / sum : 0.f;
-        } else {
-            p = softmax ? soft_exp(l, m) * rz : 1.f / (1.f + expf(-l));
+            if (EPL > 2 && lane_value((int)b1, owner) == 0 && lane == owner) largest_two(most, e);
         }
-        if (in) {
-            a.idx[t * a.k + lane] = sel;
-            a.w[t * a.k + lane] = a.scale * p;
+        sure = gap > 2.f * err;
+    }
+    if (!by_logit && !sure) sel = choose_close<EPL>(a, L, row, key, err, e0, n, groups_sure ? kept : -1, lane);
+    // the weights
+    const bool in = lane < a.k;
+    const float l = in ? no_nan(row[sel]) : -INFINITY;
+    float p;
+    if (a.renorm) {
+        // only the ratios of the chosen matter: the scores relative to the largest of
+        // them, so that none is lost where all are tiny
+        const float ml = wave_most(l);
+        if (softmax) p = soft_exp(l, ml);
+        else {
+            const float c = fminf(ml, 0.f);
+            p = l == -INFINITY ? 0.f : l < 0.f ? expf(l - c) / (1.f + expf(l)) : expf(-c) / (1.f + expf(-l));
         }
+        const float sum = wave_total(in ? p : 0.f);
+        p = sum > 0.f ? p / sum : 0.f;
+    } else {
+        p = softmax ? soft_exp(l, m) * rz : 1.f / (1.f + expf(-l));
+    }
+    if (in) {
+        a.idx[t * a.k + lane] = sel;
+        a.w[t * a.k + lane] = a.scale * p;
     }
 }
 
@@ -403,10 +448,8 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
 // ================================================================ launchers
 template <int EPL>
 static int route_(const RouteArgs& a, const Lanes& L, hipStream_t st) {
-    const bool vec = a.E % 4 == 0 && L.Eg % 4 == 0 && (uintptr_t)a.logits % 16 == 0;
-    // (from 8192 blocks on a wave goes over several tokens and keeps the bias)
-    const int64_t blocks = ((int64_t)a.T + 3) / 4;
-    const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
+    const bool vec = L.Eg % 4 == 0 && ((uintptr_t)a.logits | (uintptr_t)a.bias) % 16 == 0;
+    const dim3 grid = rows_grid(((int64_t)a.T + 3) / 4);
     if (a.scores) k_route<EPL, true><<<grid, 256, 0, st>>>(a, L, vec);
     else k_route<EPL, false><<<grid, 256, 0, st>>>(a, L, vec);
     return hipGetLastError() == hipSuccess ? 0 : -1;
