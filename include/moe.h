@@ -588,9 +588,12 @@ MOE_API moe_status moe_linear_w4_workspace_size(const moe_linear_w4_config* cfg,
  *   byte k/2 for even k, the high one for odd k; scales [K/group, N] (or [E,
  *   K/group, N]) of cfg->dtype; zeros, bytes of scales' shape, may be NULL: 8.
  *   The rest as in moe_linear_forward (no z: there is no backward).
- * The products are those of the exact code - zero, summed in fp32 over a group,
- * and a group's sum is multiplied by its scale in fp32: the weights are rounded
- * nowhere.  A scale of 0 switches a group off only where x is finite. */
+ * The weights are rounded nowhere: whole numbers times x, summed in fp32 over a
+ * group, and the group's sum times its scale in fp32.  The whole numbers are
+ * code - zero; for bf16 without zeros they may be the codes, with 8 times the
+ * group's sum of x taken off: the fp32 rounding is then that of sums of at most
+ * 16 |x| scale, also where code is 8 throughout, and a row with an infinite x is NaN.
+ * A scale of 0 switches a group off only where x is finite. */
 MOE_API moe_status moe_linear_w4_forward(const moe_linear_w4_config* cfg, const int32_t* offsets, const void* x,
                                          const void* codes, const void* scales, const void* zeros,
                                          const void* bias, const void* residual, void* y, void* workspace,
