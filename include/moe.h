@@ -298,7 +298,10 @@ MOE_API moe_status moe_router_backward(const moe_config* cfg, const void* x, con
  * router-weighted reduction in a fixed order).
  *   x [T, H] bf16; y [T, H] bf16 (written);
  *   y_t = FFN_shared(x_t) + sum_{j=0..k-1} w[t,j] * o_(t,j), accumulated in
- *   fp32 in that order and rounded to bf16 once.
+ *   fp32 in that order and rounded to bf16 once.  A slot without a row (see
+ *   moe_schedule_from_topk) adds nothing, here and to moe_backward's dx, has
+ *   dw 0 and sets MOE_DEVERR_BAD_ROW; y and dx of a token without any are 0
+ *   or the shared expert's.
  *   saved: g, u written for the backward.
  * Macrobatches are processed in order through the ring buffer; every
  * dynamic size stays on the device ([AREX] second decision). */

@@ -283,11 +283,17 @@ struct Ptrs {
 // gradient) is its one routed row, so the down GEMM (and the gate/up input
 // gradient) write it straight to the token's row of y (dx) and the combine
 // (reverse-dispatch) pass is skipped.  The single fp32 term rounds once
-// either way, so the bits are those of the combine.
+// either way, so the bits are those of the combine.  A token without a row
+// gets its zeros beside the tile prefix, before the GEMMs.
 bool top1_direct(const Geom& g) { return g.k == 1 && !g.shared; }
 
 RowDest token_rows(const Geom& g, const moe_sched* s, int grow0) {
     return top1_direct(g) ? RowDest{s->slot_of_row, grow0, g.k, g.S} : RowDest{nullptr, 0, 1, 0};
+}
+
+DirectRows direct_rows(const Geom& g, const moe_sched* s, int m, void* out) {
+    if (!top1_direct(g)) return {};
+    return {out, g.H, s->row_of_slot, s->slot_of_row, m * g.M, g.M, m * g.Sm};
 }
 
 // Where macrobatch m's gate and up projections are kept for the backward:
@@ -354,8 +360,9 @@ moe_status forward_mx(const Geom& g, const Layout& L, const Ptrs& P, const moe_s
         const bool big = !g.w4 && tm == 128 && g.I % (kBig / 2) == 0;
         int32_t* tsmall = (int32_t*)(P.ws + L.tile_split) + (size_t)m * 2 * (g.E + 1);
         int32_t* tbig = tsmall + (g.E + 1);
-        if (big ? launch_tile_prefix_split(off, g.E, g.Sm, tm, toff, kBigRows, kBig, tsmall, tbig, err, st)
-                : launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st))
+        const DirectRows direct = direct_rows(g, sched, m, y);
+        if (big ? launch_tile_prefix_split(off, g.E, g.Sm, tm, toff, kBigRows, kBig, tsmall, tbig, err, st, direct)
+                : launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st, direct))
             return MOE_ERR_HIP;
         GroupRows grp{off, toff, g.E, g.Sm, 0, err, nullptr, 0, tm};
         GroupRows grp_split = grp;
@@ -455,7 +462,7 @@ moe_status backward_mx(const Geom& g, const Layout& L, const Ptrs& P, const moe_
         const int grow0 = m * g.Sm, t0 = m * g.M;
         const int32_t* off = sched->offsets + (size_t)m * (g.E + 1);
         int32_t* toff = (int32_t*)(ws + L.tile_off) + (size_t)m * (g.E + 1);
-        if (launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st)) return MOE_ERR_HIP;
+        if (launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st, direct_rows(g, sched, m, dx))) return MOE_ERR_HIP;
         if (launch_tile_prefix(off, g.E, g.Sm, 32, blk, err, st)) return MOE_ERR_HIP;
         GroupRows grp{off, toff, g.E, g.Sm, 0, err, nullptr, 0, tm};
         const GU gu = gu_routed(g, L, P, saved, m, false);
@@ -808,8 +815,9 @@ moe_status moe_forward(const moe_config* cfg, const moe_sched* sched, const void
         const bool big = tm == 128 && g.H % kBig == 0 && g.I % (kBig / 2) == 0;
         int32_t* tsmall = (int32_t*)((char*)workspace + L.tile_split) + (size_t)m * 2 * (g.E + 1);
         int32_t* tbig = tsmall + (g.E + 1);
-        if (big ? launch_tile_prefix_split(off, g.E, g.Sm, tm, toff, kBigRows, kBig, tsmall, tbig, err, st)
-                : launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st))
+        const DirectRows direct = direct_rows(g, sched, m, y);
+        if (big ? launch_tile_prefix_split(off, g.E, g.Sm, tm, toff, kBigRows, kBig, tsmall, tbig, err, st, direct)
+                : launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st, direct))
             return MOE_ERR_HIP;
         // dispatch fused into the gate/up GEMM: its operand loads gather each
         // routed row from the row of its token
@@ -917,8 +925,9 @@ moe_status moe_backward(const moe_config* cfg, const moe_sched* sched, const moe
         const bool big = tm == 128 && g.H % kBig == 0 && g.I % kBig == 0;
         int32_t* tsmall = (int32_t*)((char*)workspace + L.tile_split) + (size_t)m * 2 * (g.E + 1);
         int32_t* tbig = tsmall + (g.E + 1);
-        if (big ? launch_tile_prefix_split(off, g.E, g.Sm, tm, toff, kBigRows, kBig, tsmall, tbig, err, st)
-                : launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st))
+        const DirectRows direct = direct_rows(g, sched, m, dx);
+        if (big ? launch_tile_prefix_split(off, g.E, g.Sm, tm, toff, kBigRows, kBig, tsmall, tbig, err, st, direct)
+                : launch_tile_prefix(off, g.E, g.Sm, tm, toff, err, st, direct))
             return MOE_ERR_HIP;
         GroupRows grp{off, toff, g.E, g.Sm, 0, err, nullptr, 0, tm};
         GroupRows grp_split = grp;

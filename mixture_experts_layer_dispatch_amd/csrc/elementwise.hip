@@ -198,6 +198,11 @@ __global__ __launch_bounds__(256) void k_softmax_bwd(const float* __restrict__ p
 // the same prefix over the groups below big_rows rows only (small, TM-row
 // tiles) and over the others only (big, big_tm-row tiles), for GEMMs that
 // take the large groups in a tile form of their own.  One block, E <= 1024.
+//
+// Further blocks (direct.out), beside it in one launch: the tokens whose one
+// row the last GEMM writes straight to the output, 1024 a block.  Those that no
+// row is for (the table names an expert outside the layer) are zeroed here,
+// as a combine would leave them.
 __device__ __forceinline__ int block_excl_scan(int n, int32_t* wsum, int& total) {
     const int lane = lane_id(), wv = threadIdx.x >> 6;
     int incl = n;
@@ -219,8 +224,24 @@ __device__ __forceinline__ int block_excl_scan(int n, int32_t* wsum, int& total)
 __global__ __launch_bounds__(1024) void k_tile_prefix(const int32_t* __restrict__ offsets, int E,
                                                       int rows, int TM, int32_t* __restrict__ tile_off,
                                                       int big_rows, int big_tm, int32_t* __restrict__ small,
-                                                      int32_t* __restrict__ big, int32_t* __restrict__ err) {
+                                                      int32_t* __restrict__ big, DirectRows direct,
+                                                      int32_t* __restrict__ err) {
     __shared__ int32_t wsum[16];
+    if (blockIdx.x > 0) {
+        const int i0 = ((int)blockIdx.x - 1) * 1024 + wave_id() * 64, i = i0 + lane_id();
+        bool none = false;
+        if (i < direct.tokens) {
+            const int t = direct.t0 + i, r = direct.row_of_slot[t] - direct.ring_row0;
+            const bool in = (unsigned)r < (unsigned)rows;
+            if (!in) raise_err(err, ERR_BAD_ROW);
+            none = !in || direct.slot_of_row[direct.ring_row0 + r] != t;
+        }
+        for (uint64_t m = __ballot(none); m; m &= m - 1) {
+            uint4* out = (uint4*)direct.out + (size_t)(direct.t0 + i0 + __builtin_ctzll(m)) * (direct.H / 8);
+            for (int c = lane_id(); c < direct.H / 8; c += 64) out[c] = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
     const int e = threadIdx.x;
     int cnt = 0;
     if (e < E) {
@@ -310,16 +331,17 @@ int launch_softmax_bwd(const float* part, int P, const int32_t* row_of_slot, con
 }
 
 int launch_tile_prefix(const int32_t* offsets, int E, int rows, int TM, int32_t* tile_off,
-                       int32_t* err, hipStream_t st) {
-    return launch_tile_prefix_split(offsets, E, rows, TM, tile_off, 0, 0, nullptr, nullptr, err, st);
+                       int32_t* err, hipStream_t st, const DirectRows& direct) {
+    return launch_tile_prefix_split(offsets, E, rows, TM, tile_off, 0, 0, nullptr, nullptr, err, st, direct);
 }
 
 int launch_tile_prefix_split(const int32_t* offsets, int E, int rows, int TM, int32_t* tile_off,
                              int big_rows, int big_tm, int32_t* small, int32_t* big, int32_t* err,
-                             hipStream_t st) {
+                             hipStream_t st, const DirectRows& direct) {
     ProfScope prof_(st, "tile_prefix");
     if (E > 1024 || (big && (!small || big_rows <= 0 || big_tm <= 0))) return -1;
-    k_tile_prefix<<<1, 1024, 0, st>>>(offsets, E, rows, TM, tile_off, big_rows, big_tm, small, big, err);
+    const int blocks = 1 + (direct.out ? (direct.tokens + 1023) / 1024 : 0);
+    k_tile_prefix<<<blocks, 1024, 0, st>>>(offsets, E, rows, TM, tile_off, big_rows, big_tm, small, big, direct, err);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -331,13 +331,24 @@ int launch_rd_reduce(const void* dxd, int H, const int32_t* row_of_slot, int t0,
 int launch_softmax_bwd(const float* part, int P, const int32_t* row_of_slot, const int32_t* idx,
                        const float* w, int t0, int t1, int k, int E, int ring_row0, int ring_rows,
                        float* dw, float* d_logits, int32_t* err, hipStream_t st);
+// The tokens of a macrobatch whose rows the last GEMM writes to out itself (one
+// expert a token, no combine); out null: none are.
+struct DirectRows {
+    void* out;                  // [T, H] bf16
+    int H;
+    const int32_t* row_of_slot;
+    const int32_t* slot_of_row;
+    int t0, tokens;
+    int ring_row0;
+};
+// tile_off, and zeros in the rows of direct.out that no row is for
 int launch_tile_prefix(const int32_t* offsets, int E, int rows, int TM, int32_t* tile_off,
-                       int32_t* err, hipStream_t st);
+                       int32_t* err, hipStream_t st, const DirectRows& direct = {});
 // the same, plus the prefixes over the groups below big_rows rows (TM-row
 // tiles) and over the rest (big_tm-row tiles)
 int launch_tile_prefix_split(const int32_t* offsets, int E, int rows, int TM, int32_t* tile_off,
                              int big_rows, int big_tm, int32_t* small, int32_t* big, int32_t* err,
-                             hipStream_t st);
+                             hipStream_t st, const DirectRows& direct = {});
 int launch_deep_list(const int32_t* offsets, int E, int rows, int thr, int32_t* list, hipStream_t st);
 // the same, with the groups of at least big_thr rows in a list of their own
 int launch_deep_list_split(const int32_t* offsets, int E, int rows, int thr, int32_t* list, int big_thr,
