@@ -108,15 +108,47 @@ __device__ __forceinline__ void dev_act(int act, const F& f) {
 // what is taken off the codes: 8, by the sums of x; 8, exactly; zeros, exactly
 enum { W4_MID, W4_EIGHT, W4_ZEROS };
 
+// By the sums of x, an infinite x makes all outputs of its row NaN, and x beyond 2^128 / (15 G)
+// can take sums of the codes past fp32's range where those of code - 8 are inside it.  No sum that
+// has left it comes back, so what comes out finite is right, and the waves that have other
+// sums replace them by exact ones, straight from memory.  (x is seldom so: 2048 x 4096 x 4096
+// takes 76 us, and 518 with an infinite x in one row or all; 4 rows 6 and 29.)
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
 // ================================================================ few rows
+// Exact sums of 16 rows from row0 by 16 columns from col0: lane j + 16 q has row j's
+// columns 4 q .. 4 q + 3.
+template <class D, int G>
+__device__ __forceinline__ f32x4 w4_exact16(const W4Args& a, int e, int row0, int hi, int col0) {
+    const LinFwdArgs& f = a.f;
+    const int j = lane_id() & 15, q = lane_id() >> 4, groups = f.K / G;
+    const uint16_t* x = f.x + (int64_t)min(row0 + j, hi - 1) * f.K + 8 * q;
+    const uint8_t* codes = a.codes + ((int64_t)e * f.N + min(col0 + j, f.N - 1)) * (f.K / 2) + 4 * q;
+    const uint16_t* scales = a.scales + (int64_t)e * groups * f.N + min(col0 + 4 * q, f.N - 4);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < groups; ++g) {
+        f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < G / 32; ++s) {
+            const int k = g * G + 32 * s;
+            part = D::mfma(codes8<D>(*(const uint32_t*)(codes + k / 2), 8.f), *(const uint4*)(x + k), part);
+        }
+        const f32x4 scale = unpack4<D>(*(const uint2*)(scales + (int64_t)g * f.N));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(scale[r], part[r], acc[r]);
+    }
+    return acc;
+}
+
 // A handful of rows: the codes are read once and everything else is small, so the
 // product is a stream.  A block computes 16 rows by 16 NB columns; its W waves split
 // the reduction in units of 128 inputs, whose codes they read straight into registers,
 // UNITS at a time.  A lane quarter reads 16 bytes of a row, 32 inputs in a row; groups of
 // 128 are multiplied in that order (word s of every quarter, and the same inputs of x,
-// to an MFMA), smaller ones are first transposed over the quarters.
+// to an MFMA), smaller ones are first transposed over the quarters.  (The second launch bound
+// keeps two blocks to a CU; 64 columns are faster without: 4096 -> 65536 27.5 us, 29.5 with it.)
 template <class D, int G, int MODE, int NB, int W, int UNITS>
-__global__ __launch_bounds__(64 * W) void k_w4_stream(W4Args a) {
+__global__ __launch_bounds__(64 * W, NB == 4 ? 1 : W / 2) void k_w4_stream(W4Args a) {
     constexpr int TN = 16 * NB, NG = 128 / G, PER = G / 32;
     __shared__ __attribute__((aligned(16))) float sums[W][16][TN + 4];
     const LinFwdArgs& f = a.f;
@@ -205,6 +237,19 @@ __global__ __launch_bounds__(64 * W) void k_w4_stream(W4Args a) {
     f32x4 v = *(const f32x4*)&sums[0][r][c];
 #pragma unroll
     for (int p = 1; p < W; ++p) v += *(const f32x4*)&sums[p][r][c];
+    if constexpr (MODE == W4_MID) {
+        const bool bad = !(finite(v[0]) && finite(v[1]) && finite(v[2]) && finite(v[3]));
+        if (__builtin_expect(__ballot(bad) != 0, 0)) {
+            for (int n = 0; n < NB; ++n) {
+                const f32x4 y = w4_exact16<D, G>(a, e, lo, hi, nt * TN + 16 * n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float t = __shfl(y[i], r + 16 * (c >> 2 & 3));
+                    if (bad && c >> 4 == n) v[i] = t;
+                }
+            }
+        }
+    }
     if (lo + r < hi && nt * TN + c < f.N) w4_out<D>(f, e, lo + r, nt * TN + c, v);
 }
 
@@ -434,6 +479,34 @@ struct W4Loop {
     }
 };
 
+// Exact sums of 32 rows from row0 by the lanes' columns over the groups from g0 to g1, in the layout
+// of the loop's (lane halves have the same 32 columns).
+template <class D, int G>
+__device__ __forceinline__ f32x16 w4_exact32(const W4Args& a, int e, int row0, int hi, int col, int g0, int g1) {
+    const LinFwdArgs& f = a.f;
+    const int j = lane_id() & 31, h = lane_id() >> 5, groups = f.K / G;
+    col = min(col, f.N - 1);
+    const uint16_t* x = f.x + (int64_t)min(row0 + j, hi - 1) * f.K + 8 * h;
+    const uint8_t* codes = a.codes + ((int64_t)e * f.N + col) * (f.K / 2) + 4 * h;
+    const uint16_t* scales = a.scales + (int64_t)e * groups * f.N + col;
+    f32x16 acc, part;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+    for (int g = g0; g < min(g1, groups); ++g) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) part[r] = 0.f;
+#pragma unroll
+        for (int s = 0; s < G / 16; ++s) {
+            const int k = g * G + 16 * s;
+            part = mfma32<D>(*(const uint4*)(x + k), codes8<D>(*(const uint32_t*)(codes + k / 2), 8.f), part);
+        }
+        const float scale = D::lo(scales[(int64_t)g * f.N]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[r] = fmaf(scale, part[r], acc[r]);
+    }
+    return acc;
+}
+
 template <class D, int G, int MODE>
 __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
     typedef W4Loop<D, G, MODE> Loop;
@@ -514,6 +587,21 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
         if (s + 6 >= l.last) break;
     }
     t2_wait<0>();                              // (the copies of the last step again)
+    if constexpr (Loop::MID) {
+        f32x4 t = {0.f, 0.f, 0.f, 0.f};        // 0, or NaN where a sum is not finite
+#pragma unroll
+        for (int i = 0; i < 64; ++i) t[i & 3] = fmaf(l.acc[i >> 5][i >> 4 & 1][i & 15], 0.f, t[i & 3]);
+        if (__builtin_expect(__ballot(t[0] + t[1] + t[2] + t[3] != 0.f) != 0, 0)) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const f32x16 y = w4_exact32<D, G>(a, e, lo + 32 * m, hi, col + n, first * Loop::NG, l.last * Loop::NG);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) l.acc[m][n][r] = finite(l.acc[m][n][r]) ? l.acc[m][n][r] : y[r];
+                }
+        }
+    }
     if (col >= f.N) return;
     if (ks > 1) {                              // k_w4_sum does the rest
         float* out = f.part + (int64_t)part * f.t.rows * f.N + col;
