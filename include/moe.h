@@ -317,7 +317,8 @@ MOE_API moe_status moe_forward(const moe_config* cfg, const moe_sched* sched, co
  *   grads: every weight gradient (overwritten, not accumulated);
  *   dw [T, k] fp32: gradient of the combine weights (written);
  *   d_logits [T, E] fp32: gradient of the logits through the top-k softmax,
- *   zero for experts a token did not choose (written; may be NULL). */
+ *   zero for experts a token did not choose, the sum over its slots for one
+ *   that a caller's table names more than once (written; may be NULL). */
 MOE_API moe_status moe_backward(const moe_config* cfg, const moe_sched* sched, const moe_saved* saved,
                         const void* x, const moe_weights* w, const void* dy, void* dx,
                         const moe_grads* grads, float* dw, float* d_logits,

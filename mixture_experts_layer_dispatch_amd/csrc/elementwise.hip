@@ -148,8 +148,8 @@ static int launch_combine_(const void* src, int H, const int32_t* row_of_slot, c
 
 // ============================================================== softmax backward
 // dw[t,j] = sum_p part[row(t,j)][p] (p ascending), then
-// d_logit[t, idx[t,j]] = w_j (dw_j - sum_i w_i dw_i), zero for other experts.
-// One wave per token.
+// d_logit[t, idx[t,j]] = w_j (dw_j - sum_i w_i dw_i), zero for other experts, the
+// sum over j for one that a caller's table names more than once.  One wave per token.
 __global__ __launch_bounds__(256) void k_softmax_bwd(const float* __restrict__ part, int P,
                                                      const int32_t* __restrict__ row_of_slot,
                                                      const int32_t* __restrict__ idx,
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(256) void k_softmax_bwd(const float* __restrict__ p
             for (int j = 0; j < k; ++j) {
                 const int ejj = __shfl(ej, j);
                 const float dlj = __shfl(dl, j);
-                if (ejj == e) v = dlj;
+                if (ejj == e) v += dlj;
             }
             if (e < E) out[e] = v;
         }

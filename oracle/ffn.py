@@ -259,10 +259,10 @@ def backward(x, wg, wu, wd, idx, w, dy, shared=None, mx=False, sched=None,
 
 
 def d_logits_dense(idx, dl_sel, E, tokens=None):
-    """Scatter the selected-logit gradients into a dense [n, E] array."""
+    """Add the selected-logit gradients up in a dense [n, E] array."""
     idx = np.asarray(idx)
     tokens = np.arange(idx.shape[0]) if tokens is None else np.asarray(tokens)
     out = np.zeros((tokens.size, E))
     rows = np.arange(tokens.size)[:, None]
-    out[rows, idx[tokens]] = dl_sel
+    np.add.at(out, (rows, idx[tokens]), dl_sel)
     return out
