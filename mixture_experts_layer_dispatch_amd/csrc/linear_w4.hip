@@ -660,6 +660,14 @@ __global__ __launch_bounds__(256) void k_w4_sum(W4Args a) {
 }
 
 // ================================================================ quantiser
+// v, not negative, as fp32 for a rounding to 16 bits: towards zero, the last bit set where
+// something is lost, so that the second rounding is v's own (the quotient of a group with
+// zeros can lie closer to halfway between two fp16 numbers than fp32 tells apart).
+__device__ __forceinline__ float to_odd(double v) {
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
 // A wave takes 512 neighbouring weights of a row, eight to a lane; a group is
 // G / 8 lanes.  Quotients of two 16-bit numbers are told from the halves between
 // whole numbers by fp32's correctly rounded division.
@@ -685,7 +693,7 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a, int64_t total) 
         hi = fmaxf(hi, __shfl_xor(hi, off));
     }
     const double range = a.zeros ? ((double)hi - lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
-    const uint32_t sbits = D::pack2((float)range, 0.f) & 0xffffu;
+    const uint32_t sbits = D::pack2(to_odd(range), 0.f) & 0xffffu;
     const float scale = D::lo(sbits);
     float zero = 8.f;
     if (a.zeros) zero = scale > 0.f ? fminf(fmaxf(rintf(-lo / scale), 0.f), 15.f) : 0.f;

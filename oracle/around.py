@@ -154,6 +154,14 @@ def linear_w4(x, codes, scales, zeros=None, bias=None, residual=None, activation
     return (y if residual is None else y + np.asarray(residual, np.float64)), z, mag
 
 
+def _to_odd(v):
+    """Values that are not negative as float32 for a rounding to 16 bits: towards zero, the last bit set
+    where something is lost, so that the second rounding is that of v."""
+    f = np.asarray(v, np.float64).astype(np.float32)
+    f = np.where(f.astype(np.float64) > v, np.nextafter(f, np.float32(0)), f)
+    return np.where(f.astype(np.float64) == v, f, (f.view(np.int32) | 1).view(np.float32))
+
+
 def w4_quantize(w, group, round_to, zeros=False):
     """(codes [.., N, K], scales [.., K / group, N], zeros or None); round_to(float32 array) gives the
     scales' type's values as float64."""
@@ -161,7 +169,7 @@ def w4_quantize(w, group, round_to, zeros=False):
     g = w.reshape(*w.shape[:-1], -1, group)
     lo, hi = np.minimum(g.min(-1), 0), np.maximum(g.max(-1), 0)
     rng = (hi - lo) / 15 if zeros else np.maximum(hi, -lo) / 7
-    s = round_to(rng.astype(np.float32))
+    s = round_to(_to_odd(rng))
     live = s > 0
     safe = np.where(live, s, 1.0)
     z = np.where(live, np.clip(np.rint(-lo / safe), 0, 15), 0) if zeros else np.full(s.shape, 8.0)
