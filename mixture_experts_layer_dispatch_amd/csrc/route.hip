@@ -164,8 +164,10 @@ __device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, 
 // of 1 (2^-24):
 //   sigmoid: exp(-v) by exp2 is off by 1.5 |v| + 2 relative, the score by s (1 - s) times
 //     that, below 0.5 + 0.5, and by 3 s from 1 + exp and the reciprocal; 8 are taken;
-//   softmax: s (|v - m| + 32), with s |v - m| <= 0.37 and 32 for the exponential and the sum
-//     over the experts, 1 / z the largest s;
+//   softmax: s (|v - m| + EPL + 16), 1 / z the largest s: |v - m| and 2 from the exponential, 2 and
+//     at most 4.5 in z from those of all experts (the mean of |v - m| weighted by the scores, 4.43
+//     at the most for 1024), EPL - 1 and 6 from its sum in a lane and over the wave, 2 from the
+//     reciprocal and the product; s |v - m| <= 0.37 goes as 1;
 //   both: the rounding of c, |c| <= 1 + the largest |bias|; 2 (1 + that) are taken.
 //
 // 34 MB are read once, yet the instructions bound it, 950 vector and 370 scalar ones a
@@ -239,7 +241,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
         }
         key[j] = j < n ? order(c) : 0u;
     }
-    const float err = (softmax ? 0x1p-24f + 0x1p-19f * rz : 0x1p-21f) + 0x1p-23f * size;
+    const float err = (softmax ? 0x1p-24f * (1.f + (EPL + 16) * rz) : 0x1p-21f) + 0x1p-23f * size;
     bool kept = true, sure = true;
     if (groups) {
         uint32_t t1 = 0, t2 = 0;
