@@ -19,6 +19,14 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
+// Between a wave's LDS accesses of which one lane's read what another's wrote: they are done in
+// order, and the fences keep the compiler from carrying a lane's own values past this place.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ float no_nan(float v) { return v == v ? v : -INFINITY; }
 __device__ __forceinline__ double no_nan(double v) { return v == v ? v : -(double)INFINITY; }
 
@@ -445,9 +453,9 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteArgs a) {
             if (j < lane) first = false;
         }
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     if (first) out[e] += mine;
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int c = (i * 64 + lane) * V;
