@@ -271,11 +271,12 @@ __global__ __launch_bounds__(64 * W, NB == 4 ? 1 : W / 2) void k_w4_stream(W4Arg
 // sum of x over the group, which each wave computes for the eight rows that it copied,
 // one step ahead (bf16 codes minus 8 take twice the instructions).
 //
-// Bounds: 20480 rows at 512 experts, 4096 -> 1024, 350 us (memory alone 260, the rest alone
-// 240); 8192 x 4096 x 4096 286, 0.96 PFLOP/s, at the clock that power leaves (the MFMAs
-// alone 204).  Groups of 32 multiply and add 64 sums four times a step: 1111 x 4104 x 4032
-// fp16 with zeros 92 us, 24 of them for that, 28 for the codes; its 162 tiles leave
-// a third of the CUs idle.
+// Bounds: two waves a SIMD that convert and multiply in turn.  8192 x 4096 x 4096 takes 283 us,
+// 0.97 PFLOP/s: MFMAs are 49 % of the SIMDs' cycles, other vector instructions 50 %, at 2.06 GHz.
+// 20480 rows at 512 experts, 4096 -> 1024, 343 us, its 1.3 GB at 3.85 TB/s.  Groups of 32
+// multiply and add 64 sums four times a step: 1024 x 4096 x 4096 61 us, 31 % and 59 % (groups
+// of 128 49 us, 44 % and 46 %); 1111 x 4104 x 4032 fp16 with zeros 93 us: its 162 tiles leave a
+// third of the CUs idle.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <class D>
@@ -715,10 +716,12 @@ __global__ __launch_bounds__(256) void k_w4_quant(W4QuantArgs a, int64_t total) 
 // ================================================================ launchers
 // The tiles of a product and the parts of its reduction.  Few rows go as a stream, 16
 // at a time (512 experts, 4096 -> 1024: of 8 rows 291 us, in tiles of 64 rows 336; of 12
-// 335 both, of 16 395 and 339; dense 4096 x 4096, 32 rows 12 and 18, 64 rows 15 and 19).
-// A round of tiles over the
-// 256 CUs takes 2.3 us a step of 128 inputs, its beginning and end about 5; parts
-// cost a launch more (6 us) and their sums' way through memory.
+// 335 both, of 16 395 and 339; dense 4096 x 4096, 32 rows 12 and 18, 64 rows 15 and 19), by the
+// groups' mean: the host does not know each (6000 rows at those experts evenly 326 us, by a
+// Zipf law with 1136 at most 374).  A round of tiles over the 256 CUs takes 2.3 us a step of 128
+// inputs, its beginning and end about 5; parts cost a launch more (6 us) and their sums'
+// way through memory.  (The step is that of bf16 in groups of 128; groups of 32 with zeros
+// take 2.9, and one cost serves both.)
 W4Plan w4_plan(int M, int E, int K, int N) {
     W4Plan p{{nullptr, nullptr, E, M, (E ? M <= 12LL * E : M <= 64) ? 16 : 64, nullptr}, 1};
     if (p.t.tm == 16) return p;
@@ -744,8 +747,11 @@ static int w4_(const W4Args& a, hipStream_t st) {
     const int64_t tiles = max_tiles(f.t);
     if (f.t.tm == 16) {
         // Several columns of 16 share the loads of x, and few waves a block's beginning and
-        // end, where the blocks are enough for the chip (4 rows, 4096 -> 65536: by 64
-        // columns 28 us, by 32 36; 160 rows at 512 experts 70 and 72, by 16 92).
+        // end, where the blocks are enough for the chip.  By 16, 32 and 64 columns, us, K 4096:
+        // 4 rows, N 4096 6.1, 7.2, 10.5; 8192 8.6, 7.3, 10.6; 16384 14.2, 11.3, 13.2; 32768 24.3,
+        // 18.8, 19.1; 65536 46.6, 31.8, 27.7.  64 rows, N 4096 21.8, 15.0, 14.8; 8192 39.1, 25.9, 21.3;
+        // 16384 74, 47, 36.  160 rows at 512 experts, N 1024, 92, 65 to 72, 68 to 70; 40 rows 29, 23.5,
+        // 26.5.  (32 columns from 256 blocks on, and 64 from 512 for more than 16 rows, would win too.)
         const int64_t four = tiles * ((f.N + 63) / 64), two = tiles * ((f.N + 31) / 32);
         if (four >= 1024) return go(k_w4_stream<D, G, MODE, 4, 4, 2>, four, 256, a, st);
         if (two >= 512) return go(k_w4_stream<D, G, MODE, 2, 4, 4>, two, 256, a, st);

@@ -59,7 +59,7 @@ __device__ __forceinline__ void store_params(void* p, int at, const float* f) {
 // ================================================================ forward
 // A block has 4 rows of a wave each (W 1), or one row of W waves; a thread has NC
 // chunks of 16 bytes of its row.  HBM bounds it: 16384 x 4096 bf16, 268 MB without a residual
-// in 49 us, 5.5 TB/s; 4 rows take what a launch takes.
+// in 46 to 49 us, 5.5 to 5.8 TB/s; 4 rows take what a launch takes.
 template <class D, class P, int W, int NC>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_norm(NormArgs a) {
     constexpr int RB = W == 1 ? 4 : 1, PER = D::PER16;
@@ -145,9 +145,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_norm(NormArgs a) {
 // A block has RG rows at a time, W waves each (one, or the whole block), and
 // goes over the rows RG b, RG b + 1, ..., then RG (b + parts), ...  A thread keeps its
 // columns' sums for dgamma and dbeta over its rows; the block adds them up over its
-// rows in LDS and writes one part, which k_norm_params adds up block by block.  HBM bounds
-// it: 16384 x 4096 bf16 with d_total, 537 MB in 132 us, 4.1 TB/s (373 with a row per block and
-// parts added in sequence).
+// rows in LDS and writes one part, which k_norm_params adds up block by block.  Latency
+// bounds it, with a block of eight waves a CU and no row fetched ahead of the one before:
+// 16384 x 4096 bf16 with d_total, 537 MB in 132 us, 4.1 TB/s where the forward reaches 5.8
+// (373 with a row per block and parts added in sequence).
 template <class D, class P, int W, int NC, int RG>
 __global__ __launch_bounds__(64 * W * RG, 1) void k_norm_bwd(NormArgs a, int parts) {
     constexpr int PER = D::PER16, Q = PER / 4;
@@ -344,7 +345,16 @@ __global__ __launch_bounds__(1024) void k_norm_params(NormArgs a, int parts) {
 
 // ================================================================ launchers
 // The forward's rows: f(W, NC).  (Rows of at most 2^16 elements: 2^13 chunks of
-// 16 bits, 2^14 of fp32.)
+// 16 bits, 2^14 of fp32.)  bf16 rows of 134 MB in all, over and over, us, in (W, NC):
+//    512 elements  (1, 1) 47, (4, 1) 136
+//   1024           (4, 1) 76, (2, 4) 58, (1, 2) 43
+//   2048           (4, 1) 48, (1, 4) 44, (8, 1) 75
+//   4096           (4, 2) 43, (1, 8) 46, (8, 1) 49, (16, 1) 86
+//   8192           (4, 4) 43, (8, 2) 43, (16, 1) 57
+//   16384          (16, 4) 60, (16, 2) 47, (8, 4) 45
+//   32768          (16, 4) 58, (8, 8) 50
+// and 4 rows of 4096: (4, 2) 3.8, (1, 8) 6.2, (8, 1) 3.5, (16, 1) 3.8.  The first of each
+// is taken: one form for four sizes keeps the library small, and 1024, 16384 and 32768 lose by it.
 template <class D, class F>
 static int with_shape(int C, const F& f) {
     using std::integral_constant;
@@ -366,7 +376,12 @@ static int with_types(int dtype, int params, const F& f) {
 }
 
 // The backward's rows: up to 512 chunks in a wave, eight rows to a block, up to
-// 2048 a block each, f(W, NC, RG); longer ones go over memory twice, f(0, 0, 1)
+// 2048 a block each, f(W, NC, RG); longer ones go over memory twice, f(0, 0, 1).  As above,
+// 134 MB each of x, dy and dx, us:
+//   512 elements  (1, 1, 8) 125, (8, 1, 1) 378;  1024  (1, 2, 8) 104, (8, 1, 1) 228
+//   2048          (1, 4, 8) 92, (8, 1, 1) 137;   4096  (1, 8, 8) 97, (8, 1, 1) 100, (4, 2, 1) 106
+//   8192          (8, 2, 1) 97, (16, 1, 1) 111;  16384 (8, 4, 1) 113, (16, 2, 1) 114, twice 139
+//   32768         twice 148, (16, 4, 1), which spills, 325
 template <class F>
 static int with_bwd_shape(int C, const F& g) {
     using std::integral_constant;
@@ -379,6 +394,9 @@ static int with_bwd_shape(int C, const F& g) {
     return g(integral_constant<int, 0>{}, integral_constant<int, 0>{}, integral_constant<int, 1>{});
 }
 
+// Blocks of the backward, each with its part.  As above, with 128, 256, 512 and 1024 blocks:
+// 128 elements 294, 153, 109, 97 us; 512: 218, 125, 99, 100; 2048: 151, 93, 95, 100; 4096: 141,
+// 97, 105, 118; 8192 (a block a row) 176, 106, 98, 106; 16384: 156, 106, 112, 143.
 int norm_parts(int M, int H, int dtype) {
     return with_bwd_shape(H / (dtype == 2 ? 4 : 8), [&](auto w, auto n, auto rg) {
         constexpr int RG = decltype(rg)::value, most = RG > 1 ? 256 : decltype(w)::value ? 512 : 64;

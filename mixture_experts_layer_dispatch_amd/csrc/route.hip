@@ -179,8 +179,9 @@ __device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, 
 //   both: the rounding of c, |c| <= 1 + the largest |bias|; 2 (1 + that) are taken.
 //
 // 34 MB are read once, yet the instructions bound it, 950 vector and 370 scalar ones a
-// token (with sigmoid, bias and groups), of which ten rounds of the choice are 220 (16384 x 512: softmax 19 us, with sigmoid and bias 26, with 8 groups
-// 30; the bytes alone 7.4).  Rounds that look at all of a lane's keys each time and a choice
+// token (with sigmoid, bias and groups), of which ten rounds of the choice are 220 (16384 x 512:
+// softmax 21 us, with sigmoid and bias 28, with 8 groups 32, with all scores out 32 by
+// softmax; the bytes alone 5.5).  Rounds that look at all of a lane's keys each time and a choice
 // in 64 bits from the start for the tokens that are not sure took 50, all in 64 bits 75:
 // the second way's registers left four waves a SIMD instead of eight.  4 tokens take
 // what a launch takes (10 us a call).
