@@ -999,7 +999,8 @@ class LinearW4Config:
 
     @functools.cached_property
     def shapes(self) -> tuple:
-        """Shapes of the codes, and of the scales and zeros."""
+        """Shapes of the codes, and of the scales and zeros; raises what is wrong with the config."""
+        self.checked
         lead = (self.E,) if self.E else ()
         return (*lead, self.N, self.K // 2), (*lead, self.K // self.group, self.N)
 
