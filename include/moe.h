@@ -468,6 +468,7 @@ MOE_API moe_status moe_linear_backward(const moe_linear_config* cfg, const int32
  *   moe_norm_forward (residual added), moe_router_forward, moe_route_forward,
  *   moe_schedule_from_topk, moe_permute_forward, moe_linear_forward or
  *   moe_linear_w4_forward, moe_unpermute_forward
+ * A workspace that is another buffer of the call is refused, as outputs are.
  * ------------------------------------------------------------------------ */
 typedef enum moe_score {
     MOE_SCORE_SOFTMAX = 0,   /* s = softmax of a token's logits over all experts         */

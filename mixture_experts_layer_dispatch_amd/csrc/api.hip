@@ -714,13 +714,15 @@ moe_status moe_schedule_from_topk(const moe_config* cfg, const moe_sched* sched,
     Layout L;
     moe_status s = common_checks(cfg, g, L, workspace, workspace_bytes);
     if (s != MOE_OK) return s;
-    // the outputs have to be other buffers than topk_idx, and each other
+    // the outputs have to be other buffers than topk_idx, and each other, and none the workspace
     if (!sched_ok(sched)) return MOE_ERR_INVALID_ARG;
     const void* all[] = {sched->topk_idx, sched->topk_w, sched->counts, sched->offsets, sched->mini_counts,
                          sched->row_of_slot, sched->slot_of_row};
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < 7; ++i) {
+        if (all[i] == workspace) return MOE_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (all[i] == all[j]) return MOE_ERR_INVALID_ARG;
+    }
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;

@@ -299,7 +299,8 @@ moe_status moe_route_backward(const moe_config* cfg, const moe_route_config* rou
     if (s != MOE_OK) return s;
     if (!at(workspace, 256) || workspace_bytes < 256) return MOE_ERR_WORKSPACE;
     if (!at(dw, 4) || (d_scores && !at(d_scores, 4)) || !at(d_logits, 4) ||
-        among(d_logits, {logits, sched->topk_idx, dw, d_scores}))
+        among(d_logits, {logits, sched->topk_idx, dw, d_scores}) ||
+        among(workspace, {logits, sched->topk_idx, dw, d_scores, d_logits}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     a.dw = dw;
@@ -347,7 +348,8 @@ moe_status moe_norm_backward(const moe_norm_config* c, const void* x, const void
         !at_or_null(dbeta) || (rms && dbeta) || (d_total && !dx))
         return MOE_ERR_INVALID_ARG;
     if (among(dx, {x, gamma, mean, rstd, dgamma, dbeta}) || among(dgamma, {x, gamma, mean, rstd, dy, d_total, dbeta}) ||
-        among(dbeta, {x, gamma, mean, rstd, dy, d_total}))
+        among(dbeta, {x, gamma, mean, rstd, dy, d_total}) ||
+        among(workspace, {x, gamma, mean, rstd, dy, d_total, dx, dgamma, dbeta}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     const NormArgs a{c->M, c->H, c->dtype, c->params, rms, c->eps, x, gamma, nullptr, d_total, dx, nullptr,
@@ -373,7 +375,8 @@ moe_status moe_linear_w4_forward(const moe_linear_w4_config* c, const int32_t* o
     if (!at(workspace, 256) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
     if ((c->E > 0 ? !at(offsets, 4) : offsets != nullptr) || !at(x, 16) || !at(codes, 16) || !at(scales, 16) ||
         !at_or_null(zeros) || !at_or_null(bias) || !at_or_null(residual) || !at(y, 16) ||
-        among(y, {offsets, x, codes, scales, zeros, bias}))
+        among(y, {offsets, x, codes, scales, zeros, bias}) ||
+        among(workspace, {offsets, x, codes, scales, zeros, bias, residual, y}))
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED_DEVICE;
     hipStream_t st = (hipStream_t)stream;
