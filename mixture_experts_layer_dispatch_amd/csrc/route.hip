@@ -114,9 +114,9 @@ __device__ __forceinline__ bool kept64(const RouteArgs& a, const Lanes& L, const
     return better < a.topk_group;
 }
 
-// The choice among the places of `key`, each off by less than err: k rounds of the largest,
-// and where others are as close to it as both errors, the largest of those in 64 bits, the
-// lower index first.  kept: 1 or 0, or -1 where the groups are not sure either.
+// The choice among the places of `key`, each c off by less than err + 2^-23 |c|: k rounds of
+// the largest, and where others are as close to it as both errors, the largest of those in
+// 64 bits, the lower index first.  kept: 1 or 0, or -1 where the groups are not sure either.
 template <int EPL>
 __device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, const float* row, const uint32_t (&key)[EPL],
                                             float err, int e0, int n, int kept, int lane) {
@@ -137,7 +137,8 @@ __device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, 
         for (int j = 0; j < EPL; ++j) best = max(best, open >> j & 1u ? key[j] : 0u);
         best = wave_most(best);
         const float c = value_of(best);
-        const uint32_t thr = fabsf(c) < INFINITY ? order(c - 3.f * err) : best;       // (c - 3 err is rounded itself)
+        // (three errors: those of the others are a little larger, and the difference is rounded itself)
+        const uint32_t thr = fabsf(c) < INFINITY ? order(c - 3.f * (err + 0x1p-23f * fabsf(c))) : best;
         uint32_t close = 0;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) close |= (key[j] >= thr ? 1u : 0u) << j;
@@ -165,18 +166,20 @@ __device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, 
 }
 
 // The choice is the one in 64 bits.  Without a bias (and sums of two in the groups) it is
-// that of the logits, exactly.  Else the scores are computed in 32 bits, each off by
-// less than `err`, and where two that the choice tells apart, neighbours among the k + 1
+// that of the logits, exactly.  Else c is computed in 32 bits, off by less than `err` for
+// the score and 2^-23 |c| for the sum, and where two that the choice tells apart, neighbours among the k + 1
 // best or a kept group's and another's, are closer than both errors, the token is done
 // again in 64 bits (16384 x 512, sigmoid and bias: one token in a thousand).  In half steps
 // of 1 (2^-24):
 //   sigmoid: exp(-v) by exp2 is off by 1.5 |v| + 2 relative, the score by s (1 - s) times
 //     that, below 0.5 + 0.5, and by 3 s from 1 + exp and the reciprocal; 8 are taken;
 //   softmax: s (|v - m| + EPL + 16), 1 / z the largest s: |v - m| and 2 from the exponential, 2 and
-//     at most 4.5 in z from those of all experts (the mean of |v - m| weighted by the scores, 4.43
+//     at most 4.5 in z from those of all experts (the mean of |v - m| weighted by the scores, 4.44
 //     at the most for 1024), EPL - 1 and 6 from its sum in a lane and over the wave, 2 from the
 //     reciprocal and the product; s |v - m| <= 0.37 goes as 1;
-//   both: the rounding of c, |c| <= 1 + the largest |bias|; 2 (1 + that) are taken.
+//   both: the rounding of c, |c|; 2 |c| are taken.  (It is c's own size that counts, not the
+//     largest of the biases: one of -10^9 or fp32's lowest, for an expert that is not to be
+//     chosen, would leave no token sure, 235 us instead of 28 for 16384 x 512.)
 //
 // 34 MB are read once, yet the instructions bound it, 950 vector and 370 scalar ones a
 // token (with sigmoid, bias and groups), of which ten rounds of the choice are 220 (16384 x 512:
@@ -213,13 +216,9 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
     };
     float v[EPL], bias[EPL];
     load(row, -INFINITY, v);
-    float m = -INFINITY, size = 1.f;                           // size: 1 + the largest finite |bias|
+    float m = -INFINITY;
     if (a.bias) {
         load(a.bias, 0.f, bias);
-        float most = 0.f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) most = fmaxf(most, fabsf(bias[j]) < INFINITY ? fabsf(bias[j]) : 0.f);
-        size = 1.f + wave_most(most);
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) bias[j] = 0.f;
@@ -250,7 +249,7 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
         }
         key[j] = j < n ? order(c) : 0u;
     }
-    const float err = (softmax ? 0x1p-24f * (1.f + (EPL + 16) * rz) : 0x1p-21f) + 0x1p-23f * size;
+    const float err = softmax ? 0x1p-24f * (1.f + (EPL + 16) * rz) : 0x1p-21f;
     bool kept = true, sure = true;
     if (groups) {
         uint32_t t1 = 0, t2 = 0;
@@ -272,9 +271,15 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
             better += o > score || (o == score && g < lane / L.per);
         }
         kept = mine && better < a.topk_group;
-        if (!by_logit && a.topk_group < a.n_group) {       // the worst kept and the best other
-            const float lo = value_of(~wave_most(kept ? ~score : 0u)), hi = value_of(wave_most(mine && !kept ? score : 0u));
-            sure = lo - hi > (two ? 4.f * err + 0x1p-22f * size : 2.f * err);      // (equal infinities: not sure)
+        if (!by_logit && a.topk_group < a.n_group) {
+            // the worst kept at its least and the best other at its most; of sums of two each
+            // has its rounding, and the sum, which is no larger than both
+            float size = fabsf(value_of(t1)), c = value_of(score);
+            if (two) size = 2.f * (size + fabsf(value_of(t2)));
+            size = size < INFINITY ? 0x1p-23f * size : 0.f;
+            const float lo = value_of(~wave_most(kept ? ~order(c - size) : 0u));
+            const float hi = value_of(wave_most(mine && !kept ? order(c + size) : 0u));
+            sure = lo - hi > (two ? 4.f : 2.f) * err;      // (equal infinities: not sure)
         }
     }
     // Rounds of the wave's largest.  A lane has its two largest at hand and looks at its
@@ -297,12 +302,13 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a, Lanes L, bool vec) {
             }
         };
         if (kept) largest_two(~0u, 0);
-        float above = INFINITY, gap = INFINITY;            // (equal infinities need no 64 bits)
+        float above = INFINITY, gap = INFINITY;            // (infinite ones need no 64 bits: NaN, left out)
         for (int r = 0;; ++r) {
             const uint32_t most = wave_most(b1);
             if (!by_logit && most) {
-                gap = fminf(gap, above - value_of(most));
-                above = value_of(most);
+                const float c = value_of(most);
+                gap = fminf(gap, fmaf(-0x1p-22f, fmaxf(fabsf(above), fabsf(c)), above - c));
+                above = c;
             }
             if (r == a.k) break;
             const int owner = __builtin_ctzll(__ballot(b1 == most));
