@@ -597,10 +597,10 @@ MOE_API moe_status moe_linear_w4_workspace_size(const moe_linear_w4_config* cfg,
  * group, and the group's sum times its scale in fp32.  The whole numbers are
  * code - zero; for bf16 without zeros they may be the codes, with 8 times the
  * group's sum of x taken off: the fp32 rounding is then that of sums of at most
- * 16 |x| scale, also where code is 8 throughout.  Rows whose sums are not finite that
- * way are those of code - 8: an infinite x gives what IEEE's rules make of the
- * formula (NaN where code is 8, else an infinity), at the cost of a slow pass for its
- * row.  A scale of 0 switches a group off only where x is finite. */
+ * 16 |x| scale, also where code is 8 throughout.  Sums that are not finite that way
+ * are computed again from code - 8, slowly: an infinite x gives what IEEE's rules make
+ * of the formula (NaN where code is 8, else an infinity).  A scale of 0 switches a
+ * group off only where x is finite. */
 MOE_API moe_status moe_linear_w4_forward(const moe_linear_w4_config* cfg, const int32_t* offsets, const void* x,
                                          const void* codes, const void* scales, const void* zeros,
                                          const void* bias, const void* residual, void* y, void* workspace,

@@ -111,9 +111,34 @@ enum { W4_MID, W4_EIGHT, W4_ZEROS };
 // By the sums of x, an infinite x makes all outputs of its row NaN, and x beyond 2^128 / (15 G)
 // can take sums of the codes past fp32's range where those of code - 8 are inside it.  No sum that
 // has left it comes back, so what comes out finite is right, and the waves that have other
-// sums replace them by exact ones, straight from memory.  (x is seldom so: 2048 x 4096 x 4096
-// takes 76 us, and 518 with an infinite x in one row or all; 4 rows 6 and 29.)
+// sums replace them by exact ones, straight from memory; but for rows that have a NaN,
+// which is what they come out as, so that a padded batch need not be cleared.  2048 x 4096 x
+// 4096 takes 76 us; a call with its launch 82, with an infinite x in one row 328, in all 631,
+// with one row of random bits 84, with only such rows 110.
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
+// Which of `rows` (bit j: row row0 + j, 16 of them) have a NaN in x (bf16)
+__device__ __forceinline__ uint32_t nan_rows(const LinFwdArgs& f, int row0, int hi, uint32_t rows) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const int j = lane_id() & 15, q = lane_id() >> 4;
+    const uint16_t* x = f.x + (int64_t)min(row0 + j, hi - 1) * f.K + 8 * q;
+    uint32_t found = 0;
+    for (int k = 0; k < f.K && (rows & ~found); k += 256) {
+        u16x2 most = {0, 0};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint4 v = *(const uint4*)(x + min(k + 32 * u, f.K - 32));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+        }
+        uint64_t m = __ballot(most[0] > 0x7f80 || most[1] > 0x7f80);
+        m |= m >> 32;
+        found |= (uint32_t)(m | m >> 16) & 0xffffu;
+    }
+    return rows & found;
+}
 
 // ================================================================ few rows
 // Exact sums of 16 rows from row0 by 16 columns from col0: lane j + 16 q has row j's
@@ -239,8 +264,11 @@ __global__ __launch_bounds__(64 * W, NB == 4 ? 1 : W / 2) void k_w4_stream(W4Arg
     for (int p = 1; p < W; ++p) v += *(const f32x4*)&sums[p][r][c];
     if constexpr (MODE == W4_MID) {
         const bool bad = !(finite(v[0]) && finite(v[1]) && finite(v[2]) && finite(v[3]));
-        if (__builtin_expect(__ballot(bad) != 0, 0)) {
-            for (int n = 0; n < NB; ++n) {
+        if (uint64_t m = __ballot(bad && lo + r < hi); __builtin_expect(m != 0, 0)) {
+            uint32_t rows = 0;                 // (a wave has whole rows)
+            for (; m; m &= m - 1) rows |= 1u << ((64 * wv + __builtin_ctzll(m)) / (4 * NB));
+            rows &= ~nan_rows(f, lo, hi, rows);
+            for (int n = 0; n < NB && rows; ++n) {
                 const f32x4 y = w4_exact16<D, G>(a, e, lo, hi, nt * TN + 16 * n);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -593,14 +621,27 @@ __global__ __launch_bounds__(64 * kW4Waves, 2) void k_w4_tile(W4Args a) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) t[i & 3] = fmaf(l.acc[i >> 5][i >> 4 & 1][i & 15], 0.f, t[i & 3]);
         if (__builtin_expect(__ballot(t[0] + t[1] + t[2] + t[3] != 0.f) != 0, 0)) {
+            uint64_t rows = 0;
 #pragma unroll
             for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const uint64_t b = __ballot(!finite(l.acc[m][0][r]) || !finite(l.acc[m][1][r]));
+                    rows |= (uint64_t)(((uint32_t)b ? 1 : 0) | (b >> 32 ? 16 : 0)) << (32 * m + 8 * (r >> 2) + (r & 3));
+                }
+            if (hi - lo < TM) rows &= (1ull << (hi - lo)) - 1;
+            for (int i = 0; i < TM; i += 16)
+                if (rows >> i & 0xffff) rows &= ~((uint64_t)nan_rows(f, lo + i, hi, (uint32_t)(rows >> i) & 0xffffu) << i);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (!(uint32_t)(rows >> 32 * m)) continue;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const f32x16 y = w4_exact32<D, G>(a, e, lo + 32 * m, hi, col + n, first * Loop::NG, l.last * Loop::NG);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) l.acc[m][n][r] = finite(l.acc[m][n][r]) ? l.acc[m][n][r] : y[r];
                 }
+            }
         }
     }
     if (col >= f.N) return;

@@ -354,7 +354,7 @@ __global__ __launch_bounds__(1024) void k_norm_params(NormArgs a, int parts) {
 //   16384          (16, 4) 60, (16, 2) 47, (8, 4) 45
 //   32768          (16, 4) 58, (8, 8) 50
 // and 4 rows of 4096: (4, 2) 3.8, (1, 8) 6.2, (8, 1) 3.5, (16, 1) 3.8.  The first of each
-// is taken: one form for four sizes keeps the library small, and 1024, 16384 and 32768 lose by it.
+// is taken; at 1024, 16384 and 32768 another is faster.
 template <class D, class F>
 static int with_shape(int C, const F& f) {
     using std::integral_constant;
@@ -381,7 +381,7 @@ static int with_types(int dtype, int params, const F& f) {
 //   512 elements  (1, 1, 8) 125, (8, 1, 1) 378;  1024  (1, 2, 8) 104, (8, 1, 1) 228
 //   2048          (1, 4, 8) 92, (8, 1, 1) 137;   4096  (1, 8, 8) 97, (8, 1, 1) 100, (4, 2, 1) 106
 //   8192          (8, 2, 1) 97, (16, 1, 1) 111;  16384 (8, 4, 1) 113, (16, 2, 1) 114, twice 139
-//   32768         twice 148, (16, 4, 1), which spills, 325
+//   32768         twice 148, (16, 4, 1) 325
 template <class F>
 static int with_bwd_shape(int C, const F& g) {
     using std::integral_constant;

@@ -131,3 +131,23 @@ def test_subnormal_x(M, N, K, counts, group):
     y = call(wc, x, codes, scales, None, off)
     z, mag, most = definition(wc, x, codes, scales, off, rows)
     compare(y[:rows], z, mag, most, wc)
+
+
+@pytest.mark.parametrize("M,N,K,counts,group", SIZES)
+def test_rows_of_a_padded_batch(M, N, K, counts, group):
+    """Rows that were never written: whatever bits. A NaN anywhere makes a row NaN, beside rows with infinities,
+    and the others keep their bits."""
+    g, wc, x, codes, scales, off, rows = case(M, N, K, counts, group, M * 3 + K)
+    good = call(wc, x, codes, scales, None, off)
+    x2 = x.clone()
+    x2[rows // 2:].view(torch.int16).random_(-32768, 32767, generator=g)
+    x2[rows // 2:, ::9] = float("nan")
+    x2[0, K - 1], x2[1, 0] = float("nan"), INF
+    x2[1, 1:].clamp_(-1, 1)
+    bad = call(wc, x2, codes, scales, None, off)
+    assert bad[0].isnan().all() and bad[rows // 2:rows].isnan().all()
+    z, mag, most = definition(wc, x2[:2], codes if not wc.E else codes[:1], scales if not wc.E else scales[:1],
+                              None if not wc.E else torch.tensor([0, 2]), 2)
+    compare(bad[:2], z, mag, np.where(np.isfinite(most), most, 0), wc)
+    assert torch.equal(good[2:rows // 2], bad[2:rows // 2])
+    assert (bad[rows:] == 7).all()
