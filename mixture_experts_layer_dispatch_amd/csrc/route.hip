@@ -181,7 +181,7 @@ __device__ __forceinline__ int choose_close(const RouteArgs& a, const Lanes& L, 
 //     largest of the biases: one of -10^9 or fp32's lowest, for an expert that is not to be
 //     chosen, would leave no token sure, 235 us instead of 28 for 16384 x 512.)
 //
-// 34 MB are read once, yet the instructions bound it, 950 vector and 370 scalar ones a
+// 34 MB are read once, yet the instructions bound it, 950 vector and 400 scalar ones a
 // token (with sigmoid, bias and groups), of which ten rounds of the choice are 220 (16384 x 512:
 // softmax 21 us, with sigmoid and bias 28, with 8 groups 32, with all scores out 32 by
 // softmax; the bytes alone 5.5).  Rounds that look at all of a lane's keys each time and a choice
